@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -23,6 +24,13 @@ GDN_ERR_SCRATCH_LIMIT = 6
 GDN_F32 = 0
 GDN_BF16 = 1
 
+GDN_ROPE_HALF = 0
+GDN_ROPE_INTERLEAVED = 1
+
+# struct formats of gdn_rows and gdn_rotation
+ROWS = struct.Struct("Pqq")
+ROTATION = struct.Struct("PPqiiiiiiif")
+
 # name -> (restype, argtypes), mirroring include/gdn.h
 _vp, _fp, _i, _ll = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
 _SCAN_ARGS = [_vp, _vp, _vp, _fp, _fp, _fp, _fp, _vp] + [_i] * 5 + [_i, _i, _vp]
@@ -37,6 +45,10 @@ SIGNATURES = {
     "gdn_chunk_bidir_logits": (ctypes.c_int, _SCAN_ARGS),
     "gdn_sink_window_attention": (ctypes.c_int, [_vp] * 6 + [_i] * 8 + [_vp]),
     "gdn_sink_window_slot": (ctypes.c_int, [_i, _i, _i]),
+    "gdn_rope": (ctypes.c_int, [_vp] * 3 + [_i] + [_vp] * 2 + [_i] * 6 + [_vp]),
+    "gdn_qk_norm_rope": (ctypes.c_int, [_vp] * 7 + [_i] * 5 + [ctypes.c_float, _i, _vp]),
+    "gdn_qk_norm_rope_backward": (ctypes.c_int,
+                                  [_vp] * 11 + [_i] * 5 + [ctypes.c_float, _i, _vp]),
     "gdn_state_reset": (ctypes.c_int, [_fp, _i, _i, _i, _i, _vp]),
     "gdn_device_error": (ctypes.c_int, [_vp]),
     "gdn_workspace_release": (ctypes.c_int, []),

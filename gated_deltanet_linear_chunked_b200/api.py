@@ -11,6 +11,8 @@ fp32; state [B,H,Dk,Dv] fp32.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import _lib
@@ -184,6 +186,243 @@ def sink_window_attention(q, k, v, k_cache, v_cache, chunk_index, n_sink, window
         int(n_sink), int(window), int(chunk_index), _lib.GDN_BF16, _stream(stream))
     _lib.check(st, "gdn_sink_window_attention")
     return out
+
+
+_LAYOUTS = {"half": _lib.GDN_ROPE_HALF, "interleaved": _lib.GDN_ROPE_INTERLEAVED}
+_POSITION_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+def _raw_stream(stream, device):
+    """The cudaStream_t to launch on: `stream`'s, or the device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _fresh(stream, make, *args, **kw):
+    """A new tensor from `make`, from the memory of the stream it is used on."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
+def _used_on(stream, *tensors):
+    """Keeps tensors of another stream alive until `stream` is done with them."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _view(t, name, dtype, shape):
+    """A [B, T, H, D] tensor whose heads and features are contiguous, as gdn_rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    sb, st, sh, sd = t.stride()
+    B, T, H, D = shape
+    if B * T * H and (sd != 1 or (H > 1 and sh != D)):
+        raise ValueError(f"{name} must have contiguous heads and features")
+    return _lib.ROWS.pack(t.data_ptr(), sb if B > 1 else 0, st if T > 1 else 0)
+
+
+def rope_frequencies(dim, base=10000.0, sections=None, scaling="none", factor=1.0,
+                     original_length=None, device=None):
+    """The rotation's frequencies (fp64, [dim / 2], radians per position) and its
+    amplitude, for ``rope`` and ``qk_norm_rope``.
+
+    ``sections`` gives the pairs of each position axis (their sum is dim / 2; one
+    axis by default); the n pairs of an axis have base^(-i / n), i < n.
+    ``scaling`` stretches them for contexts ``factor`` times longer than trained:
+
+    * ``"linear"``: every frequency divided by the factor (position interpolation);
+    * ``"ntk"``: the base times factor^(n / (n - 1)), so that the slowest pair is
+      stretched by the factor and the fastest not at all;
+    * ``"yarn"``: pairs that turn less than once over ``original_length`` are
+      divided by the factor, those that turn more than 32 times are kept, a linear
+      ramp between; amplitude 0.1 ln(factor) + 1 (Peng et al., "YaRN", 2023).
+    """
+    if dim % 2 or dim < 0:
+        raise ValueError("dim must be even")
+    if scaling not in ("none", "linear", "ntk", "yarn"):
+        raise ValueError("scaling must be 'none', 'linear', 'ntk' or 'yarn'")
+    if not factor >= 1.0:
+        raise ValueError("factor must be 1 or more")
+    if scaling == "yarn" and not original_length:
+        raise ValueError("scaling 'yarn' needs original_length")
+    sections = (dim // 2,) if sections is None else tuple(int(n) for n in sections)
+    if sum(sections) != dim // 2 or min(sections, default=0) < 0:
+        raise ValueError("sections must add up to dim / 2")
+    parts = []
+    for n in sections:
+        i = torch.arange(n, dtype=torch.float64)
+        b = base * factor ** (n / (n - 1)) if scaling == "ntk" and n > 1 else base
+        f = b ** (-i / max(n, 1))
+        if scaling == "linear":
+            f = f / factor
+        elif scaling == "yarn":
+            turns = original_length * f / (2.0 * math.pi)
+            keep = ((turns - 1.0) / 31.0).clamp(0.0, 1.0)
+            f = f * keep + f / factor * (1.0 - keep)
+        parts.append(f)
+    amplitude = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" else 1.0
+    return torch.cat(parts).to(device or "cuda"), amplitude
+
+
+def _rotation(positions, inv_freq, sections, layout, amplitude, B, T):
+    """gdn_rotation of a call, or None without positions."""
+    if positions is None and inv_freq is None:
+        return None
+    if positions is None or inv_freq is None:
+        raise ValueError("positions and inv_freq go together")
+    if layout not in _LAYOUTS:
+        raise ValueError("layout must be 'half' or 'interleaved'")
+    pairs = inv_freq.numel()
+    sections = (pairs,) if sections is None else sections
+    axes = len(sections)
+    if not 1 <= axes <= 3:
+        raise ValueError("sections must name 1 to 3 position axes")
+    for t, name in ((positions, "positions"), (inv_freq, "inv_freq")):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise TypeError("inv_freq must be a contiguous float64 vector")
+    if positions.dtype not in _POSITION_BYTES:
+        raise TypeError("positions must be int32 or int64")
+    shape, stride = positions.shape, positions.stride()
+    if axes == 1 and (shape == (T,) or shape == (B, T)):  # the one axis left out
+        shape, stride = (*shape, 1), (*stride, 1)
+    if shape == (T, axes):
+        bs, st = 0, stride
+    elif shape == (B, T, axes):
+        bs, st = stride[0] if B > 1 else 0, stride[1:]
+    else:
+        raise ValueError(f"positions must be [T], [B, T] (one axis), [T, {axes}] or "
+                         f"[B, T, {axes}], got {tuple(positions.shape)}")
+    if B * T and ((axes > 1 and st[1] != 1) or (T > 1 and st[0] != axes)):
+        raise ValueError("positions must be contiguous over tokens and axes")
+    s = (*sections, 0, 0)
+    return _lib.ROTATION.pack(positions.data_ptr(), inv_freq.data_ptr(), bs,
+                              _POSITION_BYTES[positions.dtype], axes, s[0], s[1], s[2], 2 * pairs,
+                              _LAYOUTS[layout], amplitude)
+
+
+def _heads(q, k):
+    """B, T, Hq, Hk, D, dtype code and the shapes of q and k (k may be None)."""
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("q, k must be [B,T,H,D]")
+    B, T, Hq, D = q.shape
+    Hk = 0 if k is None else k.shape[2]
+    code = _DTYPES.get(q.dtype)
+    if code is None:
+        raise TypeError(f"q, k must be bfloat16 or float32, got {q.dtype}")
+    return B, T, Hq, Hk, D, code, (B, T, Hq, D), (B, T, Hk, D)
+
+
+def _weight(w, name, D):
+    if w is not None:
+        _check_tensor(w, name, torch.float32, (D,))
+    return _ptr(w)
+
+
+def _out_view(t, name, dtype, shape, stream, device):
+    """`t`, or a new tensor where it is None, and its gdn_rows."""
+    if t is None:
+        t = _fresh(stream, torch.empty, shape, dtype=dtype, device=device)
+    return t, _view(t, name, dtype, shape)
+
+
+def _turn(q, k, positions, inv_freq, sections, layout, amplitude, inverse, q_out, k_out, stream):
+    B, T, Hq, Hk, D, code, qs, ks = _heads(q, k)
+    dt, dev = q.dtype, q.device
+    vq, vk = _view(q, "q", dt, qs), None if k is None else _view(k, "k", dt, ks)
+    rot = _rotation(positions, inv_freq, sections, layout, amplitude, B, T)
+    if rot is None:
+        raise ValueError("rope needs positions and inv_freq")
+    q_out, oq = _out_view(q_out, "q_out", dt, qs, stream, dev)
+    ok = None
+    if k is not None:
+        k_out, ok = _out_view(k_out, "k_out", dt, ks, stream, dev)
+    st = _lib.load().gdn_rope(vq, vk, rot, inverse, oq, ok, B, T, Hq, Hk, D, code,
+                              _raw_stream(stream, dev))
+    _lib.check(st, "gdn_rope")
+    _used_on(stream, q, k, positions, inv_freq, q_out, k_out)
+    return q_out, k_out
+
+
+def rope(q, k, positions, inv_freq, *, sections=None, layout="half", amplitude=1.0, q_out=None,
+         k_out=None, stream=None):
+    """Rotary positions of q [B,T,Hq,D] and k [B,T,Hk,D] (or None), bf16 or fp32:
+    the first 2 * len(inv_freq) features of every head turn by position *
+    inv_freq, pair i being features i and i + half ("half") or 2i and 2i + 1
+    ("interleaved").  ``positions`` are int32 or int64 [T], [B,T] or, with several
+    axes, [T,axes] or [B,T,axes]; ``sections`` says how many pairs turn by each
+    axis.  q and k may be views of one projection; ``q_out`` and ``k_out`` may be
+    q and k themselves (in place) or, say, a slot of a cache.  Returns
+    ``(q_out, k_out)``."""
+    return _turn(q, k, positions, inv_freq, sections, layout, amplitude, 0, q_out, k_out, stream)
+
+
+def rope_backward(dq_out, dk_out, positions, inv_freq, *, sections=None, layout="half",
+                  amplitude=1.0, dq=None, dk=None, stream=None):
+    """Gradients of ``rope``: a dict with dq and dk (None without keys), the
+    inverse turn of the gradients of its outputs."""
+    dq, dk = _turn(dq_out, dk_out, positions, inv_freq, sections, layout, amplitude, 1, dq, dk, stream)
+    return {"dq": dq, "dk": dk}
+
+
+def qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, *, eps=1e-6,
+                 sections=None, layout="half", amplitude=1.0, q_out=None, k_out=None, stream=None):
+    """RMS norm over the features of every head of q and k (k may be None), times
+    the fp32 weights [D] (None: ones), and the rotary positions of ``rope``
+    (none without ``positions``), in one pass.  Returns ``(q_out, k_out)``."""
+    B, T, Hq, Hk, D, code, qs, ks = _heads(q, k)
+    dt, dev = q.dtype, q.device
+    vq, vk = _view(q, "q", dt, qs), None if k is None else _view(k, "k", dt, ks)
+    wq, wk = _weight(q_weight, "q_weight", D), _weight(k_weight, "k_weight", D)
+    rot = _rotation(positions, inv_freq, sections, layout, amplitude, B, T)
+    q_out, oq = _out_view(q_out, "q_out", dt, qs, stream, dev)
+    ok = None
+    if k is not None:
+        k_out, ok = _out_view(k_out, "k_out", dt, ks, stream, dev)
+    st = _lib.load().gdn_qk_norm_rope(vq, vk, wq, wk, rot, oq, ok, B, T, Hq, Hk, D, eps, code,
+                                      _raw_stream(stream, dev))
+    _lib.check(st, "gdn_qk_norm_rope")
+    _used_on(stream, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out)
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(q, k, q_weight, k_weight, dq_out, dk_out, positions=None, inv_freq=None,
+                          *, eps=1e-6, sections=None, layout="half", amplitude=1.0, dq=None, dk=None,
+                          stream=None):
+    """Gradients of ``qk_norm_rope`` given its inputs and the gradients of its
+    outputs: a dict with dq, dk (q's dtype) and dq_weight, dk_weight (fp32 [D]);
+    those of the keys are None without keys."""
+    B, T, Hq, Hk, D, code, qs, ks = _heads(q, k)
+    dt, dev = q.dtype, q.device
+    vq, vk = _view(q, "q", dt, qs), None if k is None else _view(k, "k", dt, ks)
+    wq, wk = _weight(q_weight, "q_weight", D), _weight(k_weight, "k_weight", D)
+    rot = _rotation(positions, inv_freq, sections, layout, amplitude, B, T)
+    gq = _view(dq_out, "dq_out", dt, qs)
+    gk = None if k is None else _view(dk_out, "dk_out", dt, ks)
+    dq, oq = _out_view(dq, "dq", dt, qs, stream, dev)
+    dqw = _fresh(stream, torch.empty, (D,), dtype=torch.float32, device=dev)
+    ok = dkw = None
+    if k is not None:
+        dk, ok = _out_view(dk, "dk", dt, ks, stream, dev)
+        dkw = _fresh(stream, torch.empty, (D,), dtype=torch.float32, device=dev)
+    st = _lib.load().gdn_qk_norm_rope_backward(vq, vk, wq, wk, rot, gq, gk, oq, ok, dqw.data_ptr(),
+                                               _ptr(dkw), B, T, Hq, Hk, D, eps, code,
+                                               _raw_stream(stream, dev))
+    _lib.check(st, "gdn_qk_norm_rope_backward")
+    _used_on(stream, q, k, q_weight, k_weight, positions, inv_freq, dq_out, dk_out, dq, dk, dqw, dkw)
+    return {"dq": dq, "dk": dk, "dq_weight": dqw, "dk_weight": dkw}
 
 
 def state_reset(state, stream=None):

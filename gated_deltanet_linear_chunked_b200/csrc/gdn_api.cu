@@ -72,40 +72,6 @@ bool debug_sync() {
   return s && s[0] && std::strcmp(s, "0") != 0;
 }
 
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range_of(const void* p, size_t bytes) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return {lo, lo + bytes};
-}
-
-bool overlaps(Range a, Range b) {
-  if (a.lo == a.hi || b.lo == b.hi) return false;
-  return a.lo < b.hi && b.lo < a.hi;
-}
-
-bool aligned16(const void* p) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
-}
-
-bool supported_dim(int d) { return d >= 16 && d <= 128 && d % 16 == 0; }
-
-// A pointer the current device can use as ordinary device memory.
-gdn_status check_device_pointer(const void* p, int dev) {
-  cudaPointerAttributes attr;
-  const cudaError_t e = cudaPointerGetAttributes(&attr, p);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return GDN_ERR_CUDA;
-  }
-  if (attr.type == cudaMemoryTypeManaged) return GDN_OK;
-  if (attr.type != cudaMemoryTypeDevice) return GDN_ERR_INVALID_ARG;
-  if (attr.device != dev) return GDN_ERR_INVALID_ARG;
-  return GDN_OK;
-}
-
 // Reads and clears one error word; GDN_ERR_TIMEOUT if it was set.
 gdn_status take_error(unsigned int* err) {
   unsigned int word = 0;
@@ -249,6 +215,19 @@ gdn_status scan(const void* q, const void* k, const void* v, const void* g,
 
 }  // namespace
 
+gdn_status check_device_pointer(const void* p, int dev) {
+  cudaPointerAttributes attr;
+  const cudaError_t e = cudaPointerGetAttributes(&attr, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return GDN_ERR_CUDA;
+  }
+  if (attr.type == cudaMemoryTypeManaged) return GDN_OK;
+  if (attr.type != cudaMemoryTypeDevice) return GDN_ERR_INVALID_ARG;
+  if (attr.device != dev) return GDN_ERR_INVALID_ARG;
+  return GDN_OK;
+}
+
 gdn_status check_scan_host(const void* q, const void* k, const void* v, const void* g,
                            const void* beta, const float* state_in, float* state_out,
                            void* out, int B, int T, int H, int Dk, int Dv, gdn_dtype dtype,
@@ -350,8 +329,25 @@ gdn_status finish(cudaStream_t s, cudaError_t launch_err, unsigned int* err) {
 
 void count_launches(unsigned n) { g_launches.fetch_add(n); }
 
-gdn_status stream_scratch(int dev, cudaStream_t s, size_t bytes, unsigned int** err, void** ws) {
-  return stream_context(dev, s, bytes, err, ws);
+gdn_status op_scratch(int dev, cudaStream_t s, size_t bytes, unsigned int** err, OpScratch* sc) {
+  sc->stream = s;
+  sc->captured = bytes > 0 && capturing(s);
+  gdn_status st = stream_context(dev, s, sc->captured ? 0 : bytes, err, &sc->p);
+  if (st != GDN_OK) return st;
+  if (!*err && error_word(err) != cudaSuccess) {
+    cudaGetLastError();
+    return GDN_ERR_CUDA;
+  }
+  if (!sc->captured) return GDN_OK;
+  if (cudaMallocAsync(&sc->p, bytes, s) != cudaSuccess) {
+    cudaGetLastError();
+    return GDN_ERR_CUDA;
+  }
+  return GDN_OK;
+}
+
+cudaError_t op_scratch_done(const OpScratch& sc) {
+  return sc.captured ? cudaFreeAsync(sc.p, sc.stream) : cudaSuccess;
 }
 
 namespace {
@@ -780,6 +776,9 @@ const char* gdn_kernel_name(int id) {
     case gdn::kKernBwdChunk: return "gdn_bwd_pre_kernel";
     case gdn::kKernBwdChain: return "gdn_bwd_chain_kernel";
     case gdn::kKernBwdGrad: return "gdn_bwd_grad_kernel";
+    case gdn::kKernNormRope: return "gdn_norm_rope_kernel";
+    case gdn::kKernNormRopeBwd: return "gdn_norm_rope_bwd_kernel";
+    case gdn::kKernNormRopeReduce: return "gdn_norm_rope_reduce_kernel";
   }
   return "unknown";
 }

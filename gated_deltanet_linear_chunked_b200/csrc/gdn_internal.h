@@ -10,6 +10,23 @@
 
 namespace gdn {
 
+// ---- host checks shared by the entry points
+struct Range {
+  uintptr_t lo, hi;  // [lo, hi)
+};
+inline Range range_of(const void* p, size_t bytes) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return {lo, lo + bytes};
+}
+inline bool overlaps(Range a, Range b) {
+  if (a.lo == a.hi || b.lo == b.hi) return false;
+  return a.lo < b.hi && b.lo < a.hi;
+}
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool supported_dim(int d) { return d >= 16 && d <= 128 && d % 16 == 0; }
+// A pointer the current device can use as ordinary device memory.
+gdn_status check_device_pointer(const void* p, int dev);
+
 // One scan call, after validation.  Pointers are device pointers.
 struct ScanArgs {
   const void* q;
@@ -47,7 +64,10 @@ enum KernelId : int {
   kKernBwdChunk = 8,   // the chunked backward's pre pass
   kKernBwdChain = 9,
   kKernBwdGrad = 10,
-  kNumKernelIds = 11,
+  kKernNormRope = 11,
+  kKernNormRopeBwd = 12,
+  kKernNormRopeReduce = 13,
+  kNumKernelIds = 14,
 };
 
 // While profiling is armed, records CUDA events around one launch.
@@ -170,9 +190,18 @@ struct SwaCall {
 int sink_window_slot(int chunk, int n_sink, int window);
 cudaError_t launch_sink_window(const SwaCall& c);
 
-// The per-(device, stream) scratch of at least `bytes` (nullptr under stream
-// capture when it cannot be provided); GDN_OK or GDN_ERR_CUDA.
-gdn_status stream_scratch(int dev, cudaStream_t s, size_t bytes, unsigned int** err, void** ws);
+// Scratch of one call of an operator: the (device, stream) context's, or, for
+// a call that is being captured, an allocation of the graph's own (memory
+// nodes), so that two captured graphs never share it whatever streams they are
+// replayed on.  `err` gets the stream's error word, or the device-wide one.
+// GDN_OK or GDN_ERR_CUDA.
+struct OpScratch {
+  void* p;
+  cudaStream_t stream;
+  bool captured;
+};
+gdn_status op_scratch(int dev, cudaStream_t s, size_t bytes, unsigned int** err, OpScratch* sc);
+cudaError_t op_scratch_done(const OpScratch& sc);
 
 // Device error word values.
 enum : unsigned int {

@@ -310,6 +310,89 @@ GDN_API gdn_status gdn_sink_window_attention(const void* q, const void* k, const
 GDN_API int gdn_sink_window_slot(int chunk_index, int n_sink, int window);
 
 /*
+ * Queries and keys of a softmax block on their way to the attention: an RMS
+ * norm of every head and rotary positions, in one pass over each row, and the
+ * gradients.  The pages keep the block's attention and leave its projections'
+ * norms and positions unwritten; these are the forms that are in use for such
+ * blocks.  For one head row x of D features:
+ *
+ *     r = (mean(x^2) + eps)^(-1/2),   y = weight * r x    (gdn_rope: y = x)
+ *     out_a = A (y_a cos t - y_b sin t),  out_b = A (y_a sin t + y_b cos t)
+ *
+ * for the pairs (a, b) of the first rot_dim features, the other features being
+ * y.  All arithmetic is fp32 with one rounding at the end; the angle
+ * t = position * inv_freq[pair] is formed in fp64 (positions of any size up to
+ * 2^31 keep an angle good to fp32).
+ *
+ * Views.  q, k and the buffers of their shape are [B, T, H, D] views: heads and
+ * features contiguous, batch and token strides given in elements (of 0 or
+ * more, multiples of 16 bytes, at most 2^40; a stride whose extent is 1 is not
+ * used).  So q and k may lie side by side in one projection's output, and
+ * k_out may be a chunk's slot of a cache.  An output may be exactly the view it
+ * is computed from (in place), and outputs may interleave with other views of
+ * the same strides; any other overlap is GDN_ERR_ALIAS.  Hk = 0 leaves the
+ * keys out (and then takes NULL for them); Hq = 0 the queries.
+ */
+typedef struct {
+  void* data;               /* 16-byte aligned device pointer; inputs are only read */
+  long long batch_stride;   /* elements */
+  long long token_stride;
+} gdn_rows;
+
+typedef enum {
+  GDN_ROPE_HALF = 0,         /* pair i: features i and i + rot_dim / 2 */
+  GDN_ROPE_INTERLEAVED = 1   /* pair i: features 2i and 2i + 1 */
+} gdn_rope_layout;
+
+typedef struct {
+  const void* positions;            /* [B, T, axes], int32 or int64 */
+  const double* inv_freq;           /* [rot_dim / 2], radians per position */
+  long long position_batch_stride;  /* elements; 0: every batch row has the same */
+  int position_bytes;               /* 4 or 8 */
+  int axes;                         /* 1 to 3 position axes (say frame, row, column) */
+  int section[3];                   /* pairs that turn by each axis, in order; sum rot_dim / 2 */
+  int rot_dim;                      /* features that turn: a multiple of 16, 0 to D */
+  int layout;                       /* gdn_rope_layout */
+  float amplitude;                  /* A: 1, or the long-context factor */
+} gdn_rotation;
+
+/*
+ * Rotary positions alone.  inverse != 0 turns by -t, which is also the
+ * gradient: d(input) is the inverse turn (same amplitude) of d(output).
+ * dtype is GDN_F32 or GDN_BF16; D a multiple of 16 in [16, 128]
+ * (else GDN_ERR_UNSUPPORTED); B * T below 2^30.  Nothing to do with B, T or
+ * both head counts zero: GDN_OK.
+ */
+GDN_API gdn_status gdn_rope(const gdn_rows* q, const gdn_rows* k, const gdn_rotation* rotation,
+                            int inverse, const gdn_rows* q_out, const gdn_rows* k_out, int B, int T,
+                            int Hq, int Hk, int D, gdn_dtype dtype, void* stream);
+
+/*
+ * Norm and rotary positions in one pass.  q_weight, k_weight [D] fp32, shared
+ * by the heads, or NULL for ones; rotation NULL (or rot_dim 0): the norm alone.
+ */
+GDN_API gdn_status gdn_qk_norm_rope(const gdn_rows* q, const gdn_rows* k, const float* q_weight,
+                                    const float* k_weight, const gdn_rotation* rotation,
+                                    const gdn_rows* q_out, const gdn_rows* k_out, int B, int T, int Hq,
+                                    int Hk, int D, float eps, gdn_dtype dtype, void* stream);
+
+/*
+ * Gradients of gdn_qk_norm_rope, given its inputs and the gradients dq_out,
+ * dk_out of its outputs: dq, dk (dtype; may be the views of dq_out, dk_out or
+ * of q, k) and dq_weight, dk_weight [D] fp32 (NULL: not wanted), which are sums
+ * over every row, taken in a fixed order: the same call gives the same bits.
+ * With no rows the weights' gradients are zero.  Scratch comes from the
+ * stream's context, or, in a call that is being captured, from the graph.
+ */
+GDN_API gdn_status gdn_qk_norm_rope_backward(const gdn_rows* q, const gdn_rows* k,
+                                             const float* q_weight, const float* k_weight,
+                                             const gdn_rotation* rotation, const gdn_rows* dq_out,
+                                             const gdn_rows* dk_out, const gdn_rows* dq,
+                                             const gdn_rows* dk, float* dq_weight, float* dk_weight,
+                                             int B, int T, int Hq, int Hk, int D, float eps,
+                                             gdn_dtype dtype, void* stream);
+
+/*
  * Time segments of the bf16 path's recurrence.  The stage that walks the
  * chunks is a dependent chain of ceil(T / 64) steps per (head, 16 state
  * columns).  When a call has too few such chains to fill the GPU and many
@@ -345,7 +428,8 @@ GDN_API unsigned long long gdn_launch_count(void);
  * 1 stage A (prep), 2 stage B (recurrence, every pass), 3 stage C (output),
  * 4 the time-segment prefix, 5 the token-serial backward, 6 the backward
  * reduction, 7 the sink + window attention, 8 / 9 / 10 the chunked
- * backward's pre, chain and gradient passes; names from gdn_kernel_name.  Not thread-safe against concurrent calls on other
+ * backward's pre, chain and gradient passes, 11 / 12 / 13 the norm and rotary
+ * pass, its gradients and their reduction; names from gdn_kernel_name.  Not thread-safe against concurrent calls on other
  * threads; meant for benchmarks.
  */
 GDN_API gdn_status gdn_profile_begin(int max_launches);
