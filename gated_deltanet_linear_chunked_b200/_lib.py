@@ -49,6 +49,8 @@ SIGNATURES = {
     "gdn_qk_norm_rope": (ctypes.c_int, [_vp] * 7 + [_i] * 5 + [ctypes.c_float, _i, _vp]),
     "gdn_qk_norm_rope_backward": (ctypes.c_int,
                                   [_vp] * 11 + [_i] * 5 + [ctypes.c_float, _i, _vp]),
+    "gdn_cross_attention": (ctypes.c_int, [_vp] * 4 + [_ll] + [_vp] * 2 + [_i] * 6 +
+                            [ctypes.c_float, _i, _vp]),
     "gdn_state_reset": (ctypes.c_int, [_fp, _i, _i, _i, _i, _vp]),
     "gdn_device_error": (ctypes.c_int, [_vp]),
     "gdn_workspace_release": (ctypes.c_int, []),

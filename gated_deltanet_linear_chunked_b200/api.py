@@ -425,6 +425,58 @@ def qk_norm_rope_backward(q, k, q_weight, k_weight, dq_out, dk_out, positions=No
     return {"dq": dq, "dk": dk, "dq_weight": dqw, "dk_weight": dkw}
 
 
+def _cross_args(q, k, v, key_mask, scale):
+    """Shapes, views, mask pointer and stride, and scale of a cross-attention call."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B,Tq,Hq,D] and k, v [B,S,Hk,D]")
+    B, Tq, Hq, D = q.shape
+    S, Hk = k.shape[1], k.shape[2]
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q, k, v must be bfloat16, got {q.dtype}")
+    qs, ks = (B, Tq, Hq, D), (B, S, Hk, D)
+    vq = _view(q, "q", torch.bfloat16, qs)
+    vk, vv = _view(k, "k", torch.bfloat16, ks), _view(v, "v", torch.bfloat16, ks)
+    mp, ms = None, 0
+    if key_mask is not None:
+        if not key_mask.is_cuda:
+            raise ValueError("key_mask must be a CUDA tensor")
+        if key_mask.dtype != torch.bool and key_mask.dtype != torch.uint8:
+            raise TypeError(f"key_mask must be bool or uint8, got {key_mask.dtype}")
+        if key_mask.shape != (B, S):
+            raise ValueError(f"key_mask must have shape {(B, S)}, got {tuple(key_mask.shape)}")
+        ms, step = key_mask.stride()
+        if S > 1 and step != 1:
+            raise ValueError("key_mask must be contiguous over the keys")
+        mp, ms = key_mask.data_ptr(), ms if B > 1 else 0
+    if scale is None:
+        scale = D ** -0.5 if D else 1.0
+    return B, Tq, S, Hq, Hk, D, vq, vk, vv, mp, ms, scale
+
+
+def cross_attention(q, k, v, key_mask=None, *, scale=None, out=None, return_lse=False, stream=None):
+    """Softmax attention of q [B,Tq,Hq,D] over an encoder's k, v [B,S,Hk,D] (bf16;
+    Hq a multiple of Hk, query head h reading key head h // (Hq // Hk)).
+    ``key_mask`` [B,S] (bool or uint8) keeps the keys it is nonzero for; a batch row
+    that keeps none gives zeros.  ``scale`` defaults to 1/sqrt(D).  k and v may be
+    views of one projection, or expanded over the batch.  Returns ``out``
+    [B,Tq,Hq,D], or ``(out, lse)`` with lse [B,Hq,Tq] fp32, which
+    ``cross_attention_backward`` takes."""
+    B, Tq, S, Hq, Hk, D, vq, vk, vv, mp, ms, scale = _cross_args(q, k, v, key_mask, scale)
+    dev = q.device
+    if out is None:
+        out = _fresh(stream, torch.empty, (B, Tq, Hq, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_tensor(out, "out", torch.bfloat16, (B, Tq, Hq, D))
+    lse = None
+    if return_lse:
+        lse = _fresh(stream, torch.empty, (B, Hq, Tq), dtype=torch.float32, device=dev)
+    st = _lib.load().gdn_cross_attention(vq, vk, vv, mp, ms, out.data_ptr(), _ptr(lse), B, Tq, S, Hq,
+                                         Hk, D, scale, _lib.GDN_BF16, _raw_stream(stream, dev))
+    _lib.check(st, "gdn_cross_attention")
+    _used_on(stream, q, k, v, key_mask, out, lse)
+    return (out, lse) if return_lse else out
+
+
 def state_reset(state, stream=None):
     """Zero a state tensor [B,H,Dk,Dv] in place (streaming restart)."""
     _check_tensor(state, "state", torch.float32)

@@ -1,0 +1,140 @@
+// cross_api.cu -- the cross-attention entry points (include/gdn.h): host-side
+// checks, scratch and launch.
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "gdn_internal.h"
+
+namespace gdn {
+namespace {
+
+constexpr long long kMaxStride = 1ll << 36;  // elements: TMA strides stay below 2^40 bytes
+
+// A [B, T, H, D] bf16 view the TMA maps can take: data aligned to 16 bytes,
+// strides in range and multiples of 16 bytes.
+bool good_view(const gdn_rows* v, int B, int T) {
+  if (!v || !v->data || !aligned16(v->data)) return false;
+  if (v->batch_stride < 0 || v->batch_stride > kMaxStride || v->token_stride < 0 ||
+      v->token_stride > kMaxStride)
+    return false;
+  if ((B > 1 && v->batch_stride % 8) || (T > 1 && (v->token_stride % 8 || v->token_stride == 0)))
+    return false;
+  return true;
+}
+
+Range range_of_view(const gdn_rows& v, int B, int T, long long row) {
+  if (B == 0 || T == 0) return {0, 0};
+  const uintptr_t lo = (uintptr_t)v.data;
+  return {lo, lo + (uintptr_t)(2 * ((B - 1) * v.batch_stride + (T - 1) * v.token_stride + row))};
+}
+
+struct Checked {
+  CrossCall c;
+  Range reads[8];
+  int nreads;
+  const void* ptrs[16];
+  int nptrs;
+  bool nothing;  // nothing to compute
+};
+
+// The checks both directions share, none of which makes a CUDA call.
+gdn_status check_inputs(const gdn_rows* q, const gdn_rows* k, const gdn_rows* v, const unsigned char* mask,
+                        long long mask_bs, int B, int Tq, int S, int Hq, int Hk, int D, float scale,
+                        gdn_dtype dtype, void* stream, Checked* o) {
+  if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+  if (B < 0 || Tq < 0 || S < 0 || Hq < 0 || Hk < 0 || D < 0) return GDN_ERR_INVALID_ARG;
+  if (!(scale >= 0.f) || std::isinf(scale)) return GDN_ERR_INVALID_ARG;
+  if (mask_bs < 0 || mask_bs > kMaxStride) return GDN_ERR_INVALID_ARG;
+  if (dtype != GDN_BF16 || !supported_dim(D)) return GDN_ERR_UNSUPPORTED;
+  if (Hq > 0 && (Hk == 0 || Hq % Hk)) return GDN_ERR_INVALID_ARG;
+  if (Hq > 0 && Hq / Hk > 128) return GDN_ERR_UNSUPPORTED;
+  // one-dimensional grids over (batch, head, tile): query and key tiles are at
+  // least a token each
+  if (S > (1 << 30) || Tq > (1 << 30) || (double)B * Hq * (Tq / 16.0 + S / 16.0 + 2.0) > 1.0e9)
+    return GDN_ERR_UNSUPPORTED;
+  CrossCall& c = o->c;
+  c = CrossCall{};
+  c.B = B; c.Tq = Tq; c.S = S; c.Hq = Hq; c.Hk = Hk; c.D = D;
+  c.scale = scale;
+  c.stream = static_cast<cudaStream_t>(stream);
+  o->nreads = o->nptrs = 0;
+  o->nothing = B == 0 || Hq == 0;
+  if (o->nothing) return GDN_OK;
+  if (Tq > 0) {
+    if (!good_view(q, B, Tq)) return GDN_ERR_INVALID_ARG;
+    c.q = *q;
+    if (B == 1) c.q.batch_stride = 1;  // not used; nonzero, so that it is no broadcast
+    o->reads[o->nreads++] = range_of_view(c.q, B, Tq, (long long)Hq * D);
+    o->ptrs[o->nptrs++] = q->data;
+  }
+  if (S > 0) {
+    if (!good_view(k, B, S) || !good_view(v, B, S)) return GDN_ERR_INVALID_ARG;
+    c.k = *k;
+    c.v = *v;
+    if (B == 1) c.k.batch_stride = c.v.batch_stride = 1;
+    o->reads[o->nreads++] = range_of_view(c.k, B, S, (long long)Hk * D);
+    o->reads[o->nreads++] = range_of_view(c.v, B, S, (long long)Hk * D);
+    o->ptrs[o->nptrs++] = k->data;
+    o->ptrs[o->nptrs++] = v->data;
+    if (mask) {
+      c.mask = mask;
+      c.mask_bs = mask_bs;
+      o->reads[o->nreads++] = range_of(mask, (size_t)((B - 1) * mask_bs + S));
+      o->ptrs[o->nptrs++] = mask;
+    }
+  }
+  return GDN_OK;
+}
+
+gdn_status check_device(const Checked& o, int* dev) {
+  if (cudaGetDevice(dev) != cudaSuccess) {
+    cudaGetLastError();
+    return GDN_ERR_CUDA;
+  }
+  for (int i = 0; i < o.nptrs; ++i) {
+    const gdn_status st = check_device_pointer(o.ptrs[i], *dev);
+    if (st != GDN_OK) return st;
+  }
+  cudaGetLastError();
+  return GDN_OK;
+}
+
+}  // namespace
+}  // namespace gdn
+
+extern "C" {
+
+gdn_status gdn_cross_attention(const gdn_rows* q, const gdn_rows* k, const gdn_rows* v,
+                               const unsigned char* key_mask, long long mask_batch_stride, void* out,
+                               float* lse, int B, int Tq, int S, int Hq, int Hk, int D, float scale,
+                               gdn_dtype dtype, void* stream) {
+  using namespace gdn;
+  Checked o;
+  gdn_status st = check_inputs(q, k, v, key_mask, mask_batch_stride, B, Tq, S, Hq, Hk, D, scale, dtype,
+                               stream, &o);
+  if (st != GDN_OK || o.nothing || Tq == 0) return st;
+  if (!out || !aligned16(out) || (lse && !aligned16(lse))) return GDN_ERR_INVALID_ARG;
+  const Range ro = range_of(out, (size_t)B * Tq * Hq * D * 2);
+  const Range rl = range_of(lse, lse ? (size_t)B * Tq * Hq * 4 : 0);
+  if (overlaps(ro, rl)) return GDN_ERR_ALIAS;
+  for (int i = 0; i < o.nreads; ++i)
+    if (overlaps(ro, o.reads[i]) || overlaps(rl, o.reads[i])) return GDN_ERR_ALIAS;
+  o.ptrs[o.nptrs++] = out;
+  if (lse) o.ptrs[o.nptrs++] = lse;
+  int dev = 0;
+  st = check_device(o, &dev);
+  if (st != GDN_OK) return st;
+  CrossCall& c = o.c;
+  c.out = out;
+  c.lse = lse;
+  OpScratch sc;
+  st = op_scratch(dev, c.stream, cross_workspace_bytes(c), &c.err, &sc);
+  if (st != GDN_OK) return st;
+  c.limit = current_wait_limit();
+  const cudaError_t e = launch_cross(c, sc.p);
+  const cudaError_t f = op_scratch_done(sc);
+  return finish(c.stream, e == cudaSuccess ? f : e, c.err);
+}
+
+}  // extern "C"

@@ -779,6 +779,8 @@ const char* gdn_kernel_name(int id) {
     case gdn::kKernNormRope: return "gdn_norm_rope_kernel";
     case gdn::kKernNormRopeBwd: return "gdn_norm_rope_bwd_kernel";
     case gdn::kKernNormRopeReduce: return "gdn_norm_rope_reduce_kernel";
+    case gdn::kKernCross: return "gdn_cross_kernel";
+    case gdn::kKernCrossJoin: return "gdn_cross_join_kernel";
   }
   return "unknown";
 }

@@ -67,7 +67,12 @@ enum KernelId : int {
   kKernNormRope = 11,
   kKernNormRopeBwd = 12,
   kKernNormRopeReduce = 13,
-  kNumKernelIds = 14,
+  kKernCross = 14,
+  kKernCrossJoin = 15,
+  kKernCrossDq = 16,
+  kKernCrossDkv = 17,
+  kKernCrossDkvJoin = 18,
+  kNumKernelIds = 19,
 };
 
 // While profiling is armed, records CUDA events around one launch.
@@ -171,6 +176,14 @@ cudaError_t launch_backward_chunked(const BwdCall& c, void* workspace, float** p
 // lands in shared memory in the [slab][token][8] core-matrix layout.
 bool make_tile_map(CUtensorMap* m, const void* base, int nb, int T, int H, int D, int box_rows);
 
+// A [nb, T, Hk * G, D] bf16 view (strides in elements) as 5-D (D, G, T, Hk, nb):
+// one box is 64 features of the G heads that share a key head, box_tokens
+// tokens of them, and lands in shared memory as rows token * G + head of 128
+// bytes with the 128-byte swizzle.  Features past D and tokens past T read as 0
+// and are not stored.
+bool make_heads_map(CUtensorMap* m, const void* base, int nb, int T, int Hk, int G, int D,
+                    long long batch_stride, long long token_stride, int box_tokens);
+
 // Streaming multiprocessors of the current device (cached per device).
 int num_sms();
 
@@ -202,6 +215,27 @@ struct OpScratch {
 };
 gdn_status op_scratch(int dev, cudaStream_t s, size_t bytes, unsigned int** err, OpScratch* sc);
 cudaError_t op_scratch_done(const OpScratch& sc);
+
+// One cross-attention call, after validation.
+struct CrossCall {
+  gdn_rows q, k, v;            // [B, Tq, Hq, D], [B, S, Hk, D] bf16 views
+  const uint8_t* mask;         // [B, S] or nullptr; nonzero: the key is seen
+  long long mask_bs;
+  void* out;                   // [B, Tq, Hq, D] bf16 (backward: read)
+  float* lse;                  // [B, Hq, Tq] fp32, or nullptr (backward: read)
+  const void* d_out;           // backward: [B, Tq, Hq, D] bf16
+  void *dq, *dk, *dv;          // backward: [B, Tq, Hq, D], [B, S, Hk, D] bf16
+  int B, Tq, S, Hq, Hk, D;
+  float scale;
+  cudaStream_t stream;
+  unsigned int* err;
+  long long limit;
+};
+// Scratch of the two directions, and the launches into it.
+size_t cross_workspace_bytes(const CrossCall& c);
+cudaError_t launch_cross(const CrossCall& c, void* ws);
+size_t cross_backward_workspace_bytes(const CrossCall& c);
+cudaError_t launch_cross_backward(const CrossCall& c, void* ws);
 
 // Device error word values.
 enum : unsigned int {

@@ -65,33 +65,6 @@ constexpr uint32_t kMinSmem = 116 * 1024;      // more than half an SM: one CTA 
 constexpr float kRescaleLog2 = 8.f;            // headroom of the running maximum
 constexpr long long kDrainPolls = 1LL << 40;   // drains are bounded by the 2 s timer
 
-// 2^x for a pair of x <= 2^8 on the FMA pipe, so that the special-function
-// unit's ex2 is not the only source of exponentials: Cody and Waite's range
-// reduction x = n + f (n = round(x) by adding and subtracting 1.5 * 2^23, f in
-// [-1/2, 1/2]) with 2^f from a degree-3 polynomial whose coefficients were
-// fitted here to 2^f on [-1/2, 1/2] by weighted least squares in relative
-// error (Lawson's iteration); its largest relative error is 7.5e-5, far under
-// the bf16 rounding of P.  2^n enters by adding n to the exponent field.
-// Inputs are clamped at -125 (2^-125 stands for 0, as ex2 gives for -inf).
-__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x) {
-  float x0, x1;
-  f2_unpack(x, x0, x1);
-  const uint64_t xc = f2_pack(fmaxf(x0, -125.f), fmaxf(x1, -125.f));
-  const uint64_t magic = f2_pack(12582912.f, 12582912.f);
-  const uint64_t t = f2_add(xc, magic);                        // n in the low bits
-  const uint64_t n = f2_add(t, f2_pack(-12582912.f, -12582912.f));
-  const uint64_t f = f2_fma(n, f2_pack(-1.f, -1.f), xc);       // x - n
-  uint64_t p = f2_fma(f2_pack(0.0551716648f, 0.0551716648f), f,
-                      f2_pack(0.2426111251f, 0.2426111251f));
-  p = f2_fma(p, f, f2_pack(0.6932609677f, 0.6932609677f));
-  p = f2_fma(p, f, f2_pack(0.9999280572f, 0.9999280572f));
-  float p0, p1, t0, t1;
-  f2_unpack(p, p0, p1);
-  f2_unpack(t, t0, t1);
-  return f2_pack(__uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23)),
-                 __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23)));
-}
-
 struct SwaParams {
   int Tc, H, D, nslot;
   // work units: blockIdx.x < pair_units is the pair of query tiles

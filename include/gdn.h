@@ -393,6 +393,41 @@ GDN_API gdn_status gdn_qk_norm_rope_backward(const gdn_rows* q, const gdn_rows* 
                                              gdn_dtype dtype, void* stream);
 
 /*
+ * The softmax blocks' second attention: over an encoder's states of another
+ * length (the prompt's, or the source clip's; the pages quantise the blocks'
+ * cross-attention projections, "SANA-Streaming：基于混合扩散Transformer的实时流式
+ * 视频编辑系统", 实验结果, without writing the operation, which is the softmax
+ * attention of the streaming blocks over these keys).  Per query head h, with
+ * key head h / (Hq / Hk):
+ *
+ *     s = scale q.k over the keys the mask keeps,  lse = log sum e^s,
+ *     out = sum e^(s - lse) v
+ *
+ * fp32 scores, softmax and sums, bf16 P and out.  A batch row that keeps no key
+ * (or S = 0) has out = 0 and lse = -infinity.  Values in masked rows of k and v
+ * (NaN and infinities among them) do not reach any result.
+ *
+ *   q [B, Tq, Hq, D], k, v [B, S, Hk, D]   bf16 views as for gdn_qk_norm_rope
+ *                          (batch stride 0: one batch row's states for all)
+ *   key_mask               [B, S] bytes, nonzero: the key is seen; NULL: all are;
+ *                          mask_batch_stride bytes between rows (0: one row for all)
+ *   out                    [B, Tq, Hq, D] bf16, contiguous
+ *   lse                    [B, Hq, Tq] fp32, or NULL; the backward needs it
+ *
+ * Requirements: dtype GDN_BF16 and D a multiple of 16 in [16, 128] (else
+ * GDN_ERR_UNSUPPORTED); Hq a multiple of Hk, scale finite and not negative (else
+ * GDN_ERR_INVALID_ARG); Hq / Hk at most 128, sizes whose products of a launch
+ * stay below 2^31 (else GDN_ERR_UNSUPPORTED).  out and lse must not overlap
+ * anything (GDN_ERR_ALIAS).  B, Tq or Hq zero: nothing to do.  Errors and the
+ * per-stream error word as for the scan; scratch from the stream's context, or,
+ * in a call that is being captured, from the graph.
+ */
+GDN_API gdn_status gdn_cross_attention(const gdn_rows* q, const gdn_rows* k, const gdn_rows* v,
+                                       const unsigned char* key_mask, long long mask_batch_stride,
+                                       void* out, float* lse, int B, int Tq, int S, int Hq, int Hk,
+                                       int D, float scale, gdn_dtype dtype, void* stream);
+
+/*
  * Time segments of the bf16 path's recurrence.  The stage that walks the
  * chunks is a dependent chain of ceil(T / 64) steps per (head, 16 state
  * columns).  When a call has too few such chains to fill the GPU and many
@@ -429,7 +464,8 @@ GDN_API unsigned long long gdn_launch_count(void);
  * 4 the time-segment prefix, 5 the token-serial backward, 6 the backward
  * reduction, 7 the sink + window attention, 8 / 9 / 10 the chunked
  * backward's pre, chain and gradient passes, 11 / 12 / 13 the norm and rotary
- * pass, its gradients and their reduction; names from gdn_kernel_name.  Not thread-safe against concurrent calls on other
+ * pass, its gradients and their reduction, 14 / 15 the cross attention and the
+ * join of its splits; names from gdn_kernel_name.  Not thread-safe against concurrent calls on other
  * threads; meant for benchmarks.
  */
 GDN_API gdn_status gdn_profile_begin(int max_launches);

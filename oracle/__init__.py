@@ -22,6 +22,8 @@ Contents
   * ``backward``   -- the forward definition in plain PyTorch CPU float64,
                       differentiated by autograd: the reference gradients of
                       the scan.
+  * ``cross_attn`` -- the softmax blocks' attention to an encoder's states under
+                      a key mask, and its gradients, in numpy float64.
   * ``norm_rope``  -- the softmax blocks' query/key norm and rotary positions,
                       and their gradients, in numpy float64.
   * ``sink_window_attn`` -- the softmax blocks' attention over a persistent
@@ -41,6 +43,7 @@ from .cpu import (  # noqa: F401
     oracle_fwd_logits,
 )
 from . import backward  # noqa: F401
+from . import cross_attn  # noqa: F401
 from . import norm_rope  # noqa: F401
 from . import sink_window_attn  # noqa: F401
 from .numpy_ref import (  # noqa: F401
