@@ -15,21 +15,29 @@
 //
 // A CTA takes two such tiles g (one where there is only one) of a (b, key head)
 // and walks 128-key tiles; every K and V tile loaded serves both.
-//   warp 8         TMA producer: the Q tiles, then K_0 V_0 K_1 V_1 ... through a
+//   warp 16        TMA producer: the Q tiles, then K_0 V_0 K_1 V_1 ... through a
 //                  ring of four slots (128-byte swizzle: a box row is 128 bytes).
-//   warps 9, 10    MMA issue for g = 0, 1, one lane each: S_g = Q_g K_j^T (M 128,
+//   warp 17        MMA issue, one lane, g = 0, 1 in turn: S_g = Q_g K_j^T (M 128,
 //                  N 128, K D) and O_g += P_g V_j (M 128, N D, K 128), both in
-//                  TMEM; P_g is read from TMEM (bf16, over the first 64 columns of
+//                  TMEM; P_g is read from TMEM (bf16, over columns of
 //                  S_g), which leaves shared memory's bandwidth to K and V: from
 //                  shared memory P alone would take 4 KB per 16 keys against V's
 //                  2 D bytes x 16, more than the tensor core's time allows.
-//   warps 0-3, 4-7 softmax of g = 0, 1, a row per thread (its TMEM lane): maximum,
-//                  p = 2^(s c - m), sum, P back to TMEM; O is rescaled in TMEM
-//                  only when the maximum has grown by more than 2^8 (until then p
-//                  may reach 2^8, which fp32 sums and bf16 P hold as well as 1).
+//   warps 0-15     softmax, eight warps for each g: a row (TMEM lane) by two
+//                  threads, 64 keys each: maximum, p = 2^(s c - m), sum, P back to
+//                  TMEM.  m moves, and O is rescaled in TMEM, only when a row's
+//                  maximum has grown by more than 2^8 (until then p may reach 2^8,
+//                  which fp32 sums and bf16 P hold as well as 1), so the halves of a
+//                  row only vote in a barrier whether any has, and exchange maxima
+//                  if so.  One thread per row left the schedulers idle two cycles in
+//                  three.  The product with V starts on the half that is ready.
 // P_g,j is used up before S_g,j+1 is written over it because one thread issues
-// both and tensor-core operations of one thread complete in order; while one
-// tile's softmax runs the other's products do.
+// both and tensor-core operations of one thread complete in order.  That thread
+// takes the tiles strictly in turn (P V and the next S of g = 0, then of g = 1),
+// which keeps them half a step apart: one's softmax runs under the other's
+// products.  With an issuing thread each, the products interleaved, both tiles'
+// scores were ready at the same time and their softmaxes ran together, the tensor
+// core waiting (7920 keys, 7 x 256 queries, 20 heads of 112: 186 us).
 // Masked keys: a CTA first reads its batch row's mask into one bit per key and
 // lists the key tiles that have any, so tiles without are never loaded; in tiles
 // with some, scores of masked keys become -inf whatever they were, and the masked
@@ -56,10 +64,12 @@ using namespace sm100;
 
 constexpr int kQTiles = 2;
 constexpr int kRows = 128;             // rows of a query tile, keys of a key tile
+constexpr int kHalf = kRows / 2;       // keys of a softmax thread
 constexpr int kSlots = 4;              // ring of K and V tiles
-constexpr int kProducerWarp = 8;
-constexpr int kMmaWarp = 9;
-constexpr int kThreads = 32 * (kMmaWarp + kQTiles);
+constexpr int kSoftmaxWarps = 8 * kQTiles;  // two groups of four warps per query tile
+constexpr int kProducerWarp = kSoftmaxWarps;
+constexpr int kMmaWarp = kProducerWarp + 1;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr uint32_t kTileCols = 256;    // TMEM columns of a tile: S (and P) [0, 128) | O [128, 128 + D)
 constexpr uint32_t kBlock = kRows * 128;  // one 64-feature block of a 128-row tile, bytes
 constexpr int kMaskTiles = 128;        // key tiles of one CTA under a mask, at most
@@ -87,37 +97,47 @@ struct CrossParams {
 struct CrossAux {
   uint64_t q_full;
   uint64_t full[kSlots], empty[kSlots];
-  uint64_t s_full[kQTiles], p_full[kQTiles], o_full[kQTiles], drain[kQTiles];
+  uint64_t s_full[kQTiles], p_full[kQTiles][2], o_full[kQTiles], drain;
   uint32_t tmem;
   int abort;
   int count;                       // key tiles to walk
+  float row[kQTiles][2][kRows];    // a row's two halves exchange maxima, later sums
   uint32_t bits[kMaskTiles * 4];   // seen keys of each of the CTA's tiles (under a mask)
   uint8_t list[kMaskTiles];        // tiles with any
 };
 
 // Shared memory: Q tiles (later the output's), the ring, the barriers and mask.
+template <int NB>  // 64-feature blocks of a head
 struct CrossLayout {
-  uint32_t tile, q, ring, aux, total;
+  static constexpr uint32_t tile = NB * kBlock;
+  static constexpr uint32_t q = 0;
+  static constexpr uint32_t ring = kQTiles * tile;
+  static constexpr uint32_t aux = ring + kSlots * tile;
+  static constexpr uint32_t total = aux + (uint32_t)sizeof(CrossAux);
 };
-__host__ __device__ inline CrossLayout cross_layout(int D) {
-  CrossLayout L;
-  L.tile = ((D + 63) / 64) * kBlock;
-  L.q = 0;
-  L.ring = kQTiles * L.tile;
-  L.aux = L.ring + kSlots * L.tile;
-  L.total = L.aux + (uint32_t)sizeof(CrossAux);
-  return L;
+
+// 32 scores of a row, those of masked keys -inf whatever they were.
+__device__ __forceinline__ void scores(uint32_t taddr, uint32_t seen, float (&s)[32]) {
+  tmem_ld32(taddr, s);
+  tmem_wait_ld();
+  if (seen != ~0u) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (!(seen >> i & 1)) s[i] = -INFINITY;
+  }
 }
 
+template <int NB>
 __global__ void __launch_bounds__(kThreads, 1)
 gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_out,
                  const __grid_constant__ CrossParams P) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int D = P.D, nb = (D + 63) / 64;
-  const CrossLayout L = cross_layout(D);
-  CrossAux& aux = *reinterpret_cast<CrossAux*>(smem + L.aux);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int D = P.D;
+  constexpr int nb = NB;
+  using L = CrossLayout<NB>;
+  CrossAux& aux = *reinterpret_cast<CrossAux*>(smem + L::aux);
+  const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;  // uniform
   // unit: ((b * Hk + hk) * groups + group) * nsplit + split
   const int split = blockIdx.x % P.nsplit, u = blockIdx.x / P.nsplit;
   const int group = u % P.groups, bh = u / P.groups;
@@ -130,14 +150,15 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     mbar_init(&aux.q_full, 1);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&aux.full[s], 1);
-      mbar_init(&aux.empty[s], nq);
+      mbar_init(&aux.empty[s], 1);
     }
     for (int g = 0; g < kQTiles; ++g) {
       mbar_init(&aux.s_full[g], 1);
-      mbar_init(&aux.p_full[g], kRows);
+      mbar_init(&aux.p_full[g][0], kRows);
+      mbar_init(&aux.p_full[g][1], kRows);
       mbar_init(&aux.o_full[g], 1);
-      mbar_init(&aux.drain[g], 1);
     }
+    mbar_init(&aux.drain, 1);
     aux.abort = 0;
     aux.count = kn;
     fence_mbar_init();
@@ -172,7 +193,7 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     __syncthreads();
   }
-  const uint32_t tm = aux.tmem;
+  const uint32_t tm = 0;  // all 512 columns: the allocation starts at the first
   const int n = aux.count;
   const bool masked = P.mask != nullptr;
   auto fail = [&]() {
@@ -180,7 +201,7 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     atomicOr(P.err, kErrTimeout);
   };
   // ring item i: K (even i) or V (odd i) of listed tile i / 2
-  auto slot_ptr = [&](int i) { return smem + L.ring + (i % kSlots) * L.tile; };
+  auto slot_ptr = [&](int i) { return smem + L::ring + (i % kSlots) * L::tile; };
   auto wait_full = [&](int i) { return mbar_wait(&aux.full[i % kSlots], (i / kSlots) & 1, P.limit); };
 
   if (warp == kProducerWarp) {
@@ -189,7 +210,7 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       mbar_arrive_expect_tx(&aux.q_full, nq * nb * qbytes);
       for (int g = 0; g < nq; ++g)
         for (int c = 0; c < nb; ++c)
-          tma_load_5d(smem + L.q + g * L.tile + c * kBlock, &tm_q, &aux.q_full, c * 64, 0,
+          tma_load_5d(smem + L::q + g * L::tile + c * kBlock, &tm_q, &aux.q_full, c * 64, 0,
                       (tile0 + g) * P.tokens, hk, b * P.qb);
       int issued = 0;
       for (int i = 0; i < 2 * n; ++i) {
@@ -200,7 +221,7 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         const int tile = k0 + (masked ? aux.list[i / 2] : i / 2);
         uint64_t* bar = &aux.full[i % kSlots];
-        mbar_arrive_expect_tx(bar, L.tile);
+        mbar_arrive_expect_tx(bar, L::tile);
         for (int c = 0; c < nb; ++c)
           tma_load_5d(slot_ptr(i) + c * kBlock, i & 1 ? &tm_v : &tm_k, bar, c * 64, 0, tile * kRows, hk,
                       b * (i & 1 ? P.vb : P.kb));
@@ -211,145 +232,161 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       for (int i = max(0, issued - kSlots); i < issued; ++i)
         mbar_wait(&aux.full[i % kSlots], (i / kSlots) & 1, kDrainPolls);
     }
-  } else if (warp >= kMmaWarp) {
-    const int g = warp - kMmaWarp;
-    if (lane == 0 && g < nq && n > 0) {
+  } else if (warp == kMmaWarp) {
+    if (n > 0) {  // the whole warp walks the loop, one elected lane issues
       const uint32_t idS = idesc_bf16(kRows, kRows, 0, 0), idO = idesc_bf16(kRows, D, 0, 1);
-      const uint32_t tS = tm + g * kTileCols, tO = tS + kRows;
-      const uint64_t dq = sdesc_sw128(smem_u32(smem + L.q + g * L.tile), 16);
-      bool ok = mbar_wait(&aux.q_full, 0, P.limit);
-      if (!ok) fail();
+      const uint64_t dq = sdesc_sw128(smem_u32(smem + L::q), 16);
+      bool ok = __all_sync(~0u, mbar_wait(&aux.q_full, 0, P.limit));
       for (int j = 0; ok && j <= n; ++j) {
-        if (*abort_flag) break;
-        if (j > 0) {
-          const int i = 2 * (j - 1) + 1;
-          if (!wait_full(i) || !mbar_wait(&aux.p_full[g], (j - 1) & 1, P.limit)) {
-            fail();
-            break;
-          }
-          tc_fence_after_sync();
-          // O_g += P_g V: P in TMEM (8 columns per 16 keys), V MN-major
-          const uint64_t dv = sdesc_sw128(smem_u32(slot_ptr(i)), kBlock);
+        for (int g = 0; g < nq; ++g) {
+          const uint32_t tS = tm + g * kTileCols, tO = tS + kRows;
+          if (j > 0) {
+            // O_g += P_g V, a half of the keys at a time: P in TMEM (8 columns per
+            // 16 keys, over the half's own scores), V MN-major
+            const int i = 2 * (j - 1) + 1;
+            if (g == 0) ok = __all_sync(~0u, wait_full(i));
+            const uint64_t dv = sdesc_sw128(smem_u32(slot_ptr(i)), kBlock);
 #pragma unroll
-          for (int ks = 0; ks < kRows / 16; ++ks)
-            mma_bf16_ts(tO, tS + ks * 8, dv + ks * (2048 >> 4), idO, j > 1 || ks > 0);
-          mma_commit(&aux.empty[i % kSlots]);
-        }
-        if (j < n) {
-          const int i = 2 * j;
-          if (!wait_full(i)) {
-            fail();
-            break;
+            for (int half = 0; half < 2; ++half) {
+              ok = ok && __all_sync(~0u, mbar_wait(&aux.p_full[g][half], (j - 1) & 1, P.limit));
+              if (!ok) break;
+              tc_fence_after_sync();
+#pragma unroll
+              for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                mma_bf16_ts_elect(tO, tS + kHalf * half + (ks & 3) * 8, dv + ks * (2048 >> 4), idO,
+                                  j > 1 || ks > 0);
+            }
+            if (!ok) break;
+            if (g == nq - 1) mma_commit_elect(&aux.empty[i % kSlots]);
           }
-          tc_fence_after_sync();
-          // S_g = Q_g K^T: both K-major
-          const uint64_t dk = sdesc_sw128(smem_u32(slot_ptr(i)), 16);
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t at = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
-            mma_bf16(tS, dq + at, dk + at, idS, ks > 0);
+          if (j < n) {
+            // S_g = Q_g K^T: both K-major
+            const int i = 2 * j;
+            if (g == 0) ok = __all_sync(~0u, wait_full(i));
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint64_t dk = sdesc_sw128(smem_u32(slot_ptr(i)), 16);
+            const uint64_t dqg = dq + (g * L::tile >> 4);
+#pragma unroll
+            for (int ks = 0; ks < 4 * NB; ++ks) {
+              const uint32_t at = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
+              if (ks < D / 16) mma_bf16_elect(tS, dqg + at, dk + at, idS, ks > 0);
+            }
+            mma_commit_elect(&aux.s_full[g]);
+            if (g == nq - 1) mma_commit_elect(&aux.empty[i % kSlots]);
+          } else {
+            mma_commit_elect(&aux.o_full[g]);
           }
-          mma_commit(&aux.s_full[g]);
-          mma_commit(&aux.empty[i % kSlots]);
-        } else {
-          mma_commit(&aux.o_full[g]);
         }
+        if (__any_sync(~0u, *abort_flag != 0)) break;
       }
-      mma_commit(&aux.drain[g]);
-      mbar_wait(&aux.drain[g], 0, kDrainPolls);
+      // every MMA issued has completed before TMEM and shared memory go
+      if (!ok && lane == 0) fail();
+      mma_commit_elect(&aux.drain);
+      mbar_wait(&aux.drain, 0, kDrainPolls);
+      __syncwarp();
     }
-  } else if ((warp >> 2) < nq) {
-    const int g = warp >> 2;
+  } else if ((warp >> 3) < nq) {
+    const int g = warp >> 3, half = (warp >> 2) & 1;  // keys [64 half, 64 half + 64) of each tile
     const int r = tid & (kRows - 1);
     const uint32_t tS = tm + g * kTileCols + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tO = tS + kRows;
+    const int oc0 = half ? (D / 32 + (D / 16) % 2) * 16 : 0;  // this half's columns of O
+    const int oc1 = half ? D : (D / 32 + (D / 16) % 2) * 16;
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      if (__any_sync(~0u, *abort_flag != 0)) {
-        ok = false;
-        break;
-      }
-      if (!__all_sync(~0u, mbar_wait(&aux.s_full[g], j & 1, P.limit))) {
-        if (lane == 0) fail();
-        ok = false;
-        break;
-      }
+      bool got = __all_sync(~0u, *abort_flag == 0 && mbar_wait(&aux.s_full[g], j & 1, P.limit));
       tc_fence_after_sync();
-      float s[kRows];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
-      tmem_wait_ld();
-      // the seen keys of the tile
-      uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
-      const int tile = masked ? aux.list[j] : j;
+      // the seen keys of this half of the tile
+      uint32_t bits[2] = {~0u, ~0u};
       if (masked) {
+        const int w = 4 * aux.list[j] + 2 * half;
+        bits[0] = aux.bits[w];
+        bits[1] = aux.bits[w + 1];
+      } else if (j == n - 1) {
+        const int left = P.S - (k0 + j) * kRows - kHalf * half;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) bits[c] = aux.bits[4 * tile + c];
-      } else {
-        const int left = P.S - (k0 + tile) * kRows;  // > 0
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 2; ++c)
           if (left < 32 * (c + 1)) bits[c] = left <= 32 * c ? 0u : (1u << (left - 32 * c)) - 1;
       }
-      const bool part = (bits[0] & bits[1] & bits[2] & bits[3]) != ~0u;  // uniform over the CTA
-      if (part) {
-#pragma unroll
-        for (int i = 0; i < kRows; ++i)
-          if (!(bits[i / 32] >> (i % 32) & 1)) s[i] = -INFINITY;
-        if (masked) {  // clear the masked rows of V
-          const int i = 2 * j + 1;
-          if (!__all_sync(~0u, wait_full(i))) {
-            if (lane == 0) fail();
-            ok = false;
-            break;
-          }
-          if (!(bits[r / 32] >> (r % 32) & 1)) {
-            for (int c = 0; c < nb * 8; ++c)
-              *reinterpret_cast<uint4*>(slot_ptr(i) + (c >> 3) * kBlock + r * 128 + (c & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
+      if (masked && (bits[0] & bits[1]) != ~0u) {  // clear the masked rows of V, a row by two threads
+        const int i = 2 * j + 1;
+        got = __all_sync(~0u, wait_full(i)) && got;
+        const int key = r >> 1, side = r & 1;
+        if (got && !(bits[key / 32] >> (key % 32) & 1)) {
+          uint8_t* row = slot_ptr(i) + (half * kHalf + key) * 128 + side * 64;
+          for (int c = 0; c < nb * 4; ++c)
+            *reinterpret_cast<uint4*>(row + (c >> 2) * kBlock + (c & 3) * 16) = make_uint4(0, 0, 0, 0);
         }
+        fence_proxy_async_smem();
       }
-      float acc[8];
+      // the scores are read twice, for the maximum and for p, 32 at a time:
+      // holding all 64 between costs more registers than 16 warps can have
+      float mx = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmax3(s[e], s[e + 8], s[e + 16]);
+      for (int c = 0; c < 2; ++c) {
+        float s[32];
+        scores(tS + kHalf * half + 32 * c, bits[c], s);
+        float acc[4];
 #pragma unroll
-      for (int i = 24; i + 16 <= 120; i += 16)
+        for (int e = 0; e < 4; ++e) acc[e] = fmax3(s[e], s[e + 4], s[e + 8]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = fmax3(acc[e], s[i + e], s[i + 8 + e]);
+        for (int i = 12; i + 8 <= 28; i += 8)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaxf(acc[e], s[120 + e]);
-      float mx = fmax3(fmax3(acc[0], acc[1], acc[2]), fmax3(acc[3], acc[4], acc[5]), fmaxf(acc[6], acc[7]));
+          for (int e = 0; e < 4; ++e) acc[e] = fmax3(acc[e], s[i + e], s[i + 4 + e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = fmaxf(acc[e], s[28 + e]);
+        mx = fmaxf(mx, fmaxf(fmax3(acc[0], acc[1], acc[2]), acc[3]));
+      }
       mx *= P.scale_log2;
-      float m_new = m_run, alpha = 1.f;
-      bool resc = false;
-      if (mx > m_run + kRescaleLog2) {
-        m_new = mx;
-        alpha = ex2_approx(m_run - m_new);  // 0 on the first tile
-        resc = j > 0;
-      }
-      if (__any_sync(~0u, resc)) {  // P V of the tile before is done: S of this one came after it
-        const float a = resc ? alpha : 1.f;
-        for (int c0 = 0; c0 < D; c0 += 16) {
-          float o[16];
-          tmem_ld16(tO + c0, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] *= a;
-          tmem_st16(tO + c0, o);
+      // does any row of the tile need a larger maximum (or has a wait given up)?
+      // One barrier with a vote; the rows' halves meet in shared memory only then.
+      float alpha = 1.f;
+      const bool quiet = got && !(mx > m_run + kRescaleLog2);
+      if (!named_barrier_and(1 + g, 2 * kRows, quiet)) {
+        aux.row[g][half][r] = mx;
+        if (!named_barrier_and(1 + g, 2 * kRows, got)) {
+          if (!got) fail();
+          ok = false;
+          break;
         }
+        mx = fmaxf(mx, aux.row[g][half ^ 1][r]);
+        const bool grow = mx > m_run + kRescaleLog2;
+        if (grow) {
+          alpha = ex2_approx(m_run - mx);  // 0 on the first tile
+          m_run = mx;
+        }
+        if (j > 0) {  // P V of the tile before is done: S of this one came after it
+          if (__any_sync(~0u, grow)) {
+            for (int c0 = oc0; c0 < oc1; c0 += 16) {
+              float o[16];
+              tmem_ld16(tO + c0, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= alpha;
+              tmem_st16(tO + c0, o);
+            }
+            tmem_wait_st();
+          }
+          tc_fence_before_sync();
+        }
+        named_barrier(1 + g, 2 * kRows);  // O is whole again before either half's P is handed on
+        tc_fence_after_sync();
       }
       // p = 2^(s c - m), two at a time: one pair in four on the FMA pipe, the
-      // rest on the special-function unit; P packed to bf16 into TMEM as it goes
-      const uint64_t c2 = f2_pack(P.scale_log2, P.scale_log2), nm2 = f2_pack(-m_new, -m_new);
-      uint64_t sum2[4] = {0, 0, 0, 0};
+      // rest on the special-function unit; P packed to bf16 into TMEM as it goes,
+      // over columns of this half that have been read
+      const uint64_t c2 = f2_pack(P.scale_log2, P.scale_log2), nm2 = f2_pack(-m_run, -m_run);
+      uint64_t sum2[2] = {0, 0};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
+        float s[32];
+        scores(tS + kHalf * half + 32 * c, bits[c], s);
         uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-          const uint64_t x = f2_fma(f2_pack(s[32 * c + i], s[32 * c + i + 1]), c2, nm2);
+          const uint64_t x = f2_fma(f2_pack(s[i], s[i + 1]), c2, nm2);
           uint64_t p2;
           float a, e;
           if ((i & 7) == 6) {
@@ -361,27 +398,28 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             e = ex2_approx(e);
             p2 = f2_pack(a, e);
           }
-          sum2[(i >> 1) & 3] = f2_add(sum2[(i >> 1) & 3], p2);
+          sum2[(i >> 1) & 1] = f2_add(sum2[(i >> 1) & 1], p2);
           pk[i >> 1] = pack_bf16x2(a, e);
         }
-        tmem_st16u(tS + 16 * c, pk);
+        tmem_st16u(tS + kHalf * half + 16 * c, pk);
       }
-      const uint64_t sa = f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3]));
+      tmem_wait_st();
+      tc_fence_before_sync();
+      mbar_arrive(&aux.p_full[g][half]);
+      const uint64_t sa = f2_add(sum2[0], sum2[1]);
       float rs0, rs1;
       f2_unpack(sa, rs0, rs1);
       l_run = l_run * alpha + (rs0 + rs1);
-      m_run = m_new;
-      tmem_wait_st();
-      tc_fence_before_sync();
-      mbar_arrive(&aux.p_full[g]);
     }
     if (ok && n > 0 && !__all_sync(~0u, mbar_wait(&aux.o_full[g], 0, P.limit))) {
-      if (lane == 0) fail();
+      fail();
       ok = false;
     }
-    ok = named_barrier_and(1 + g, kRows, ok);  // all rows of the tile agree before it is stored
+    aux.row[g][half][r] = l_run;
+    ok = named_barrier_and(1 + g, 2 * kRows, ok);  // all rows of the tile agree before it is stored
     if (ok) {
       tc_fence_after_sync();
+      l_run += aux.row[g][half ^ 1][r];
       const int Hq = P.Hk * P.G;
       const int t = (tile0 + g) * P.tokens + r / P.G, head = hk * P.G + r % P.G;
       const bool row = r < P.tokens * P.G && t < P.Tq;
@@ -389,9 +427,9 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const float inv = n > 0 ? 1.f / l_run : 0.f;
       if (P.nsplit > 1) {
         const long long at = (long long)split * P.rows + ((long long)b * P.Tq + t) * Hq + head;
-        if (row) P.part_lse[at] = lse;
+        if (row && half == 0) P.part_lse[at] = lse;
         if (n > 0) {
-          for (int c0 = 0; c0 < D; c0 += 16) {
+          for (int c0 = oc0; c0 < oc1; c0 += 16) {
             float o[16];
             tmem_ld16(tO + c0, o);
             tmem_wait_ld();
@@ -404,11 +442,11 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           }
         }
       } else {
-        if (row && P.lse) P.lse[((long long)b * Hq + head) * P.Tq + t] = lse;
+        if (row && half == 0 && P.lse) P.lse[((long long)b * Hq + head) * P.Tq + t] = lse;
         // every S MMA has completed (or none was issued and Q never loaded):
         // the tile's Q buffer takes its output
-        uint8_t* so = smem + L.q + g * L.tile + r * 128;
-        for (int c0 = 0; c0 < D; c0 += 16) {
+        uint8_t* so = smem + L::q + g * L::tile + r * 128;
+        for (int c0 = oc0; c0 < oc1; c0 += 16) {
           float o[16];
           if (n > 0) {
             tmem_ld16(tO + c0, o);
@@ -425,10 +463,10 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           *reinterpret_cast<uint4*>(blk + (((c + 1) ^ (r & 7)) << 4)) = pack8_bf16(o + 8);
         }
         fence_proxy_async_smem();
-        named_barrier(1 + g, kRows);
-        if (r == 0) {
+        named_barrier(1 + g, 2 * kRows);
+        if (r == 0 && half == 0) {
           for (int c = 0; c < nb; ++c)
-            tma_store_5d(&tm_out, smem + L.q + g * L.tile + c * kBlock, c * 64, 0, (tile0 + g) * P.tokens, hk, b);
+            tma_store_5d(&tm_out, smem + L::q + g * L::tile + c * kBlock, c * 64, 0, (tile0 + g) * P.tokens, hk, b);
           bulk_commit();
           bulk_wait_all();
         }
@@ -439,7 +477,7 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
-    tmem_dealloc(tm, kTileCols * kQTiles);
+    tmem_dealloc(aux.tmem, kTileCols * kQTiles);
   }
 }
 
@@ -500,6 +538,18 @@ void cross_shape(const CrossCall& c, CrossParams* P) {
   P->nsplit = std::max(1, (P->ntiles + P->per_split - 1) / P->per_split);
 }
 
+template <int NB>
+cudaError_t launch_nb(unsigned grid, cudaStream_t stream, const CUtensorMap& mq, const CUtensorMap& mk,
+                      const CUtensorMap& mv, const CUtensorMap& mo, const CrossParams& P) {
+  // more than half an SM's shared memory: one CTA (all of TMEM) per SM
+  constexpr int bytes = CrossLayout<NB>::total > 116 * 1024 ? CrossLayout<NB>::total : 116 * 1024;
+  const cudaError_t e = allow_smem(gdn_cross_kernel<NB>, bytes);
+  if (e != cudaSuccess) return e;
+  ProfileScope ps(stream, kKernCross);
+  gdn_cross_kernel<NB><<<grid, kThreads, bytes, stream>>>(mq, mk, mv, mo, P);
+  return cudaSuccess;
+}
+
 }  // namespace
 
 size_t cross_workspace_bytes(const CrossCall& c) {
@@ -536,29 +586,10 @@ cudaError_t launch_cross(const CrossCall& c, void* ws) {
                              c.v.token_stride, kRows)) {
     return cudaErrorInvalidValue;
   }
-  constexpr int kMaxDev = 64;
-  static std::mutex mu;
-  static bool done[kMaxDev] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!done[dev]) {
-      e = cudaFuncSetAttribute(gdn_cross_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)cross_layout(128).total);
-      if (e != cudaSuccess) return e;
-      done[dev] = true;
-    }
-  }
-  // more than half an SM's shared memory: one CTA (all of TMEM) per SM
-  const uint32_t smem = std::max(cross_layout(c.D).total, 116u * 1024);
   const unsigned grid = (unsigned)((long long)c.B * c.Hk * P.groups * P.nsplit);
-  {
-    ProfileScope ps(c.stream, kKernCross);
-    gdn_cross_kernel<<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, mo, P);
-  }
+  cudaError_t e = c.D > 64 ? launch_nb<2>(grid, c.stream, mq, mk, mv, mo, P)
+                           : launch_nb<1>(grid, c.stream, mq, mk, mv, mo, P);
+  if (e != cudaSuccess) return e;
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   count_launches(1);

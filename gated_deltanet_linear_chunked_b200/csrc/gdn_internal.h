@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "gdn.h"
 
 namespace gdn {
@@ -183,6 +185,26 @@ bool make_tile_map(CUtensorMap* m, const void* base, int nb, int T, int H, int D
 // and are not stored.
 bool make_heads_map(CUtensorMap* m, const void* base, int nb, int T, int Hk, int G, int D,
                     long long batch_stride, long long token_stride, int box_tokens);
+
+// Opts a kernel into `bytes` of dynamic shared memory, once per device.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes) {
+  constexpr int kMaxDev = 64;
+  static std::mutex mu;
+  static const void* seen[kMaxDev][4] = {};  // kernels of one type share this function
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+  const void* f = reinterpret_cast<const void*>(kernel);
+  std::lock_guard<std::mutex> lock(mu);
+  int i = 0;
+  while (i < 4 && seen[dev][i] && seen[dev][i] != f) ++i;
+  if (i < 4 && seen[dev][i]) return cudaSuccess;
+  const cudaError_t s = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (s == cudaSuccess && i < 4) seen[dev][i] = f;
+  return s;
+}
 
 // Streaming multiprocessors of the current device (cached per device).
 int num_sms();
