@@ -11,7 +11,8 @@ from . import workloads  # noqa: F401
 _API = ("chunk_fwd", "chunk_bidir", "chunk_fwd_logits", "chunk_bidir_logits",
         "chunk_fwd_backward", "chunk_bidir_backward", "sink_window_attention",
         "sink_window_cache", "sink_window_slot", "rope", "rope_backward", "rope_frequencies",
-        "qk_norm_rope", "qk_norm_rope_backward", "cross_attention", "state_reset",
+        "qk_norm_rope", "qk_norm_rope_backward", "cross_attention",
+        "cross_attention_backward", "state_reset",
         "device_error", "set_wait_limit", "set_time_segments", "workspace_release")
 __all__ = [*_API, "GDNError", "workloads"]
 

@@ -51,6 +51,8 @@ SIGNATURES = {
                                   [_vp] * 11 + [_i] * 5 + [ctypes.c_float, _i, _vp]),
     "gdn_cross_attention": (ctypes.c_int, [_vp] * 4 + [_ll] + [_vp] * 2 + [_i] * 6 +
                             [ctypes.c_float, _i, _vp]),
+    "gdn_cross_attention_backward": (ctypes.c_int, [_vp] * 4 + [_ll] + [_vp] * 6 + [_i] * 6 +
+                                     [ctypes.c_float, _i, _vp]),
     "gdn_state_reset": (ctypes.c_int, [_fp, _i, _i, _i, _i, _vp]),
     "gdn_device_error": (ctypes.c_int, [_vp]),
     "gdn_workspace_release": (ctypes.c_int, []),

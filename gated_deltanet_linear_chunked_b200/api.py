@@ -477,6 +477,27 @@ def cross_attention(q, k, v, key_mask=None, *, scale=None, out=None, return_lse=
     return (out, lse) if return_lse else out
 
 
+def cross_attention_backward(q, k, v, out, lse, d_out, key_mask=None, *, scale=None, stream=None):
+    """Gradients of ``cross_attention`` given its inputs, its results ``out`` and
+    ``lse`` and the gradient of ``out``: a dict with dq, dk and dv (bf16).  For k, v
+    expanded over the batch dk and dv hold each batch row's share."""
+    B, Tq, S, Hq, Hk, D, vq, vk, vv, mp, ms, scale = _cross_args(q, k, v, key_mask, scale)
+    dev = q.device
+    _check_tensor(out, "out", torch.bfloat16, (B, Tq, Hq, D))
+    _check_tensor(lse, "lse", torch.float32, (B, Hq, Tq))
+    _check_tensor(d_out, "d_out", torch.bfloat16, (B, Tq, Hq, D))
+    dq = _fresh(stream, torch.empty, (B, Tq, Hq, D), dtype=torch.bfloat16, device=dev)
+    dk = _fresh(stream, torch.empty, (B, S, Hk, D), dtype=torch.bfloat16, device=dev)
+    dv = _fresh(stream, torch.empty, (B, S, Hk, D), dtype=torch.bfloat16, device=dev)
+    st = _lib.load().gdn_cross_attention_backward(
+        vq, vk, vv, mp, ms, out.data_ptr(), lse.data_ptr(), d_out.data_ptr(), dq.data_ptr(),
+        dk.data_ptr(), dv.data_ptr(), B, Tq, S, Hq, Hk, D, scale, _lib.GDN_BF16,
+        _raw_stream(stream, dev))
+    _lib.check(st, "gdn_cross_attention_backward")
+    _used_on(stream, q, k, v, key_mask, out, lse, d_out, dq, dk, dv)
+    return {"dq": dq, "dk": dk, "dv": dv}
+
+
 def state_reset(state, stream=None):
     """Zero a state tensor [B,H,Dk,Dv] in place (streaming restart)."""
     _check_tensor(state, "state", torch.float32)

@@ -31,7 +31,7 @@ Range range_of_view(const gdn_rows& v, int B, int T, long long row) {
 
 struct Checked {
   CrossCall c;
-  Range reads[8];
+  Range reads[8];  // at most q, k, v, mask, out, d_out, lse
   int nreads;
   const void* ptrs[16];
   int nptrs;
@@ -133,6 +133,65 @@ gdn_status gdn_cross_attention(const gdn_rows* q, const gdn_rows* k, const gdn_r
   if (st != GDN_OK) return st;
   c.limit = current_wait_limit();
   const cudaError_t e = launch_cross(c, sc.p);
+  const cudaError_t f = op_scratch_done(sc);
+  return finish(c.stream, e == cudaSuccess ? f : e, c.err);
+}
+
+gdn_status gdn_cross_attention_backward(const gdn_rows* q, const gdn_rows* k, const gdn_rows* v,
+                                        const unsigned char* key_mask, long long mask_batch_stride,
+                                        const void* out, const float* lse, const void* d_out, void* dq,
+                                        void* dk, void* dv, int B, int Tq, int S, int Hq, int Hk, int D,
+                                        float scale, gdn_dtype dtype, void* stream) {
+  using namespace gdn;
+  Checked o;
+  gdn_status st = check_inputs(q, k, v, key_mask, mask_batch_stride, B, Tq, S, Hq, Hk, D, scale, dtype,
+                               stream, &o);
+  if (st != GDN_OK) return st;
+  const size_t qbytes = (size_t)B * Tq * Hq * D * 2, kbytes = (size_t)B * S * Hk * D * 2;
+  if (qbytes == 0 && kbytes == 0) return GDN_OK;
+  const size_t lbytes = (size_t)B * Tq * Hq * 4;
+  const struct {
+    const void* p;
+    size_t bytes;
+    bool written;
+  } bufs[] = {{out, qbytes, false}, {d_out, qbytes, false}, {lse, lbytes, false},
+              {dq, qbytes, true},   {dk, kbytes, true},     {dv, kbytes, true}};
+  for (const auto& x : bufs) {
+    if (x.bytes == 0) continue;
+    if (!x.p || !aligned16(x.p)) return GDN_ERR_INVALID_ARG;
+    if (!x.written) o.reads[o.nreads++] = range_of(x.p, x.bytes);
+    o.ptrs[o.nptrs++] = x.p;
+  }
+  for (int i = 3; i < 6; ++i) {
+    const Range w = range_of(bufs[i].p, bufs[i].bytes);
+    for (int r = 0; r < o.nreads; ++r)
+      if (overlaps(w, o.reads[r])) return GDN_ERR_ALIAS;
+    for (int x = i + 1; x < 6; ++x)
+      if (overlaps(w, range_of(bufs[x].p, bufs[x].bytes))) return GDN_ERR_ALIAS;
+  }
+  int dev = 0;
+  st = check_device(o, &dev);
+  if (st != GDN_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (qbytes == 0 || kbytes == 0) {  // nothing attends: what there is of gradients is zero
+    cudaError_t e = cudaSuccess;
+    if (qbytes) e = cudaMemsetAsync(dq, 0, qbytes, s);
+    if (kbytes) e = cudaMemsetAsync(dk, 0, kbytes, s);
+    if (kbytes && e == cudaSuccess) e = cudaMemsetAsync(dv, 0, kbytes, s);
+    return finish(s, e, nullptr);
+  }
+  CrossCall& c = o.c;
+  c.out = const_cast<void*>(out);
+  c.lse = const_cast<float*>(lse);
+  c.d_out = d_out;
+  c.dq = dq;
+  c.dk = dk;
+  c.dv = dv;
+  OpScratch sc;
+  st = op_scratch(dev, c.stream, cross_backward_workspace_bytes(c), &c.err, &sc);
+  if (st != GDN_OK) return st;
+  c.limit = current_wait_limit();
+  const cudaError_t e = launch_cross_backward(c, sc.p);
   const cudaError_t f = op_scratch_done(sc);
   return finish(c.stream, e == cudaSuccess ? f : e, c.err);
 }

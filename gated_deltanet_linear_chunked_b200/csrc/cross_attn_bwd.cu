@@ -1,0 +1,813 @@
+// cross_attn_bwd.cu -- gradients of the attention to the encoder's states.
+//
+//   P = e^(s - lse) (0 at masked keys),  delta = sum_f dO O,  dP = dO V^T,
+//   dS = P (dP - delta),  dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO,
+// the last two summed over the query heads of a key head as well: they are rows
+// of the same products, packed as in the forward (row = token * G + head).
+//
+// Two kernels instead of one over the same tiles.  One pass that makes all three
+// gradients needs five products per tile but has to add dQ (or dK and dV) up
+// across CTAs, by atomics, whose order changes the result, or through partial
+// sums of full size; two passes take seven products and every sum stays in a
+// CTA's TMEM, in a fixed order.
+//   gdn_cross_stat_kernel  (lse log2 e, delta) of every packed row; +inf for the
+//                  rows that are none (past the tokens, or with no key), for
+//                  which 2^(s - inf) = 0.
+//   gdn_cross_dq_kernel    a CTA per query tile walks the key tiles.
+//   gdn_cross_dkv_kernel   a CTA per key tile and share of the query tiles; the
+//                  products are transposed, S^T = K Q^T and dP^T = V dO^T, so that
+//                  a TMEM lane is a key, P^T and dS^T are left operands out of
+//                  TMEM, and dK and dV add up there.  gdn_cross_dkv_join_kernel
+//                  adds the shares up where there are several.
+// No maximum is searched and no row's threads meet: lse is known.  16 warps take
+// a 128 x 128 tile, 32 columns a thread; one warp copies, one issues products.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "gdn_internal.h"
+#include "sm100.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace sm100;
+
+constexpr int kRows = 128;
+constexpr int kCols = 32;               // columns of a softmax thread
+constexpr int kSoftmaxWarps = 16;
+constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
+constexpr int kProducerWarp = kSoftmaxWarps;
+constexpr int kMmaWarp = kProducerWarp + 1;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr uint32_t kBlock = kRows * 128;
+constexpr int kStages = 2;
+constexpr int kStatThreads = 256;
+constexpr long long kDrainPolls = 1LL << 40;
+
+struct BwdParams {
+  int Tq, S, Hk, G, D;
+  int tokens, qtiles, ntiles;   // tokens and tiles of queries, tiles of keys
+  int nsplit, per_split;        // dkv: shares of the query tiles, tiles of each
+  int qb, kb, vb;
+  const uint32_t* bits;         // under a mask: seen keys, [B][ntiles][4], one bit each
+  const int* list;              // ... and [B][ntiles + 1]: the tiles with any, their number last
+  float scale, scale_log2;
+  const float2* stat;           // [B * Hk][qtiles][128]
+  float* part;                  // nsplit > 1: [nsplit][2 (dk, dv)][B * Hk][ntiles][128][D]
+  long long part_rows;          // B * Hk * ntiles * 128
+  long long limit;
+  unsigned* err;
+};
+
+// The mask of batch row b as bits and as a list of the tiles with any seen key.
+// One block per batch row; the list is made by its first warp.
+__device__ void mask_lists(const uint8_t* mrow, int S, int ntiles, uint32_t* bits, int* list) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int w = warp; w < ntiles * 4; w += kStatThreads / 32) {
+    const long long key = (long long)w * 32 + lane;
+    const uint32_t x = __ballot_sync(~0u, key < S && mrow[key] != 0);
+    if (lane == 0) bits[w] = x;
+  }
+  __syncthreads();
+  if (warp) return;
+  int n = 0;
+  for (int t0 = 0; t0 < ntiles; t0 += 32) {
+    const int t = t0 + lane;
+    const bool any = t < ntiles && (bits[4 * t] | bits[4 * t + 1] | bits[4 * t + 2] | bits[4 * t + 3]) != 0;
+    const uint32_t bal = __ballot_sync(~0u, any);
+    if (any) list[n + __popc(bal & ((1u << lane) - 1))] = t;
+    n += __popc(bal);
+  }
+  if (lane == 0) list[ntiles] = n;
+}
+
+// The seen keys of tile t of batch row b, as four words.
+__device__ __forceinline__ uint4 seen_keys(const BwdParams& P, int b, int t) {
+  if (P.bits) return *reinterpret_cast<const uint4*>(P.bits + ((long long)b * P.ntiles + t) * 4);
+  const int left = P.S - t * kRows;
+  uint32_t w[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) w[c] = left >= 32 * (c + 1) ? ~0u : left <= 32 * c ? 0u : (1u << (left - 32 * c)) - 1;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint32_t word_of(const uint4& w, int c) {
+  return c == 0 ? w.x : c == 1 ? w.y : c == 2 ? w.z : w.w;
+}
+
+// ---------------------------------------------------------------- row stats
+// A warp per packed row: delta from 4 features a lane.  Under a mask, the last B
+// blocks turn the rows of the mask into bits and lists instead.
+__global__ void __launch_bounds__(kStatThreads)
+gdn_cross_stat_kernel(const __nv_bfloat16* out, const __nv_bfloat16* d_out, const float* lse, float2* stat,
+                      long long rows, unsigned row_blocks, const uint8_t* mask, long long mask_bs,
+                      const __grid_constant__ BwdParams P) {
+  if (blockIdx.x >= row_blocks) {
+    const int b = blockIdx.x - row_blocks;
+    mask_lists(mask + b * mask_bs, P.S, P.ntiles, const_cast<uint32_t*>(P.bits) + (long long)b * P.ntiles * 4,
+               const_cast<int*>(P.list) + (long long)b * (P.ntiles + 1));
+    return;
+  }
+  const int Tq = P.Tq, Hk = P.Hk, G = P.G, D = P.D, tokens = P.tokens, qtiles = P.qtiles;
+  const long long row = (long long)blockIdx.x * (kStatThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  const int r = (int)(row % kRows);
+  const long long tile = row / kRows, bh = tile / qtiles;
+  const int qt = (int)(tile - bh * qtiles), hk = (int)(bh % Hk);
+  const long long b = bh / Hk;
+  const int t = qt * tokens + r / G, head = hk * G + r % G;
+  float2 s = make_float2(INFINITY, 0.f);
+  if (r < tokens * G && t < Tq) {  // uniform over the warp
+    const int Hq = Hk * G;
+    const long long at = ((b * Tq + t) * Hq + head) * D + lane * 4;
+    float d = 0.f;
+    if (lane * 4 < D) {
+      float x[4], y[4];
+      const uint2 u = *reinterpret_cast<const uint2*>(out + at), v = *reinterpret_cast<const uint2*>(d_out + at);
+      unpack_bf16x2(u.x, x[0], x[1]);
+      unpack_bf16x2(u.y, x[2], x[3]);
+      unpack_bf16x2(v.x, y[0], y[1]);
+      unpack_bf16x2(v.y, y[2], y[3]);
+      d = x[0] * y[0] + x[1] * y[1] + (x[2] * y[2] + x[3] * y[3]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(~0u, d, o);
+    const float l = lse[(b * Hq + head) * Tq + t];
+    if (l > -INFINITY) s = make_float2(l * 1.4426950408889634f, d);
+  }
+  if (lane == 0) stat[row] = s;
+}
+
+// ----------------------------------------------------------------------- dQ
+// TMEM: S of even and odd key tiles [0, 128), [128, 256) (dS over them), dP
+// [256, 384), dQ [384, 384 + D).  With two S the product for the next tile runs
+// under this one's exponentials.
+struct DqAux {
+  uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages];
+  uint64_t s_full[2], dp_full, dp_free, ds_full[2], dq_full, drain;
+  uint32_t tmem;
+  int abort;
+};
+template <int NB>
+struct DqLayout {
+  static constexpr uint32_t tile = NB * kBlock;
+  static constexpr uint32_t q = 0, g = tile, k = 2 * tile, v = k + kStages * tile;
+  static constexpr uint32_t aux = v + kStages * tile;
+  static constexpr uint32_t total = aux + (uint32_t)sizeof(DqAux);
+};
+
+template <int NB>
+__global__ void __launch_bounds__(kThreads, 1)
+gdn_cross_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ BwdParams P) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  using L = DqLayout<NB>;
+  DqAux& aux = *reinterpret_cast<DqAux*>(smem + L::aux);
+  const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
+  const int qt = blockIdx.x % P.qtiles, bh = blockIdx.x / P.qtiles;
+  const int b = bh / P.Hk, hk = bh - b * P.Hk;
+  const int D = P.D;
+  volatile int* abort_flag = &aux.abort;
+  if (tid == 0) {
+    mbar_init(&aux.q_full, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&aux.k_full[s], 1);
+      mbar_init(&aux.k_empty[s], 1);
+      mbar_init(&aux.v_full[s], 1);
+    }
+    mbar_init(&aux.s_full[0], 1);
+    mbar_init(&aux.s_full[1], 1);
+    mbar_init(&aux.dp_full, 1);
+    mbar_init(&aux.dp_free, kSoftmaxThreads);
+    mbar_init(&aux.ds_full[0], kSoftmaxThreads);
+    mbar_init(&aux.ds_full[1], kSoftmaxThreads);
+    mbar_init(&aux.dq_full, 1);
+    mbar_init(&aux.drain, 1);
+    aux.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&aux.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  constexpr uint32_t tm = 0;  // all 512 columns: the allocation starts at the first
+  constexpr uint32_t tDP = tm + 256, tDQ = tm + 384;
+  const int* list = P.bits ? P.list + (long long)b * (P.ntiles + 1) : nullptr;
+  const int n = list ? list[P.ntiles] : P.ntiles;
+  auto fail = [&]() {
+    *abort_flag = 1;
+    atomicOr(P.err, kErrTimeout);
+  };
+
+  if (warp == kProducerWarp) {
+    if (lane == 0 && n > 0) {
+      const uint32_t bytes = (uint32_t)P.tokens * P.G * 128 * NB;
+      mbar_arrive_expect_tx(&aux.q_full, 2 * bytes);
+      for (int c = 0; c < NB; ++c) {
+        tma_load_5d(smem + L::q + c * kBlock, &tm_q, &aux.q_full, c * 64, 0, qt * P.tokens, hk, b * P.qb);
+        tma_load_5d(smem + L::g + c * kBlock, &tm_do, &aux.q_full, c * 64, 0, qt * P.tokens, hk, b);
+      }
+      int j = 0;
+      for (; j < n; ++j) {
+        if (*abort_flag) break;
+        const int s = j % kStages, t = list ? list[j] : j;
+        const uint32_t ph = (j / kStages - 1) & 1;
+        if (j >= kStages && !mbar_wait(&aux.k_empty[s], ph, P.limit)) {
+          fail();
+          break;
+        }
+        mbar_arrive_expect_tx(&aux.k_full[s], L::tile);
+        for (int c = 0; c < NB; ++c)
+          tma_load_5d(smem + L::k + s * L::tile + c * kBlock, &tm_k, &aux.k_full[s], c * 64, 0, t * kRows, hk,
+                      b * P.kb);
+        // (dP of tile j - 2, V's reader, came before its dQ, K's last one)
+        mbar_arrive_expect_tx(&aux.v_full[s], L::tile);
+        for (int c = 0; c < NB; ++c)
+          tma_load_5d(smem + L::v + s * L::tile + c * kBlock, &tm_v, &aux.v_full[s], c * 64, 0, t * kRows, hk,
+                      b * P.vb);
+      }
+      // every load has landed before shared memory goes
+      mbar_wait(&aux.q_full, 0, kDrainPolls);
+      for (int i = max(0, j - kStages); i < j; ++i) {
+        mbar_wait(&aux.k_full[i % kStages], (i / kStages) & 1, kDrainPolls);
+        mbar_wait(&aux.v_full[i % kStages], (i / kStages) & 1, kDrainPolls);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    const uint32_t idS = idesc_bf16(kRows, kRows, 0, 0), idQ = idesc_bf16(kRows, D, 0, 1);
+    const uint64_t dq = sdesc_sw128(smem_u32(smem + L::q), 16), dg = sdesc_sw128(smem_u32(smem + L::g), 16);
+    const uint64_t dk = sdesc_sw128(smem_u32(smem + L::k), 16), dv = sdesc_sw128(smem_u32(smem + L::v), 16);
+    const uint64_t dkn = sdesc_sw128(smem_u32(smem + L::k), kBlock);
+    auto all = [&](uint64_t* bar, uint32_t ph) { return __all_sync(~0u, mbar_wait(bar, ph, P.limit)); };
+    // rows of A times rows of B over the features, both K-major
+    auto product = [&](uint32_t d, uint64_t a, uint64_t bb) {
+#pragma unroll
+      for (int ks = 0; ks < 4 * NB; ++ks) {
+        const uint32_t at = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
+        if (ks < D / 16) mma_bf16_elect(d, a + at, bb + at, idS, ks > 0);
+      }
+    };
+    auto issue_s = [&](int j) {
+      const int s = j % kStages;
+      if (!all(&aux.k_full[s], (j / kStages) & 1)) return false;
+      tc_fence_after_sync();
+      product(tm + (j & 1) * 128, dq, dk + (s * L::tile >> 4));
+      mma_commit_elect(&aux.s_full[j & 1]);
+      return true;
+    };
+    auto issue_dp = [&](int j) {
+      const int s = j % kStages;
+      if (!all(&aux.v_full[s], (j / kStages) & 1)) return false;
+      if (j > 0 && !all(&aux.dp_free, (j - 1) & 1)) return false;
+      tc_fence_after_sync();
+      product(tDP, dg, dv + (s * L::tile >> 4));
+      mma_commit_elect(&aux.dp_full);
+      return true;
+    };
+    bool ok = true;
+    if (n > 0) ok = all(&aux.q_full, 0) && issue_s(0) && issue_dp(0);
+    for (int j = 0; ok && j < n; ++j) {
+      if (j + 1 < n) ok = issue_s(j + 1) && issue_dp(j + 1);
+      ok = ok && all(&aux.ds_full[j & 1], (j >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after_sync();
+      // dQ += dS K: dS in TMEM (8 columns per 16 keys, 32 keys over their own
+      // scores' columns), K MN-major
+      const int s = j % kStages;
+#pragma unroll
+      for (int ks = 0; ks < kRows / 16; ++ks)
+        mma_bf16_ts_elect(tDQ, tm + (j & 1) * 128 + (ks >> 1) * 32 + (ks & 1) * 8,
+                          dkn + ((s * L::tile + ks * 2048) >> 4), idQ, j > 0 || ks > 0);
+      mma_commit_elect(&aux.k_empty[s]);
+    }
+    if (!ok && lane == 0) fail();
+    mma_commit_elect(&aux.dq_full);
+    mma_commit_elect(&aux.drain);
+    mbar_wait(&aux.drain, 0, kDrainPolls);
+    __syncwarp();
+  } else {
+    const int r = (warp & 3) * 32 + lane, cg = warp >> 2;  // row; columns [32 cg, 32 cg + 32)
+    const uint32_t trow = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    const float2 st = P.stat[((long long)bh * P.qtiles + qt) * kRows + r];
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const uint4 keys = seen_keys(P, b, list ? list[j] : j);
+      if (!__all_sync(~0u, *abort_flag == 0 && mbar_wait(&aux.s_full[j & 1], (j >> 1) & 1, P.limit))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t ts = trow + (j & 1) * 128 + kCols * cg;
+      const uint32_t seen = word_of(keys, cg);
+      float p[kCols], dp[kCols];
+      tmem_ld32(ts, p);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) p[i] = ex2_approx(fmaf(p[i], P.scale_log2, -st.x));
+      if (!__all_sync(~0u, mbar_wait(&aux.dp_full, j & 1, P.limit))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      tmem_ld32(trow + tDP + kCols * cg, dp);
+      tmem_wait_ld();
+      tc_fence_before_sync();
+      mbar_arrive(&aux.dp_free);
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) p[i] *= dp[i] - st.y;
+      if (seen != ~0u) {
+#pragma unroll
+        for (int i = 0; i < kCols; ++i)
+          if (!(seen >> i & 1)) p[i] = 0.f;
+      }
+      uint32_t pk[kCols / 2];
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) pk[i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
+      tmem_st16u(ts, pk);
+      if (P.bits && (keys.x & keys.y & keys.z & keys.w) != ~0u) {
+        // clear the masked rows of K (its product with Q is done): 0 * NaN would reach dQ
+        const int key = tid >> 2, part = tid & 3;  // four threads a row
+        if (!(word_of(keys, key >> 5) >> (key & 31) & 1)) {
+          uint8_t* row = smem + L::k + (j % kStages) * L::tile + key * 128 + part * 32;
+#pragma unroll
+          for (int c = 0; c < NB; ++c) {
+            *reinterpret_cast<uint4*>(row + c * kBlock) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(row + c * kBlock + 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();
+      }
+      tmem_wait_st();
+      tc_fence_before_sync();
+      mbar_arrive(&aux.ds_full[j & 1]);
+    }
+    if (ok && !__all_sync(~0u, mbar_wait(&aux.dq_full, 0, P.limit))) ok = false;
+    if (!ok && lane == 0) fail();
+    ok = named_barrier_and(1, kSoftmaxThreads, ok && *abort_flag == 0);
+    if (ok) {
+      tc_fence_after_sync();
+      // every product has completed: Q's buffer takes dQ
+      uint8_t* so = smem + L::q + r * 128;
+      for (int c0 = kCols * cg; c0 < min(D, kCols * (cg + 1)); c0 += 16) {
+        float o[16];
+        if (n > 0) {
+          tmem_ld16(trow + tDQ + c0, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] *= P.scale;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = 0.f;
+        }
+        uint8_t* blk = so + (c0 >> 6) * kBlock;
+        const int c = (c0 & 63) >> 3;
+        *reinterpret_cast<uint4*>(blk + ((c ^ (r & 7)) << 4)) = pack8_bf16(o);
+        *reinterpret_cast<uint4*>(blk + (((c + 1) ^ (r & 7)) << 4)) = pack8_bf16(o + 8);
+      }
+      fence_proxy_async_smem();
+      named_barrier(1, kSoftmaxThreads);
+      if (tid == 0) {
+        for (int c = 0; c < NB; ++c)
+          tma_store_5d(&tm_dq, smem + L::q + c * kBlock, c * 64, 0, qt * P.tokens, hk, b);
+        bulk_commit();
+        bulk_wait_all();
+      }
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(aux.tmem, 512);
+  }
+}
+
+// -------------------------------------------------------------------- dK, dV
+// TMEM: S^T [0, 128) (P^T over it), dP^T [128, 256) (dS^T over it), dV
+// [256, 256 + D), dK [384, 384 + D).  P^T is handed on before dP^T is looked at:
+// dV += P^T dO and the next S^T run under the second half of the softmax, and
+// dK += dS^T Q and the next dP^T under the first half of the next.
+struct DkvAux {
+  uint64_t kv_full, q_full[kStages], q_empty[kStages];
+  uint64_t s_full, p_full, dp_full, ds_full, out_full, drain;
+  uint32_t tmem;
+  int abort;
+  __align__(16) float2 stat[kStages][kRows];
+};
+template <int NB>
+struct DkvLayout {
+  static constexpr uint32_t tile = NB * kBlock;
+  static constexpr uint32_t k = 0, v = tile, q = 2 * tile, g = q + kStages * tile;
+  static constexpr uint32_t aux = g + kStages * tile;
+  static constexpr uint32_t total = aux + (uint32_t)sizeof(DkvAux);
+};
+
+template <int NB>
+__global__ void __launch_bounds__(kThreads, 1)
+gdn_cross_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
+                     const __grid_constant__ BwdParams P) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  using L = DkvLayout<NB>;
+  DkvAux& aux = *reinterpret_cast<DkvAux*>(smem + L::aux);
+  const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
+  // unit: ((b * Hk + hk) * ntiles + tile) * nsplit + split
+  const int split = blockIdx.x % P.nsplit, u = blockIdx.x / P.nsplit;
+  const int kt = u % P.ntiles, bh = u / P.ntiles;
+  const int b = bh / P.Hk, hk = bh - b * P.Hk;
+  const int i0 = split * P.per_split, i1 = min(P.qtiles, i0 + P.per_split);
+  const int D = P.D;
+  volatile int* abort_flag = &aux.abort;
+  if (tid == 0) {
+    mbar_init(&aux.kv_full, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&aux.q_full[s], 1);
+      mbar_init(&aux.q_empty[s], 1);
+    }
+    mbar_init(&aux.s_full, 1);
+    mbar_init(&aux.p_full, kSoftmaxThreads);
+    mbar_init(&aux.dp_full, 1);
+    mbar_init(&aux.ds_full, kSoftmaxThreads);
+    mbar_init(&aux.out_full, 1);
+    mbar_init(&aux.drain, 1);
+    aux.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&aux.tmem, 512);
+    tmem_relinquish();
+  }
+  const uint4 keys = seen_keys(P, b, kt);
+  // rows of Q and dO past the packed ones are never loaded, and a product runs
+  // over them: they have to be numbers
+  for (int i = P.tokens * P.G * 8 + tid; i < kRows * 8; i += kThreads)
+    for (int c = 0; c < 2 * kStages * NB; ++c)
+      *reinterpret_cast<uint4*>(smem + L::q + c * kBlock + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  constexpr uint32_t tm = 0;
+  constexpr uint32_t tDP = tm + 128, tDV = tm + 256, tDK = tm + 384;
+  const bool any = (keys.x | keys.y | keys.z | keys.w) != 0;
+  const int n = any ? i1 - i0 : 0;
+  auto fail = [&]() {
+    *abort_flag = 1;
+    atomicOr(P.err, kErrTimeout);
+  };
+
+  if (warp == kProducerWarp) {
+    if (lane == 0 && n > 0) {
+      mbar_arrive_expect_tx(&aux.kv_full, 2 * L::tile);
+      for (int c = 0; c < NB; ++c) {
+        tma_load_5d(smem + L::k + c * kBlock, &tm_k, &aux.kv_full, c * 64, 0, kt * kRows, hk, b * P.kb);
+        tma_load_5d(smem + L::v + c * kBlock, &tm_v, &aux.kv_full, c * 64, 0, kt * kRows, hk, b * P.vb);
+      }
+      const uint32_t bytes = (uint32_t)P.tokens * P.G * 128 * NB;
+      int i = 0;
+      for (; i < n; ++i) {
+        if (*abort_flag) break;
+        const int s = i % kStages, qt = i0 + i;
+        if (i >= kStages && !mbar_wait(&aux.q_empty[s], (i / kStages - 1) & 1, P.limit)) {
+          fail();
+          break;
+        }
+        uint64_t* bar = &aux.q_full[s];
+        mbar_arrive_expect_tx(bar, 2 * bytes + kRows * (uint32_t)sizeof(float2));
+        for (int c = 0; c < NB; ++c)
+          tma_load_5d(smem + L::q + s * L::tile + c * kBlock, &tm_q, bar, c * 64, 0, qt * P.tokens, hk, b * P.qb);
+        for (int c = 0; c < NB; ++c)
+          tma_load_5d(smem + L::g + s * L::tile + c * kBlock, &tm_do, bar, c * 64, 0, qt * P.tokens, hk, b);
+        bulk_load(aux.stat[s], P.stat + ((long long)bh * P.qtiles + qt) * kRows, kRows * sizeof(float2), bar);
+      }
+      mbar_wait(&aux.kv_full, 0, kDrainPolls);
+      for (int x = max(0, i - kStages); x < i; ++x)
+        mbar_wait(&aux.q_full[x % kStages], (x / kStages) & 1, kDrainPolls);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    if (n > 0) {
+      const uint32_t idS = idesc_bf16(kRows, kRows, 0, 0), idO = idesc_bf16(kRows, D, 0, 1);
+      const uint64_t dk = sdesc_sw128(smem_u32(smem + L::k), 16), dv = sdesc_sw128(smem_u32(smem + L::v), 16);
+      const uint64_t dq = sdesc_sw128(smem_u32(smem + L::q), 16), dg = sdesc_sw128(smem_u32(smem + L::g), 16);
+      const uint64_t dqn = sdesc_sw128(smem_u32(smem + L::q), kBlock);
+      const uint64_t dgn = sdesc_sw128(smem_u32(smem + L::g), kBlock);
+      auto all = [&](uint64_t* bar, uint32_t ph) { return __all_sync(~0u, mbar_wait(bar, ph, P.limit)); };
+      auto product = [&](uint32_t d, uint64_t a, uint64_t bb) {  // over the features, both K-major
+#pragma unroll
+        for (int ks = 0; ks < 4 * NB; ++ks) {
+          const uint32_t at = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
+          if (ks < D / 16) mma_bf16_elect(d, a + at, bb + at, idS, ks > 0);
+        }
+      };
+      auto add = [&](uint32_t d, uint32_t a, uint64_t bb, bool more) {  // over the queries, A in TMEM
+#pragma unroll
+        for (int ks = 0; ks < kRows / 16; ++ks)
+          mma_bf16_ts_elect(d, a + (ks >> 1) * 32 + (ks & 1) * 8, bb + ks * (2048 >> 4), idO, more || ks > 0);
+      };
+      bool ok = all(&aux.kv_full, 0) && all(&aux.q_full[0], 0);
+      if (ok) {
+        tc_fence_after_sync();
+        product(tm, dk, dq);
+        mma_commit_elect(&aux.s_full);
+        product(tDP, dv, dg);
+        mma_commit_elect(&aux.dp_full);
+      }
+      for (int i = 0; ok && i < n; ++i) {
+        const uint32_t at = (i % kStages) * (L::tile >> 4), nx = ((i + 1) % kStages) * (L::tile >> 4);
+        ok = all(&aux.p_full, i & 1);
+        if (!ok) break;
+        tc_fence_after_sync();
+        add(tDV, tm, dgn + at, i > 0);
+        if (i + 1 < n) {
+          ok = all(&aux.q_full[(i + 1) % kStages], ((i + 1) / kStages) & 1);
+          if (!ok) break;
+          tc_fence_after_sync();
+          product(tm, dk, dq + nx);
+          mma_commit_elect(&aux.s_full);
+        }
+        ok = all(&aux.ds_full, i & 1);
+        if (!ok) break;
+        tc_fence_after_sync();
+        add(tDK, tDP, dqn + at, i > 0);
+        mma_commit_elect(&aux.q_empty[i % kStages]);
+        if (i + 1 < n) {
+          product(tDP, dv, dg + nx);
+          mma_commit_elect(&aux.dp_full);
+        }
+      }
+      if (!ok && lane == 0) fail();
+      mma_commit_elect(&aux.out_full);
+      mma_commit_elect(&aux.drain);
+      mbar_wait(&aux.drain, 0, kDrainPolls);
+    }
+    __syncwarp();
+  } else {
+    const int r = (warp & 3) * 32 + lane, cg = warp >> 2;  // key; queries [32 cg, 32 cg + 32)
+    const uint32_t trow = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    const bool seen = word_of(keys, warp & 3) >> lane & 1;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      if (!__all_sync(~0u, *abort_flag == 0 && mbar_wait(&aux.s_full, i & 1, P.limit))) {
+        ok = false;
+        break;
+      }
+      // (the product that filled S^T waited for this stage's rows and stats)
+      tc_fence_after_sync();
+      const int s = i % kStages;
+      const float4* st = reinterpret_cast<const float4*>(aux.stat[s] + kCols * cg);
+      float p[kCols], dp[kCols];
+      uint32_t pk[kCols / 2];
+      tmem_ld32(trow + kCols * cg, p);
+      tmem_wait_ld();
+      mbar_wait(&aux.q_full[s], (i / kStages) & 1, 2);  // the stats' bytes, landed already
+#pragma unroll
+      for (int c = 0; c < kCols / 2; ++c) {
+        const float4 x = st[c];
+        p[2 * c] = seen ? ex2_approx(fmaf(p[2 * c], P.scale_log2, -x.x)) : 0.f;
+        p[2 * c + 1] = seen ? ex2_approx(fmaf(p[2 * c + 1], P.scale_log2, -x.z)) : 0.f;
+        pk[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+      }
+      tmem_st16u(trow + kCols * cg, pk);
+      tmem_wait_st();
+      tc_fence_before_sync();
+      mbar_arrive(&aux.p_full);
+      if (!__all_sync(~0u, mbar_wait(&aux.dp_full, i & 1, P.limit))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      tmem_ld32(trow + tDP + kCols * cg, dp);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < kCols / 2; ++c) {
+        const float4 x = st[c];
+        const float a = seen ? p[2 * c] * (dp[2 * c] - x.y) : 0.f;
+        const float e = seen ? p[2 * c + 1] * (dp[2 * c + 1] - x.w) : 0.f;
+        pk[c] = pack_bf16x2(a, e);
+      }
+      tmem_st16u(trow + tDP + kCols * cg, pk);
+      tmem_wait_st();
+      tc_fence_before_sync();
+      mbar_arrive(&aux.ds_full);
+    }
+    if (ok && n > 0 && !__all_sync(~0u, mbar_wait(&aux.out_full, 0, P.limit))) ok = false;
+    if (!ok && lane == 0) fail();
+    ok = named_barrier_and(1, kSoftmaxThreads, ok && *abort_flag == 0);
+    if (ok) {
+      tc_fence_after_sync();
+      // dK, then dV: to the share's part, or as bf16 over K and V (all products done)
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        const float mul = which ? 1.f : P.scale;
+        const uint32_t src = trow + (which ? tDV : tDK);
+        for (int c0 = kCols * cg; c0 < min(D, kCols * (cg + 1)); c0 += 16) {
+          float o[16];
+          if (n > 0) {
+            tmem_ld16(src + c0, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] *= mul;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = 0.f;
+          }
+          if (P.nsplit > 1) {
+            const long long row = ((long long)bh * P.ntiles + kt) * kRows + r;
+            float4* to = reinterpret_cast<float4*>(
+                P.part + ((2 * split + which) * P.part_rows + row) * D + c0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) to[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else {
+            uint8_t* blk = smem + which * L::tile + r * 128 + (c0 >> 6) * kBlock;
+            const int c = (c0 & 63) >> 3;
+            *reinterpret_cast<uint4*>(blk + ((c ^ (r & 7)) << 4)) = pack8_bf16(o);
+            *reinterpret_cast<uint4*>(blk + (((c + 1) ^ (r & 7)) << 4)) = pack8_bf16(o + 8);
+          }
+        }
+      }
+      if (P.nsplit == 1) {
+        fence_proxy_async_smem();
+        named_barrier(1, kSoftmaxThreads);
+        if (tid == 0) {
+          for (int c = 0; c < NB; ++c) {
+            tma_store_5d(&tm_dk, smem + L::k + c * kBlock, c * 64, 0, kt * kRows, hk, b);
+            tma_store_5d(&tm_dv, smem + L::v + c * kBlock, c * 64, 0, kt * kRows, hk, b);
+          }
+          bulk_commit();
+          bulk_wait_all();
+        }
+      }
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(aux.tmem, 512);
+  }
+}
+
+// dK, dV = the sum of the shares, in their order.  A thread per four features.
+__global__ void __launch_bounds__(256)
+gdn_cross_dkv_join_kernel(const float* part, long long part_rows, int nsplit, int S, int Hk, int ntiles, int D,
+                          long long total, __nv_bfloat16* dk, __nv_bfloat16* dv) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= total) return;
+  const int q = D / 4;
+  const long long row = i / q;  // ((b * S) + s) * Hk + hk
+  const int f = (int)(i - row * q) * 4, hk = (int)(row % Hk), s = (int)(row / Hk % S);
+  const long long b = row / Hk / S;
+  const long long prow = (b * Hk + hk) * ntiles * kRows + s;
+  const int which = blockIdx.y;
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int x = 0; x < nsplit; ++x) {
+    const float4 v = *reinterpret_cast<const float4*>(part + ((2 * x + which) * part_rows + prow) * D + f);
+    o[0] += v.x;
+    o[1] += v.y;
+    o[2] += v.z;
+    o[3] += v.w;
+  }
+  __nv_bfloat16* to = which ? dv : dk;
+  *reinterpret_cast<uint2*>(to + row * D + f) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+}
+
+void bwd_shape(const CrossCall& c, BwdParams* P) {
+  P->Tq = c.Tq;
+  P->S = c.S;
+  P->Hk = c.Hk;
+  P->G = c.Hq / c.Hk;
+  P->D = c.D;
+  P->tokens = kRows / P->G;
+  P->qtiles = (c.Tq + P->tokens - 1) / P->tokens;
+  P->ntiles = (c.S + kRows - 1) / kRows;
+  P->part_rows = (long long)c.B * c.Hk * P->ntiles * kRows;
+  // Shares of the query tiles: the fewest tile steps over all waves of CTAs,
+  // a CTA's start and end counting as three steps and a share's fp32 part as two.
+  const long long units = (long long)c.B * c.Hk * P->ntiles;
+  const int sms = num_sms();
+  double best = 1e300;
+  P->nsplit = 1;
+  for (int s = 1; s <= 16 && s <= P->qtiles; ++s) {
+    const long long waves = (units * s + sms - 1) / sms;
+    const double cost = (double)waves * ((P->qtiles + s - 1) / s + 3 + (s > 1 ? 2 : 0));
+    if (cost < best) {
+      best = cost;
+      P->nsplit = s;
+    }
+  }
+  P->per_split = (P->qtiles + P->nsplit - 1) / P->nsplit;
+  P->nsplit = (P->qtiles + P->per_split - 1) / P->per_split;
+}
+
+// Scratch: the row stats, under a mask its bits and lists, then the shares' parts.
+struct BwdScratch {
+  size_t bits, list, part, total;
+};
+BwdScratch bwd_scratch(const CrossCall& c, const BwdParams& P) {
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  BwdScratch s;
+  s.bits = up((size_t)c.B * c.Hk * P.qtiles * kRows * sizeof(float2));
+  s.list = s.bits + (c.mask ? up((size_t)c.B * P.ntiles * 4 * sizeof(uint32_t)) : 0);
+  s.part = s.list + (c.mask ? up((size_t)c.B * (P.ntiles + 1) * sizeof(int)) : 0);
+  s.total = s.part + (P.nsplit > 1 ? (size_t)2 * P.nsplit * P.part_rows * c.D * sizeof(float) : 0);
+  return s;
+}
+
+template <int NB>
+cudaError_t launch_nb(const CrossCall& c, const BwdParams& P, const CUtensorMap& mq, const CUtensorMap& mg,
+                      const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdq,
+                      const CUtensorMap& mdk, const CUtensorMap& mdv) {
+  // more than half an SM's shared memory: one CTA (all of TMEM) per SM
+  constexpr int dq_bytes = DqLayout<NB>::total > 116 * 1024 ? DqLayout<NB>::total : 116 * 1024;
+  constexpr int dkv_bytes = DkvLayout<NB>::total > 116 * 1024 ? DkvLayout<NB>::total : 116 * 1024;
+  cudaError_t e = allow_smem(gdn_cross_dq_kernel<NB>, dq_bytes);
+  if (e == cudaSuccess) e = allow_smem(gdn_cross_dkv_kernel<NB>, dkv_bytes);
+  if (e != cudaSuccess) return e;
+  {
+    ProfileScope ps(c.stream, kKernCrossDq);
+    gdn_cross_dq_kernel<NB><<<(unsigned)(c.B * c.Hk * P.qtiles), kThreads, dq_bytes, c.stream>>>(mq, mg, mk, mv,
+                                                                                               mdq, P);
+  }
+  {
+    ProfileScope ps(c.stream, kKernCrossDkv);
+    gdn_cross_dkv_kernel<NB><<<(unsigned)(c.B * c.Hk * P.ntiles * P.nsplit), kThreads, dkv_bytes, c.stream>>>(
+        mq, mg, mk, mv, mdk, mdv, P);
+  }
+  e = cudaGetLastError();
+  if (e == cudaSuccess) count_launches(2);
+  return e;
+}
+
+}  // namespace
+
+size_t cross_backward_workspace_bytes(const CrossCall& c) {
+  BwdParams P = {};
+  bwd_shape(c, &P);
+  return bwd_scratch(c, P).total;
+}
+
+cudaError_t launch_cross_backward(const CrossCall& c, void* ws) {
+  BwdParams P = {};
+  bwd_shape(c, &P);
+  const BwdScratch at = bwd_scratch(c, P);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  P.bits = c.mask ? reinterpret_cast<const uint32_t*>(base + at.bits) : nullptr;
+  P.list = c.mask ? reinterpret_cast<const int*>(base + at.list) : nullptr;
+  P.scale = c.scale;
+  P.scale_log2 = c.scale * 1.4426950408889634f;
+  P.stat = static_cast<const float2*>(ws);
+  P.part = reinterpret_cast<float*>(base + at.part);
+  P.limit = c.limit;
+  P.err = c.err;
+  P.qb = c.q.batch_stride != 0;
+  P.kb = c.k.batch_stride != 0;
+  P.vb = c.v.batch_stride != 0;
+  CUtensorMap mq, mg, mk, mv, mdq, mdk, mdv;
+  const long long ots = (long long)c.Hq * c.D, kts = (long long)c.Hk * c.D;
+  if (!make_heads_map(&mq, c.q.data, P.qb ? c.B : 1, c.Tq, c.Hk, P.G, c.D, c.q.batch_stride, c.q.token_stride,
+                      P.tokens) ||
+      !make_heads_map(&mg, c.d_out, c.B, c.Tq, c.Hk, P.G, c.D, c.Tq * ots, ots, P.tokens) ||
+      !make_heads_map(&mk, c.k.data, P.kb ? c.B : 1, c.S, c.Hk, 1, c.D, c.k.batch_stride, c.k.token_stride,
+                      kRows) ||
+      !make_heads_map(&mv, c.v.data, P.vb ? c.B : 1, c.S, c.Hk, 1, c.D, c.v.batch_stride, c.v.token_stride,
+                      kRows) ||
+      !make_heads_map(&mdq, c.dq, c.B, c.Tq, c.Hk, P.G, c.D, c.Tq * ots, ots, P.tokens) ||
+      !make_heads_map(&mdk, c.dk, c.B, c.S, c.Hk, 1, c.D, c.S * kts, kts, kRows) ||
+      !make_heads_map(&mdv, c.dv, c.B, c.S, c.Hk, 1, c.D, c.S * kts, kts, kRows))
+    return cudaErrorInvalidValue;
+  const long long rows = (long long)c.B * c.Hk * P.qtiles * kRows;
+  {
+    ProfileScope ps(c.stream, kKernCrossStat);
+    const unsigned blocks = (unsigned)((rows + kStatThreads / 32 - 1) / (kStatThreads / 32));
+    gdn_cross_stat_kernel<<<blocks + (c.mask ? c.B : 0), kStatThreads, 0, c.stream>>>(
+        static_cast<const __nv_bfloat16*>(c.out), static_cast<const __nv_bfloat16*>(c.d_out), c.lse,
+        static_cast<float2*>(ws), rows, blocks, c.mask, c.mask_bs, P);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  count_launches(1);
+  e = c.D > 64 ? launch_nb<2>(c, P, mq, mg, mk, mv, mdq, mdk, mdv)
+               : launch_nb<1>(c, P, mq, mg, mk, mv, mdq, mdk, mdv);
+  if (e != cudaSuccess || P.nsplit == 1) return e;
+  ProfileScope ps(c.stream, kKernCrossDkvJoin);
+  const long long total = (long long)c.B * c.S * c.Hk * (c.D / 4);
+  gdn_cross_dkv_join_kernel<<<dim3((unsigned)((total + 255) / 256), 2), 256, 0, c.stream>>>(
+      P.part, P.part_rows, P.nsplit, c.S, c.Hk, P.ntiles, c.D, total, static_cast<__nv_bfloat16*>(c.dk),
+      static_cast<__nv_bfloat16*>(c.dv));
+  e = cudaGetLastError();
+  if (e == cudaSuccess) count_launches(1);
+  return e;
+}
+
+}  // namespace gdn

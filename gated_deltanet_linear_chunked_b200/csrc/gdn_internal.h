@@ -74,7 +74,8 @@ enum KernelId : int {
   kKernCrossDq = 16,
   kKernCrossDkv = 17,
   kKernCrossDkvJoin = 18,
-  kNumKernelIds = 19,
+  kKernCrossStat = 19,
+  kNumKernelIds = 20,
 };
 
 // While profiling is armed, records CUDA events around one launch.

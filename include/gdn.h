@@ -428,6 +428,23 @@ GDN_API gdn_status gdn_cross_attention(const gdn_rows* q, const gdn_rows* k, con
                                        int D, float scale, gdn_dtype dtype, void* stream);
 
 /*
+ * Gradients of gdn_cross_attention, given its arguments, its results out and lse
+ * and the gradient d_out of out (contiguous, as out): dq [B, Tq, Hq, D], dk, dv
+ * [B, S, Hk, D], contiguous bf16, every element written; those of masked keys and
+ * of rows that see none are 0.  Products of bf16 operands (P and dS rounded to
+ * bf16) with fp32 sums, taken in a fixed order: the same call gives the same bits.
+ * For states that the batch shares (batch stride 0) dk and dv hold each batch
+ * row's share.  dq, dk, dv overlap nothing.  Requirements, errors and scratch as
+ * for gdn_cross_attention.
+ */
+GDN_API gdn_status gdn_cross_attention_backward(const gdn_rows* q, const gdn_rows* k, const gdn_rows* v,
+                                                const unsigned char* key_mask,
+                                                long long mask_batch_stride, const void* out,
+                                                const float* lse, const void* d_out, void* dq, void* dk,
+                                                void* dv, int B, int Tq, int S, int Hq, int Hk, int D,
+                                                float scale, gdn_dtype dtype, void* stream);
+
+/*
  * Time segments of the bf16 path's recurrence.  The stage that walks the
  * chunks is a dependent chain of ceil(T / 64) steps per (head, 16 state
  * columns).  When a call has too few such chains to fill the GPU and many
@@ -465,7 +482,8 @@ GDN_API unsigned long long gdn_launch_count(void);
  * reduction, 7 the sink + window attention, 8 / 9 / 10 the chunked
  * backward's pre, chain and gradient passes, 11 / 12 / 13 the norm and rotary
  * pass, its gradients and their reduction, 14 / 15 the cross attention and the
- * join of its splits; names from gdn_kernel_name.  Not thread-safe against concurrent calls on other
+ * join of its splits, 16 / 17 / 18 / 19 its dq, its dk and dv, the join of their
+ * shares and the row statistics; names from gdn_kernel_name.  Not thread-safe against concurrent calls on other
  * threads; meant for benchmarks.
  */
 GDN_API gdn_status gdn_profile_begin(int max_launches);

@@ -8,6 +8,12 @@ Tolerances, element by element, with u = 2^-24 and h = 2^-8 (half a step of bf16
 * out: (h + 8e-5 + 2 d) sum p |v| from P and the row sum, and h |out| from the
   rounding at the end;
 * lse: 8e-5 + d + 4 u |lse|.
+Gradients, from bounds on each factor carried through the products:
+* P: e_P = d + 2^-22 + 4 u (|s| + |lse|) + the error of lse, relative; h more as an operand;
+* dP: 2 u (D + 4) sum |dO v|;  delta: sum |dO| (the error of out) + 2 u (D + 4) sum |dO out|;
+* dS: P ((h + e_P) |dP - delta| + both errors);
+* dv: h |dv| + sum (h + e_P) P |dO|, dk, dq: h |.| + scale sum (error of dS) |q or k|; each sum
+  in fp32 over n products adds 2 u (n + 4) of its absolute terms.
 """
 import numpy as np
 import pytest
@@ -76,6 +82,46 @@ class Case:
             assert (e <= 8e-5 + d[~none] + 4 * U * np.abs(rlse[~none])).all(), e.max()
 
 
+    def check_grads(self, got):
+        q, k, v, g = (self.np[n] for n in ("q", "k", "v", "g"))
+        B, Tq, Hq, D = q.shape
+        S, Hk = k.shape[1:3]
+        G, scale = Hq // Hk, D ** -0.5
+        ref = dict(zip(("dq", "dk", "dv"), ca.backward(q, k, v, g, self.npmask)))
+        out, lse = ca.forward(q, k, v, self.npmask)
+        size, _ = ca.forward(q, k, np.abs(v), self.npmask)
+        d = self.score_error()
+        e_out = H * np.abs(out) + (H + 8e-5 + 2 * d.transpose(0, 2, 1)[..., None]) * size
+        tol = {n: np.zeros_like(x) for n, x in ref.items()}
+        for b in range(B):
+            keep = np.arange(S) if self.npmask is None else np.flatnonzero(self.npmask[b])
+            for h in range(Hq if len(keep) else 0):
+                kh, vh = np.abs(k[b, keep, h // G]), np.abs(v[b, keep, h // G])
+                s = scale * (q[b, :, h] @ k[b, keep, h // G].T)
+                p = np.exp(s - lse[b, h][:, None])
+                dp = g[b, :, h] @ v[b, keep, h // G].T
+                delta = np.sum(g[b, :, h] * out[b, :, h], -1, keepdims=True)
+                ga = np.abs(g[b, :, h])
+                e_lse = 8e-5 + d[b, h][:, None] + 4 * U * np.abs(lse[b, h])[:, None]
+                e_p = d[b, h][:, None] + 2.0 ** -22 + 4 * U * (np.abs(s) + np.abs(lse[b, h])[:, None]) + e_lse
+                e_dp = 2 * U * (D + 4) * (ga @ vh.T)
+                e_delta = np.sum(ga * e_out[b, :, h], -1, keepdims=True) * (1 + 2 * U * (D + 4)) + \
+                    2 * U * (D + 4) * np.sum(ga * np.abs(out[b, :, h]), -1, keepdims=True)
+                size_ds = p * np.abs(dp - delta)
+                e_ds = p * ((H + e_p) * np.abs(dp - delta) + (1 + H + e_p) * (e_dp + e_delta))
+                nq, nk = 2 * U * (Tq * G + 4), 2 * U * (S + 4)
+                tol["dv"][b, keep, h // G] += ((H + e_p + nq) * p).T @ ga
+                tol["dk"][b, keep, h // G] += scale * (e_ds + nq * size_ds).T @ np.abs(q[b, :, h])
+                tol["dq"][b, :, h] = scale * (e_ds + nk * size_ds) @ kh
+        for n, x in ref.items():
+            err = np.abs(np64(got[n]) - x)
+            t = H * np.abs(x) + tol[n] * (1 + H)
+            assert got[n].dtype == torch.bfloat16 and got[n].shape == x.shape
+            assert (err <= t).all(), (n, float((err / (t + 1e-300)).max()))
+            if np.abs(x).max() > 0:   # and well within the type's accuracy as a whole
+                assert np.linalg.norm(err) <= 2 * H * np.linalg.norm(x), (n, np.linalg.norm(err) / np.linalg.norm(x))
+
+
 CASES = [
     # B, Tq, S, Hk, G, D, mask
     (1, 1, 1, 1, 1, 16, "none"),
@@ -109,10 +155,55 @@ def test_forward(B, Tq, S, Hk, G, D, mask):
         torch.testing.assert_close(gdn.cross_attention(c.q, c.k, c.v, full), out, rtol=0, atol=0)
 
 
+def both(c, mask="own", **kw):
+    mask = c.mask if isinstance(mask, str) else mask
+    out, lse = gdn.cross_attention(c.q, c.k, c.v, mask, return_lse=True, **kw)
+    return out, lse, gdn.cross_attention_backward(c.q, c.k, c.v, out, lse, c.g, mask, **kw)
+
+
+@pytest.mark.parametrize("B,Tq,S,Hk,G,D,mask", [x for x in CASES if x[2] != 20000] + [
+    (1, 2000, 130, 1, 2, 64, "none"),      # many query tiles to few key tiles: shares of them
+    (1, 128, 1, 1, 1, 32, "none"),
+    (2, 40, 3000, 1, 3, 48, "far"),
+])
+def test_gradients(B, Tq, S, Hk, G, D, mask):
+    c = Case(B, Tq, S, Hk, G, D, mask, 3 * Tq + S + D)
+    out, lse, grads = both(c)
+    torch.cuda.synchronize()
+    assert gdn.device_error() == _lib.GDN_OK
+    c.check_grads(grads)
+    again = gdn.cross_attention_backward(c.q, c.k, c.v, out, lse, c.g, c.mask)
+    assert all(torch.equal(grads[n], again[n]) for n in grads)          # the same bits
+    if c.mask is not None:
+        assert (grads["dk"][~c.mask] == 0).all() and (grads["dv"][~c.mask] == 0).all()
+
+
+def test_gradients_along_a_direction():
+    """<gradient, step> against central differences of the fp64 oracle's loss along a
+    random step: the differences are exact to 1e-6, the gradients to 2 h of their
+    norms, so the products differ by at most 2 h |gradient| |step|."""
+    c = Case(2, 70, 150, 2, 2, 64, "holes", 31)
+    _, _, grads = both(c)
+    rng = np.random.default_rng(5)
+    for n, name in (("q", "dq"), ("k", "dk"), ("v", "dv")):
+        step = rng.standard_normal(c.np[n].shape)
+
+        def loss(e):
+            x = dict(c.np)
+            x[n] = x[n] + e * step
+            return np.sum(x["g"] * ca.forward(x["q"], x["k"], x["v"], c.npmask)[0])
+        slope = (loss(1e-5) - loss(-1e-5)) / 2e-5
+        d = np64(grads[name])
+        assert abs(slope - np.sum(d * step)) <= 2 * H * np.linalg.norm(d) * np.linalg.norm(step) + 1e-5 * abs(slope)
+
+
 @pytest.mark.parametrize("q_scale", [6.0, 40.0])
 def test_sharp_softmax(q_scale):
     c = Case(1, 200, 900, 2, 1, 64, "holes", 5, q_scale=q_scale)
-    c.check(*gdn.cross_attention(c.q, c.k, c.v, c.mask, return_lse=True))
+    out, lse, grads = both(c)
+    c.check(out, lse)
+    if q_scale < 10:
+        c.check_grads(grads)
 
 
 def test_growing_scores():
@@ -133,15 +224,18 @@ def test_masked_places_hold_anything(Tq, G):
     change no bit, in tiles that are masked in part and in whole."""
     c = Case(2, Tq, 700, 2, G, 80, "holes", 9)
     c.mask[0, 128:300] = False
-    want = gdn.cross_attention(c.q, c.k, c.v, c.mask, return_lse=True)
+    want = both(c)
     bad = torch.tensor([float("nan"), float("inf"), -float("inf"), 3.3e38], device="cuda").bfloat16()
     k, v = c.k.clone(), c.v.clone()
     for x in (k, v):
         where = ~c.mask
         x[where] = bad[torch.arange(int(where.sum()), device="cuda") % 4][:, None, None]
-    got = gdn.cross_attention(c.q, k, v, c.mask, return_lse=True)
+    c.k, c.v = k, v
+    got = both(c)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert torch.isneginf(got[1][-1]).all() and (got[0][-1] == 0).all()
+    assert all(torch.equal(got[2][n], want[2][n]) for n in want[2])
+    assert (got[2]["dq"][-1] == 0).all()
 
 
 def test_no_keys():
@@ -149,6 +243,12 @@ def test_no_keys():
     k = torch.empty(2, 0, 2, 32, device="cuda").bfloat16()
     out, lse = gdn.cross_attention(q, k, k, return_lse=True)
     assert (out == 0).all() and torch.isneginf(lse).all()
+    grads = gdn.cross_attention_backward(q, k, k, out, lse, q)
+    assert (grads["dq"] == 0).all() and grads["dk"].shape == k.shape
+    k1 = torch.randn(2, 9, 2, 32, device="cuda").bfloat16()
+    e = q[:, :0]
+    grads = gdn.cross_attention_backward(e, k1, k1, e, lse[:, :, :0].contiguous(), e)
+    assert (grads["dk"] == 0).all() and (grads["dv"] == 0).all() and grads["dk"].shape == k1.shape
     assert gdn.cross_attention(q[:, :0], k, k).shape == (2, 0, 4, 32)
     assert gdn.cross_attention(q[:0], k[:0], k[:0]).shape == (0, 5, 4, 32)
 
@@ -165,6 +265,15 @@ def test_views_and_broadcast():
     assert torch.equal(got, want)
     ref, _ = ca.forward(np64(q), np64(k), np64(v), mask.cpu().numpy(), scale=0.3)
     assert np.abs(np64(got) - ref).max() <= 2 * H * np.abs(np64(v)).max()
+    out, lse = gdn.cross_attention(q, k, v, mask, scale=0.3, return_lse=True)
+    g = torch.randn_like(out)
+    grads = gdn.cross_attention_backward(q, k, v, out, lse, g, mask, scale=0.3)
+    plain = gdn.cross_attention_backward(q.contiguous(), k.contiguous(), v.contiguous(), out, lse, g,
+                                         mask.contiguous(), scale=0.3)
+    assert all(torch.equal(grads[n], plain[n]) for n in grads)
+    dq, dk, dv = ca.backward(np64(q), np64(k), np64(v), np64(g), mask.cpu().numpy(), scale=0.3)
+    for n, x in (("dq", dq), ("dk", dk), ("dv", dv)):
+        assert np.linalg.norm(np64(grads[n]) - x) <= 2 * H * np.linalg.norm(x), n
     # sequence first
     qt = q.transpose(0, 1).contiguous().transpose(0, 1)
     assert torch.equal(gdn.cross_attention(qt, k, v, mask, scale=0.3), want)
@@ -192,7 +301,17 @@ def test_expired_wait_reports_timeout_and_next_call_is_right():
         gdn.set_wait_limit(0)
     assert gdn.device_error() == _lib.GDN_ERR_TIMEOUT
     assert gdn.device_error() == _lib.GDN_OK
-    c.check(gdn.cross_attention(c.q, c.k, c.v, c.mask))
+    out, lse, want = both(c)
+    c.check(out)
+    gdn.set_wait_limit(1)
+    try:
+        gdn.cross_attention_backward(c.q, c.k, c.v, out, lse, c.g, c.mask)
+        torch.cuda.synchronize()
+    finally:
+        gdn.set_wait_limit(0)
+    assert gdn.device_error() == _lib.GDN_ERR_TIMEOUT
+    got = gdn.cross_attention_backward(c.q, c.k, c.v, out, lse, c.g, c.mask)
+    assert all(torch.equal(got[n], want[n]) for n in want)
 
 
 def test_two_graphs_of_one_stream():
@@ -223,6 +342,30 @@ def test_two_graphs_of_one_stream():
     assert torch.equal(got, want[0][0])
 
 
+def test_gradients_in_two_graphs_of_one_stream():
+    """Forward and gradients in a graph each, replayed together: shares, row
+    statistics and mask lists are each graph's own."""
+    cs = [Case(1, 2500, 200, 2, 1, 64, "holes", s) for s in (26, 27)]
+    want = [both(c) for c in cs]
+    graphs, outs = [], []
+    for c in cs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(both(c))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for w, o in zip(want, outs):
+            assert torch.equal(w[0], o[0]) and all(torch.equal(w[2][n], o[2][n]) for n in w[2])
+            for x in (o[0], o[1], *o[2].values()):
+                x.zero_()
+
+
 def test_refusals():
     c = Case(1, 8, 8, 2, 1, 32, "none", 25)
     with pytest.raises(gdn.GDNError, match="INVALID_ARG"):
@@ -237,3 +380,8 @@ def test_refusals():
         gdn.cross_attention(c.q, c.k, c.v, torch.ones(1, 7, device="cuda", dtype=torch.bool))
     with pytest.raises(gdn.GDNError, match="ALIAS"):
         gdn.cross_attention(c.q, c.k, c.v, out=c.q)
+    out, lse = gdn.cross_attention(c.q, c.k, c.v, return_lse=True)
+    with pytest.raises(TypeError):
+        gdn.cross_attention_backward(c.q, c.k, c.v, out, lse.double(), c.g)
+    with pytest.raises(ValueError):
+        gdn.cross_attention_backward(c.q, c.k, c.v, out, lse, c.g[:, :4])
