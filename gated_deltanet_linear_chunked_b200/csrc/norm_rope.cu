@@ -34,7 +34,6 @@ namespace {
 using namespace sm100;
 
 constexpr int kThreads = 256;
-constexpr int kBwdBlocks = 3 * 148;          // per side: persistent blocks of the backward, at most
 constexpr long long kMaxStride = 1ll << 40;  // elements
 
 // One side (queries or keys) of a call.
@@ -45,7 +44,7 @@ struct Side {
   const float* w;     // [D], or nullptr: ones
   long long x_bs, x_ts, dy_bs, dy_ts, o_bs, o_ts;  // elements
   int H;
-  int log_tb;         // tokens per block = 1 << log_tb
+  int per, tb;        // groups of lanes per token, tokens per block
   unsigned blocks;    // blocks of this side
 };
 
@@ -65,25 +64,46 @@ struct NormRopeParams {
   float* partial;      // backward: [blocks][D] sums of g x^, queries' blocks first
 };
 
+// 16 bytes of a row as packed fp32 pairs: V features, V / 2 pairs.
 template <typename T> struct Vec;
 template <> struct Vec<__nv_bfloat16> {
   static constexpr int V = 8;
-  static __device__ __forceinline__ uint4 raw(const void* p) { return *static_cast<const uint4*>(p); }
-  static __device__ __forceinline__ void open(uint4 u, float (&f)[8]) { unpack8_bf16(u, f); }
-  static __device__ __forceinline__ uint4 close(const float (&f)[8]) { return pack8_bf16(f); }
+  static __device__ __forceinline__ void open(uint4 u, uint64_t* f) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ uint4 close(const uint64_t* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      f2_unpack(f[i], a, b);
+      w[i] = pack_bf16x2(a, b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
 };
 template <> struct Vec<float> {
   static constexpr int V = 4;
-  static __device__ __forceinline__ uint4 raw(const void* p) { return *static_cast<const uint4*>(p); }
-  static __device__ __forceinline__ void open(uint4 u, float (&f)[4]) {
-    f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
-    f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+  static __device__ __forceinline__ void open(uint4 u, uint64_t* f) {
+    f[0] = f2_pack(__uint_as_float(u.x), __uint_as_float(u.y));
+    f[1] = f2_pack(__uint_as_float(u.z), __uint_as_float(u.w));
   }
-  static __device__ __forceinline__ uint4 close(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                      __float_as_uint(f[3]));
+  static __device__ __forceinline__ uint4 close(const uint64_t* f) {
+    float a, b, c, d;
+    f2_unpack(f[0], a, b);
+    f2_unpack(f[1], c, d);
+    return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
   }
 };
+__device__ __forceinline__ uint4 load16(const void* p) { return *static_cast<const uint4*>(p); }
+__device__ __forceinline__ uint64_t f2_swap(uint64_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return f2_pack(b, a);
+}
 
 // The two pieces of lane l (of G) of a row, as indices of V-feature pieces,
 // and whether they hold pairs that turn.  D and R are multiples of 16, so a
@@ -92,8 +112,8 @@ struct Pieces {
   int a, b;
   bool present, turns_a, turns_b;
 };
-template <int V>
-__device__ __forceinline__ Pieces pieces_of(int l, int D, int R, bool interleaved) {
+template <int V, bool interleaved>
+__device__ __forceinline__ Pieces pieces_of(int l, int D, int R) {
   Pieces p;
   const int h = R / (2 * V);
   p.present = l < D / (2 * V);
@@ -125,32 +145,27 @@ __device__ __forceinline__ float2 angle(const NormRopeParams& P, long long n, in
   return make_float2(c * P.amplitude, (P.inverse ? -s : s) * P.amplitude);
 }
 
-// Turns a lane's pairs in place: `c`, `s` hold its V pairs' cosines and sines,
-// in the half layout pair j is (a[j], b[j]), in the interleaved one pairs
-// 0 .. V/2-1 are (a[2j], a[2j+1]) and V/2 .. V-1 are b's.  Features that do not
-// turn are left alone (not multiplied by 1 and 0: their neighbour may be infinite).
-template <int V>
-__device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float (&c)[V],
-                                     const float (&s)[V], const Pieces& pc, bool interleaved) {
-  if (interleaved) {
+// A lane holds 2V features as V packed pairs, piece a's V / 2 first.  Turning is
+//   out = x * c1 + partner * c2,
+// the partner of piece a's features being piece b's in the half layout (c2 = -s,
+// and +s the other way), and each packed pair's own other half in the interleaved
+// one (c2 = (-s, s)).  Features that do not turn are only scaled by c1 (a product
+// with 0 would let an infinite neighbour in).
+template <int V, bool interleaved>
+__device__ __forceinline__ void turn(uint64_t (&x)[V], const uint64_t (&c1)[V], const uint64_t (&c2)[V],
+                                     const Pieces& pc) {
+  constexpr int N = V / 2;
 #pragma unroll
-    for (int j = 0; j < V / 2; ++j) {
-      const float a0 = a[2 * j], a1 = a[2 * j + 1], b0 = b[2 * j], b1 = b[2 * j + 1];
-      if (pc.turns_a) {
-        a[2 * j] = a0 * c[j] - a1 * s[j];
-        a[2 * j + 1] = a0 * s[j] + a1 * c[j];
-      }
-      if (pc.turns_b) {
-        b[2 * j] = b0 * c[V / 2 + j] - b1 * s[V / 2 + j];
-        b[2 * j + 1] = b0 * s[V / 2 + j] + b1 * c[V / 2 + j];
-      }
-    }
-  } else if (pc.turns_a) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float a0 = a[j], b0 = b[j];
-      a[j] = a0 * c[j] - b0 * s[j];
-      b[j] = a0 * s[j] + b0 * c[j];
+  for (int j = 0; j < N; ++j) {
+    if (interleaved) {
+      const uint64_t a = f2_mul(x[j], c1[j]), b = f2_mul(x[N + j], c1[N + j]);
+      x[j] = pc.turns_a ? f2_fma(f2_swap(x[j]), c2[j], a) : a;
+      x[N + j] = pc.turns_b ? f2_fma(f2_swap(x[N + j]), c2[N + j], b) : b;
+    } else {
+      const uint64_t a = f2_mul(x[j], c1[j]), b = f2_mul(x[N + j], c1[N + j]);
+      const uint64_t a2 = f2_fma(x[N + j], c2[j], a), b2 = f2_fma(x[j], c2[N + j], b);
+      x[j] = pc.turns_a ? a2 : a;
+      x[N + j] = pc.turns_a ? b2 : b;
     }
   }
 }
@@ -172,30 +187,46 @@ __device__ __forceinline__ void fill_angles(const NormRopeParams& P, float2* tab
   }
 }
 
-// A lane's V pairs from its token's row of the table; pairs that do not turn
-// get cos 1, sin 0.
-template <int V>
-__device__ __forceinline__ void take_angles(const NormRopeParams& P, const float2* row, const Pieces& pc,
-                                            int l, float (&c)[V], float (&s)[V]) {
+// A lane's factors c1, c2 (see turn) from its token's row of the table and the
+// weights of its features, wx of the feature itself and wp of its partner:
+// turned = wx x c1 + wp partner c2 with the weights folded in (pass ones to leave
+// them out).
+template <int V, bool interleaved>
+__device__ __forceinline__ void take_angles(const float2* row, const Pieces& pc, int l, const uint64_t (&w)[V],
+                                            uint64_t (&c1)[V], uint64_t (&c2)[V]) {
+  constexpr int N = V / 2;
+  float wf[2 * V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const bool on = pc.present && (P.interleaved && j >= V / 2 ? pc.turns_b : pc.turns_a);
-    const float2 v = on ? row[l * V + j] : make_float2(1.f, 0.f);
-    c[j] = v.x;
-    s[j] = v.y;
+  for (int j = 0; j < V; ++j) f2_unpack(w[j], wf[2 * j], wf[2 * j + 1]);
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    if (interleaved) {  // pairs V l + j (piece a) and V l + N + j (piece b)
+      const float2 a = pc.turns_a && pc.present ? row[l * V + j] : make_float2(1.f, 0.f);
+      const float2 b = pc.turns_b && pc.present ? row[l * V + N + j] : make_float2(1.f, 0.f);
+      c1[j] = f2_pack(wf[2 * j] * a.x, wf[2 * j + 1] * a.x);
+      c2[j] = f2_pack(-wf[2 * j + 1] * a.y, wf[2 * j] * a.y);
+      c1[N + j] = f2_pack(wf[V + 2 * j] * b.x, wf[V + 2 * j + 1] * b.x);
+      c2[N + j] = f2_pack(-wf[V + 2 * j + 1] * b.y, wf[V + 2 * j] * b.y);
+    } else {  // pairs V l + 2 j and V l + 2 j + 1
+      const bool on = pc.turns_a && pc.present;
+      const float2 a = on ? row[l * V + 2 * j] : make_float2(1.f, 0.f);
+      const float2 b = on ? row[l * V + 2 * j + 1] : make_float2(1.f, 0.f);
+      c1[j] = f2_pack(wf[2 * j] * a.x, wf[2 * j + 1] * b.x);
+      c2[j] = f2_pack(-wf[V + 2 * j] * a.y, -wf[V + 2 * j + 1] * b.y);
+      c1[N + j] = f2_pack(wf[V + 2 * j] * a.x, wf[V + 2 * j + 1] * b.x);
+      c2[N + j] = f2_pack(wf[2 * j] * a.y, wf[2 * j + 1] * b.y);
+    }
   }
 }
 
+// The weights of a lane's features (ones without).
 template <int V>
-__device__ __forceinline__ void take_weights(const float* w, const Pieces& pc, float (&wa)[V], float (&wb)[V]) {
+__device__ __forceinline__ void take_weights(const float* w, const Pieces& pc, uint64_t (&to)[V]) {
+  constexpr int N = V / 2;
 #pragma unroll
-  for (int j = 0; j < V; ++j) wa[j] = wb[j] = 1.f;
-  if (w && pc.present) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      wa[j] = w[pc.a * V + j];
-      wb[j] = w[pc.b * V + j];
-    }
+  for (int j = 0; j < V; ++j) {
+    const int f = j < N ? pc.a * V + 2 * j : pc.b * V + 2 * (j - N);
+    to[j] = w && pc.present ? *reinterpret_cast<const uint64_t*>(w + f) : f2_pack(1.f, 1.f);
   }
 }
 
@@ -206,59 +237,72 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-template <typename T, int G>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int G, bool interleaved>
+__global__ void __launch_bounds__(kThreads, 3)
 gdn_norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
   using VT = Vec<T>;
-  constexpr int V = VT::V, kGroups = kThreads / G;
+  constexpr int V = VT::V, N = V / 2;
   extern __shared__ float2 tab[];
   unsigned block;
   const Side& S = P.side[my_side(P, &block)];
-  const int tb = 1 << S.log_tb, per = kGroups >> S.log_tb;  // tokens; groups per token
-  const long long n0 = (long long)block << S.log_tb;
   const int l = threadIdx.x % G, grp = threadIdx.x / G;
-  const int tk = grp / per, h0 = grp - tk * per;
-  const bool interleaved = P.interleaved;
-  const Pieces pc = pieces_of<V>(l, P.D, P.R, interleaved);
-  if (P.R > 0) fill_angles(P, tab, n0, tb);
-  float wa[V], wb[V], c[V], s[V];
-  take_weights<V>(S.w, pc, wa, wb);
-  __syncthreads();
-  take_angles<V>(P, tab + tk * (P.R / 2), pc, l, c, s);
-  const long long n = n0 + tk;
-  const bool on = n < P.tokens;
-  const long long b = n / P.T, t = n - b * P.T;
-  const T* x = static_cast<const T*>(S.x) + (on ? b * S.x_bs + t * S.x_ts : 0);
-  T* out = static_cast<T*>(S.out) + (on ? b * S.o_bs + t * S.o_ts : 0);
+  const int tk = grp / S.per, h0 = grp - tk * S.per;
+  const long long n0 = (long long)block * S.tb, n = n0 + tk;
+  const Pieces pc = pieces_of<V, interleaved>(l, P.D, P.R);
+  const bool on = pc.present && tk < S.tb && n < P.tokens;
+  const long long b = on ? n / P.T : 0, t = on ? n - b * P.T : 0;
+  const T* x = static_cast<const T*>(S.x) + b * S.x_bs + t * S.x_ts;
+  T* out = static_cast<T*>(S.out) + b * S.o_bs + t * S.o_ts;
+  // two heads' loads are always under way, the first before the angles
+  uint4 ring[2][2];
+  auto fetch = [&](uint4 (&to)[2], int h) {
+    to[0] = to[1] = make_uint4(0, 0, 0, 0);
+    if (on && h < S.H) {
+      to[0] = load16(x + (long long)h * P.D + pc.a * V);
+      to[1] = load16(x + (long long)h * P.D + pc.b * V);
+    }
+  };
+  fetch(ring[0], h0);
+  fetch(ring[1], h0 + S.per);
+  uint64_t c1[V], c2[V];
+  {
+    uint64_t w[V];
+    take_weights<V>(S.w, pc, w);
+    if (P.R > 0) {
+      fill_angles(P, tab, n0, S.tb);
+      __syncthreads();
+    }
+    take_angles<V, interleaved>(tab + min(tk, S.tb - 1) * (P.R / 2), pc, l, w, c1, c2);
+  }
   const float inv_d = 1.f / P.D;
-  // the trip count is the block's, so that the group sums see whole warps
-  for (int h1 = 0; h1 < S.H; h1 += per) {
-    const int h = h1 + h0;
-    const bool act = on && pc.present && h < S.H;
-    float a[V], e[V];
-    uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
-    if (act) {
-      ra = VT::raw(x + (long long)h * P.D + pc.a * V);
-      rb = VT::raw(x + (long long)h * P.D + pc.b * V);
-    }
-    VT::open(ra, a);
-    VT::open(rb, e);
+  auto work = [&](const uint4 (&from)[2], int h) {
+    uint64_t v[V];
+    VT::open(from[0], v);
+    VT::open(from[1], v + N);
     if (P.norm) {
-      float ss = 0.f;
+      uint64_t s2[2] = {0, 0};
 #pragma unroll
-      for (int j = 0; j < V; ++j) ss += a[j] * a[j] + e[j] * e[j];
-      const float r = rsqrtf(group_sum<G>(ss) * inv_d + P.eps);
+      for (int j = 0; j < V; ++j) s2[j & 1] = f2_fma(v[j], v[j], s2[j & 1]);
+      float sa, sb;
+      f2_unpack(f2_add(s2[0], s2[1]), sa, sb);
+      const float r = rsqrtf(group_sum<G>(sa + sb) * inv_d + P.eps);
+      const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        a[j] *= r * wa[j];
-        e[j] *= r * wb[j];
-      }
+      for (int j = 0; j < V; ++j) v[j] = f2_mul(v[j], r2);
     }
-    turn<V>(a, e, c, s, pc, interleaved);
-    if (act) {
-      *reinterpret_cast<uint4*>(out + (long long)h * P.D + pc.a * V) = VT::close(a);
-      *reinterpret_cast<uint4*>(out + (long long)h * P.D + pc.b * V) = VT::close(e);
+    turn<V, interleaved>(v, c1, c2, pc);
+    if (on && h < S.H) {
+      *reinterpret_cast<uint4*>(out + (long long)h * P.D + pc.a * V) = VT::close(v);
+      *reinterpret_cast<uint4*>(out + (long long)h * P.D + pc.b * V) = VT::close(v + N);
     }
+  };
+  // the trip count is the block's, so that the group sums see whole warps
+  for (int h1 = 0; h1 < S.H; h1 += 2 * S.per) {
+    const int h = h1 + h0;
+    work(ring[0], h);
+    fetch(ring[0], h + 2 * S.per);
+    work(ring[1], h + S.per);
+    fetch(ring[1], h + 3 * S.per);
   }
 }
 
@@ -266,96 +310,105 @@ gdn_norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
 // a stride of the side's blocks, so that the weight's gradient leaves as one
 // partial row per block, which gdn_norm_rope_reduce_kernel adds up in a fixed
 // order (no atomics: the same call gives the same bits).
-template <typename T, int G>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int G, bool interleaved>
+__global__ void __launch_bounds__(kThreads, 2)
 gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
   using VT = Vec<T>;
-  constexpr int V = VT::V, kGroups = kThreads / G;
+  constexpr int V = VT::V, N = V / 2;
   extern __shared__ float2 tab[];
   unsigned block;
   const Side& S = P.side[my_side(P, &block)];
-  const int tb = 1 << S.log_tb, per = kGroups >> S.log_tb;
-  const long long tiles = (P.tokens + tb - 1) >> S.log_tb;
+  const long long tiles = (P.tokens + S.tb - 1) / S.tb;
   const int l = threadIdx.x % G, grp = threadIdx.x / G;
-  const int tk = grp / per, h0 = grp - tk * per;
-  const bool interleaved = P.interleaved;
-  const Pieces pc = pieces_of<V>(l, P.D, P.R, interleaved);
-  float wa[V], wb[V], da[V], db[V];
-  take_weights<V>(S.w, pc, wa, wb);
+  const int tk = grp / S.per, h0 = grp - tk * S.per;
+  const Pieces pc = pieces_of<V, interleaved>(l, P.D, P.R);
+  uint64_t w[V], dw[V];
+  take_weights<V>(S.w, pc, w);
 #pragma unroll
-  for (int j = 0; j < V; ++j) da[j] = db[j] = 0.f;
+  for (int j = 0; j < V; ++j) dw[j] = 0;
   const float inv_d = 1.f / P.D;
   for (long long tile = block; tile < tiles; tile += S.blocks) {
-    const long long n0 = tile << S.log_tb;
-    float c[V], s[V];
+    const long long n0 = tile * S.tb, n = n0 + tk;
+    const bool on = pc.present && tk < S.tb && n < P.tokens;
+    const long long b = on ? n / P.T : 0, t = on ? n - b * P.T : 0;
+    const T* x = static_cast<const T*>(S.x) + b * S.x_bs + t * S.x_ts;
+    const T* dy = static_cast<const T*>(S.dy) + b * S.dy_bs + t * S.dy_ts;
+    T* out = static_cast<T*>(S.out) + b * S.o_bs + t * S.o_ts;
+    // the next head's loads are always under way, the first before the angles
+    uint4 ring[4];
+    auto fetch = [&](int h) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ring[i] = make_uint4(0, 0, 0, 0);
+      if (on && h < S.H) {
+        ring[0] = load16(x + (long long)h * P.D + pc.a * V);
+        ring[1] = load16(x + (long long)h * P.D + pc.b * V);
+        ring[2] = load16(dy + (long long)h * P.D + pc.a * V);
+        ring[3] = load16(dy + (long long)h * P.D + pc.b * V);
+      }
+    };
+    fetch(h0);
     if (P.R > 0) {
       __syncthreads();  // the table's readers of the tile before
-      fill_angles(P, tab, n0, tb);
+      fill_angles(P, tab, n0, S.tb);
       __syncthreads();
     }
-    take_angles<V>(P, tab + tk * (P.R / 2), pc, l, c, s);
-    const long long n = n0 + tk;
-    const bool on = n < P.tokens;
-    const long long b = n / P.T, t = n - b * P.T;
-    const T* x = static_cast<const T*>(S.x) + (on ? b * S.x_bs + t * S.x_ts : 0);
-    const T* dy = static_cast<const T*>(S.dy) + (on ? b * S.dy_bs + t * S.dy_ts : 0);
-    T* out = static_cast<T*>(S.out) + (on ? b * S.o_bs + t * S.o_ts : 0);
-    for (int h1 = 0; h1 < S.H; h1 += per) {
+    uint64_t c1[V], c2[V];
+    {
+      uint64_t ones[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) ones[j] = f2_pack(1.f, 1.f);
+      take_angles<V, interleaved>(tab + min(tk, S.tb - 1) * (P.R / 2), pc, l, ones, c1, c2);
+    }
+    for (int h1 = 0; h1 < S.H; h1 += S.per) {
       const int h = h1 + h0;
-      const bool act = on && pc.present && h < S.H;
-      float a[V], e[V], ga[V], ge[V];
-      uint4 ra = make_uint4(0, 0, 0, 0), rb = ra, rc = ra, rd = ra;
-      if (act) {
-        ra = VT::raw(x + (long long)h * P.D + pc.a * V);
-        rb = VT::raw(x + (long long)h * P.D + pc.b * V);
-        rc = VT::raw(dy + (long long)h * P.D + pc.a * V);
-        rd = VT::raw(dy + (long long)h * P.D + pc.b * V);
-      }
-      VT::open(ra, a);
-      VT::open(rb, e);
-      VT::open(rc, ga);
-      VT::open(rd, ge);
-      turn<V>(ga, ge, c, s, pc, interleaved);
-      float ss = 0.f, dot = 0.f;
+      uint64_t v[V], g[V];
+      VT::open(ring[0], v);
+      VT::open(ring[1], v + N);
+      VT::open(ring[2], g);
+      VT::open(ring[3], g + N);
+      fetch(h + S.per);
+      turn<V, interleaved>(g, c1, c2, pc);
+      uint64_t s2[2] = {0, 0}, d2[2] = {0, 0};
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        ss += a[j] * a[j] + e[j] * e[j];
-        dot += ga[j] * wa[j] * a[j] + ge[j] * wb[j] * e[j];
+        s2[j & 1] = f2_fma(v[j], v[j], s2[j & 1]);
+        d2[j & 1] = f2_fma(f2_mul(g[j], w[j]), v[j], d2[j & 1]);
       }
-      ss = group_sum<G>(ss);
-      dot = group_sum<G>(dot);
+      float sa, sb, da, db;
+      f2_unpack(f2_add(s2[0], s2[1]), sa, sb);
+      f2_unpack(f2_add(d2[0], d2[1]), da, db);
+      const float ss = group_sum<G>(sa + sb), dot = group_sum<G>(da + db);
       const float r = rsqrtf(ss * inv_d + P.eps);
-      const float m = dot * r * inv_d;  // mean(g w x^)
+      const float m = -dot * r * inv_d;  // -mean(g w x^)
+      const uint64_t r2 = f2_pack(r, r), m2 = f2_pack(m, m);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float xa = a[j] * r, xe = e[j] * r;
-        da[j] += ga[j] * xa;
-        db[j] += ge[j] * xe;
-        ga[j] = r * (ga[j] * wa[j] - xa * m);
-        ge[j] = r * (ge[j] * wb[j] - xe * m);
+        const uint64_t hat = f2_mul(v[j], r2);
+        dw[j] = f2_fma(g[j], hat, dw[j]);
+        g[j] = f2_mul(r2, f2_fma(hat, m2, f2_mul(g[j], w[j])));
       }
-      if (act) {
-        *reinterpret_cast<uint4*>(out + (long long)h * P.D + pc.a * V) = VT::close(ga);
-        *reinterpret_cast<uint4*>(out + (long long)h * P.D + pc.b * V) = VT::close(ge);
+      if (on && h < S.H) {
+        *reinterpret_cast<uint4*>(out + (long long)h * P.D + pc.a * V) = VT::close(g);
+        *reinterpret_cast<uint4*>(out + (long long)h * P.D + pc.b * V) = VT::close(g + N);
       }
     }
   }
   // the block's sums: first over the groups of a warp, then over its warps
   __shared__ float red[kThreads / 32][128];
+  float df[2 * V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
+  for (int j = 0; j < V; ++j) f2_unpack(dw[j], df[2 * j], df[2 * j + 1]);
 #pragma unroll
-    for (int o = 16; o >= G; o >>= 1) {
-      da[j] += __shfl_xor_sync(~0u, da[j], o);
-      db[j] += __shfl_xor_sync(~0u, db[j], o);
-    }
+  for (int j = 0; j < 2 * V; ++j) {
+#pragma unroll
+    for (int o = 16; o >= G; o >>= 1) df[j] += __shfl_xor_sync(~0u, df[j], o);
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (lane < G && pc.present) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      red[warp][pc.a * V + j] = da[j];
-      red[warp][pc.b * V + j] = db[j];
+      red[warp][pc.a * V + j] = df[j];
+      red[warp][pc.b * V + j] = df[V + j];
     }
   }
   __syncthreads();
@@ -398,16 +451,26 @@ int lanes_per_row(int D, int V) {
   return g;
 }
 
-// Tokens per block: enough groups on each token that a group takes about four
-// of its heads (the angles, once in registers, serve them all), fewer tokens
-// while the grid does not fill the GPU.
-int log_tokens_per_block(int groups, int H, long long tokens, int sms) {
-  int per = 1;
-  while (per < groups && per * 4 < H) per *= 2;
-  int lt = 0;
-  while ((per << (lt + 1)) <= groups) ++lt;
-  while (lt > 0 && (tokens >> lt) < 2 * sms) --lt;
-  return lt;
+// How a block's groups are shared out: `per` of them to a token, so that the
+// angles, once in registers, serve ceil(H / per) heads of it.  Taken for the least
+// idle lanes, over the groups of a block and over the waves of blocks (`slots` run
+// at a time); among equals the one with more heads per group, down to two.
+void share_groups(int groups, int H, long long tokens, int slots, Side* S) {
+  double best = -1;
+  for (int per = 1; per <= groups; ++per) {
+    const int heads = (H + per - 1) / per;
+    if (per > 1 && heads < 2 && tokens * H > (long long)slots * groups) break;
+    const int tb = (int)std::min<long long>(groups / per, tokens);
+    const long long blocks = (tokens + tb - 1) / tb;
+    const long long waves = (blocks + slots - 1) / slots;
+    // work of all rows over the time of all waves, each as long as its heads and a start
+    const double e = (double)tokens * H / ((double)waves * slots * groups * (heads + 1.5));
+    if (e > best * 1.001) {
+      best = e;
+      S->per = per;
+      S->tb = tb;
+    }
+  }
 }
 
 template <typename T, int G>
@@ -415,23 +478,31 @@ cudaError_t launch_g(NormRopeParams& P, bool backward, cudaStream_t stream) {
   constexpr int groups = kThreads / G;
   const int sms = num_sms();
   size_t smem = 0;
+  const int heads = P.side[0].H + P.side[1].H;
   for (Side& S : P.side) {
     S.blocks = 0;
-    S.log_tb = 0;
+    S.per = S.tb = 1;
     if (!S.H) continue;
-    S.log_tb = log_tokens_per_block(groups, S.H, P.tokens, sms);
-    const long long tiles = (P.tokens + (1 << S.log_tb) - 1) >> S.log_tb;
-    S.blocks = (unsigned)tiles;
-    if (backward) S.blocks = (unsigned)std::min<long long>(tiles, kBwdBlocks);
-    smem = std::max(smem, (size_t)(1 << S.log_tb) * (P.R / 2) * sizeof(float2));
+    // each side gets its part of the blocks that run at a time
+    const int slots = std::max(1, (backward ? 2 : 3) * sms * S.H / heads);
+    share_groups(groups, S.H, P.tokens, slots, &S);
+    const long long tiles = (P.tokens + S.tb - 1) / S.tb;
+    S.blocks = (unsigned)(backward ? std::min<long long>(tiles, slots) : tiles);
+    smem = std::max(smem, (size_t)S.tb * (P.R / 2) * sizeof(float2));
   }
   const unsigned grid = P.side[0].blocks + P.side[1].blocks;
   if (backward) {
     ProfileScope ps(stream, kKernNormRopeBwd);
-    gdn_norm_rope_bwd_kernel<T, G><<<grid, kThreads, smem, stream>>>(P);
+    if (P.interleaved)
+      gdn_norm_rope_bwd_kernel<T, G, true><<<grid, kThreads, smem, stream>>>(P);
+    else
+      gdn_norm_rope_bwd_kernel<T, G, false><<<grid, kThreads, smem, stream>>>(P);
   } else {
     ProfileScope ps(stream, kKernNormRope);
-    gdn_norm_rope_kernel<T, G><<<grid, kThreads, smem, stream>>>(P);
+    if (P.interleaved)
+      gdn_norm_rope_kernel<T, G, true><<<grid, kThreads, smem, stream>>>(P);
+    else
+      gdn_norm_rope_kernel<T, G, false><<<grid, kThreads, smem, stream>>>(P);
   }
   count_launches(1);
   return cudaGetLastError();
@@ -654,8 +725,9 @@ gdn_status run(const Call& c) {
   }
   OpScratch sc;
   unsigned int* err = nullptr;
+  // a row of partial sums per block: at most two blocks an SM, and one a side
   const gdn_status st =
-      op_scratch(dev, stream, (size_t)2 * kBwdBlocks * c.D * sizeof(float), &err, &sc);
+      op_scratch(dev, stream, (size_t)(2 * num_sms() + 2) * c.D * sizeof(float), &err, &sc);
   if (st != GDN_OK) return st;
   P.partial = static_cast<float*>(sc.p);
   cudaError_t e = c.dtype == GDN_BF16 ? launch_t<__nv_bfloat16>(P, true, stream)
