@@ -15,9 +15,10 @@
 // two 16-byte pieces of it.  In the half layout the two pieces are the two sides
 // of the same pairs (features i and i + R/2), in the interleaved one they are
 // neighbours: either way a lane turns its pairs alone, and only the sum of
-// squares crosses lanes.  A block takes TB tokens of the queries or of the keys;
-// it forms the cosines and sines of its tokens once, in shared memory, each
-// group takes its token's into registers and keeps them for all of its heads.
+// squares crosses lanes.  A block takes a tile of tokens, all heads of queries and
+// keys; it forms the cosines and sines of its tokens once, in shared memory, each
+// group takes its token's into registers, with the weights of its side folded in,
+// and keeps them for its heads, two of which are always on their way from memory.
 // Angles are formed in 64 bits and reduced to a fraction of a turn there: a
 // position of 10^6 has an angle whose 32-bit rounding is already 0.06.
 #include <cuda_bf16.h>
@@ -44,8 +45,7 @@ struct Side {
   const float* w;     // [D], or nullptr: ones
   long long x_bs, x_ts, dy_bs, dy_ts, o_bs, o_ts;  // elements
   int H;
-  int per, tb;        // groups of lanes per token, tokens per block
-  unsigned blocks;    // blocks of this side
+  int per;            // groups of lanes per token
 };
 
 struct NormRopeParams {
@@ -56,12 +56,15 @@ struct NormRopeParams {
   int pos_wide;        // positions are int64, else int32
   int axes, sec1, sec2;  // pairs below sec1: axis 0, below sec2: axis 1, else axis 2
   int T, D, R;
-  long long tokens;    // B * T
+  unsigned tokens;     // B * T
+  int heads;           // heads of a group, at most
+  int tb;              // tokens of a tile: what a block's groups take at a time
+  unsigned tiles;
   float amplitude, eps;
   int interleaved;
   int norm;
   int inverse;         // turn by -t
-  float* partial;      // backward: [blocks][D] sums of g x^, queries' blocks first
+  float* partial;      // backward: [side][block][D] sums of g x^
 };
 
 // 16 bytes of a row as packed fp32 pairs: V features, V / 2 pairs.
@@ -131,10 +134,10 @@ __device__ __forceinline__ Pieces pieces_of(int l, int D, int R) {
 }
 
 // cos and sin (times the amplitude) of the pair `i` of token n, t = turns.
-__device__ __forceinline__ float2 angle(const NormRopeParams& P, long long n, int i) {
-  const long long b = n / P.T, t = n - b * P.T;
+__device__ __forceinline__ float2 angle(const NormRopeParams& P, unsigned n, int i) {
+  const unsigned b = n / (unsigned)P.T, t = n - b * P.T;
   const int axis = i < P.sec1 ? 0 : i < P.sec2 ? 1 : 2;
-  const long long at = b * P.pos_bs + t * P.axes + axis;
+  const long long at = b * P.pos_bs + (long long)t * P.axes + axis;
   const double pos = P.pos_wide ? (double)static_cast<const long long*>(P.pos)[at]
                                 : (double)static_cast<const int*>(P.pos)[at];
   // turns = position * frequency / 2 pi; only its fraction matters
@@ -170,18 +173,25 @@ __device__ __forceinline__ void turn(uint64_t (&x)[V], const uint64_t (&c1)[V], 
   }
 }
 
-// The block's side, its first token and its index within the side.
-__device__ __forceinline__ int my_side(const NormRopeParams& P, unsigned* block) {
-  *block = blockIdx.x;
-  if (blockIdx.x < P.side[0].blocks) return 0;
-  *block -= P.side[0].blocks;
-  return 1;
+// A group's place in a block: its token of the tile (or none), its side, and the
+// heads h0, h0 + per, ... of that side it takes.
+struct Place {
+  int token, side, h0;
+};
+__device__ __forceinline__ Place place_of(const NormRopeParams& P, int grp) {
+  const int per = P.side[0].per + P.side[1].per;
+  Place p;
+  p.token = grp / per;
+  const int i = grp - p.token * per;
+  p.side = i >= P.side[0].per;
+  p.h0 = p.side ? i - P.side[0].per : i;
+  return p;
 }
 
 // Fills tab[token][pair] for the tokens n0 .. n0 + tb - 1.
-__device__ __forceinline__ void fill_angles(const NormRopeParams& P, float2* tab, long long n0, int tb) {
+__device__ __forceinline__ void fill_angles(const NormRopeParams& P, float2* tab, unsigned n0) {
   const int pairs = P.R / 2;
-  for (int i = threadIdx.x; i < tb * pairs; i += kThreads) {
+  for (int i = threadIdx.x; i < P.tb * pairs; i += kThreads) {
     const int tk = i / pairs;
     if (n0 + tk < P.tokens) tab[i] = angle(P, n0 + tk, i - tk * pairs);
   }
@@ -243,14 +253,15 @@ gdn_norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
   using VT = Vec<T>;
   constexpr int V = VT::V, N = V / 2;
   extern __shared__ float2 tab[];
-  unsigned block;
-  const Side& S = P.side[my_side(P, &block)];
-  const int l = threadIdx.x % G, grp = threadIdx.x / G;
-  const int tk = grp / S.per, h0 = grp - tk * S.per;
-  const long long n0 = (long long)block * S.tb, n = n0 + tk;
+  const int l = threadIdx.x % G;
+  const Place pl = place_of(P, threadIdx.x / G);
+  const Side& S = P.side[pl.side];
+  const int tk = pl.token, h0 = pl.h0;
+  const unsigned n0 = blockIdx.x * P.tb, n = n0 + tk;
   const Pieces pc = pieces_of<V, interleaved>(l, P.D, P.R);
-  const bool on = pc.present && tk < S.tb && n < P.tokens;
-  const long long b = on ? n / P.T : 0, t = on ? n - b * P.T : 0;
+  const bool on = pc.present && tk < P.tb && n < P.tokens;
+  const unsigned bu = on ? n / (unsigned)P.T : 0, tu = on ? n - bu * P.T : 0;
+  const long long b = bu, t = tu;
   const T* x = static_cast<const T*>(S.x) + b * S.x_bs + t * S.x_ts;
   T* out = static_cast<T*>(S.out) + b * S.o_bs + t * S.o_ts;
   // two heads' loads are always under way, the first before the angles
@@ -269,10 +280,10 @@ gdn_norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
     uint64_t w[V];
     take_weights<V>(S.w, pc, w);
     if (P.R > 0) {
-      fill_angles(P, tab, n0, S.tb);
+      fill_angles(P, tab, n0);
       __syncthreads();
     }
-    take_angles<V, interleaved>(tab + min(tk, S.tb - 1) * (P.R / 2), pc, l, w, c1, c2);
+    take_angles<V, interleaved>(tab + min(tk, P.tb - 1) * (P.R / 2), pc, l, w, c1, c2);
   }
   const float inv_d = 1.f / P.D;
   auto work = [&](const uint4 (&from)[2], int h) {
@@ -297,9 +308,9 @@ gdn_norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
     }
   };
   // the trip count is the block's, so that the group sums see whole warps
-  for (int h1 = 0; h1 < S.H; h1 += 2 * S.per) {
-    const int h = h1 + h0;
+  for (int i = 0, h = h0; i < P.heads; i += 2, h += 2 * S.per) {
     work(ring[0], h);
+    if (i + 1 >= P.heads) break;
     fetch(ring[0], h + 2 * S.per);
     work(ring[1], h + S.per);
     fetch(ring[1], h + 3 * S.per);
@@ -316,21 +327,21 @@ gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
   using VT = Vec<T>;
   constexpr int V = VT::V, N = V / 2;
   extern __shared__ float2 tab[];
-  unsigned block;
-  const Side& S = P.side[my_side(P, &block)];
-  const long long tiles = (P.tokens + S.tb - 1) / S.tb;
   const int l = threadIdx.x % G, grp = threadIdx.x / G;
-  const int tk = grp / S.per, h0 = grp - tk * S.per;
+  const Place pl = place_of(P, grp);
+  const Side& S = P.side[pl.side];
+  const int tk = pl.token, h0 = pl.h0;
   const Pieces pc = pieces_of<V, interleaved>(l, P.D, P.R);
   uint64_t w[V], dw[V];
   take_weights<V>(S.w, pc, w);
 #pragma unroll
   for (int j = 0; j < V; ++j) dw[j] = 0;
   const float inv_d = 1.f / P.D;
-  for (long long tile = block; tile < tiles; tile += S.blocks) {
-    const long long n0 = tile * S.tb, n = n0 + tk;
-    const bool on = pc.present && tk < S.tb && n < P.tokens;
-    const long long b = on ? n / P.T : 0, t = on ? n - b * P.T : 0;
+  for (unsigned tile = blockIdx.x; tile < P.tiles; tile += gridDim.x) {
+    const unsigned n0 = tile * P.tb, n = n0 + tk;
+    const bool on = pc.present && tk < P.tb && n < P.tokens;
+    const unsigned bu = on ? n / (unsigned)P.T : 0, tu = on ? n - bu * P.T : 0;
+    const long long b = bu, t = tu;
     const T* x = static_cast<const T*>(S.x) + b * S.x_bs + t * S.x_ts;
     const T* dy = static_cast<const T*>(S.dy) + b * S.dy_bs + t * S.dy_ts;
     T* out = static_cast<T*>(S.out) + b * S.o_bs + t * S.o_ts;
@@ -349,7 +360,7 @@ gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
     fetch(h0);
     if (P.R > 0) {
       __syncthreads();  // the table's readers of the tile before
-      fill_angles(P, tab, n0, S.tb);
+      fill_angles(P, tab, n0);
       __syncthreads();
     }
     uint64_t c1[V], c2[V];
@@ -357,10 +368,9 @@ gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
       uint64_t ones[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) ones[j] = f2_pack(1.f, 1.f);
-      take_angles<V, interleaved>(tab + min(tk, S.tb - 1) * (P.R / 2), pc, l, ones, c1, c2);
+      take_angles<V, interleaved>(tab + min(tk, P.tb - 1) * (P.R / 2), pc, l, ones, c1, c2);
     }
-    for (int h1 = 0; h1 < S.H; h1 += S.per) {
-      const int h = h1 + h0;
+    for (int i = 0, h = h0; i < P.heads; ++i, h += S.per) {
       uint64_t v[V], g[V];
       VT::open(ring[0], v);
       VT::open(ring[1], v + N);
@@ -393,30 +403,26 @@ gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
       }
     }
   }
-  // the block's sums: first over the groups of a warp, then over its warps
-  __shared__ float red[kThreads / 32][128];
-  float df[2 * V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) f2_unpack(dw[j], df[2 * j], df[2 * j + 1]);
-#pragma unroll
-  for (int j = 0; j < 2 * V; ++j) {
-#pragma unroll
-    for (int o = 16; o >= G; o >>= 1) df[j] += __shfl_xor_sync(~0u, df[j], o);
-  }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (lane < G && pc.present) {
+  // the block's sums: every group's row to shared memory (over the angles), then a
+  // thread per side and feature adds the side's up in their order
+  float* red = reinterpret_cast<float*>(tab);
+  __syncthreads();
+  if (pc.present) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      red[warp][pc.a * V + j] = df[j];
-      red[warp][pc.b * V + j] = df[V + j];
+      const int f = j < N ? pc.a * V + 2 * j : pc.b * V + 2 * (j - N);
+      *reinterpret_cast<uint64_t*>(red + grp * P.D + f) = dw[j];
     }
   }
   __syncthreads();
-  if (threadIdx.x < P.D) {
+  const int per = P.side[0].per + P.side[1].per;
+  for (int i = threadIdx.x; i < 2 * P.D; i += kThreads) {
+    const int side = i >= P.D, f = i - side * P.D;
+    const int lo = side ? P.side[0].per : 0, hi = side ? per : P.side[0].per;
     float sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) sum += red[w][threadIdx.x];
-    P.partial[(size_t)blockIdx.x * P.D + threadIdx.x] = sum;
+    for (int k = 0; k < P.tb; ++k)
+      for (int x = lo; x < hi; ++x) sum += red[(k * per + x) * P.D + f];
+    P.partial[((size_t)side * gridDim.x + blockIdx.x) * P.D + f] = sum;
   }
   pdl_trigger();
 }
@@ -425,15 +431,15 @@ gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
 // (side, 16 features), 16 lanes across features and 32 rows at a time.
 constexpr int kRedCols = 16, kRedRows = 32;
 __global__ void __launch_bounds__(kRedCols * kRedRows)
-gdn_norm_rope_reduce_kernel(const float* partial, unsigned n0, unsigned n1, int D, float* dw0, float* dw1) {
+gdn_norm_rope_reduce_kernel(const float* partial, unsigned blocks, int D, float* dw0, float* dw1) {
   pdl_wait();
   __shared__ float red[kRedRows][kRedCols + 1];
   const int col = threadIdx.x % kRedCols, row = threadIdx.x / kRedCols;
   const int f = blockIdx.x * kRedCols + col;
-  const unsigned lo = blockIdx.y ? n0 : 0, hi = blockIdx.y ? n0 + n1 : n0;
   float* dw = blockIdx.y ? dw1 : dw0;
+  const float* from = partial + (size_t)blockIdx.y * blocks * D + f;
   float sum = 0.f;
-  for (unsigned i = lo + row; i < hi; i += kRedRows) sum += partial[(size_t)i * D + f];
+  for (unsigned i = row; i < blocks; i += kRedRows) sum += from[(size_t)i * D];
   red[row][col] = sum;
   __syncthreads();
   if (row == 0 && dw) {
@@ -451,46 +457,43 @@ int lanes_per_row(int D, int V) {
   return g;
 }
 
-// How a block's groups are shared out: `per` of them to a token, so that the
-// angles, once in registers, serve ceil(H / per) heads of it.  Taken for the least
-// idle lanes, over the groups of a block and over the waves of blocks (`slots` run
-// at a time); among equals the one with more heads per group, down to two.
-void share_groups(int groups, int H, long long tokens, int slots, Side* S) {
-  double best = -1;
-  for (int per = 1; per <= groups; ++per) {
-    const int heads = (H + per - 1) / per;
-    if (per > 1 && heads < 2 && tokens * H > (long long)slots * groups) break;
-    const int tb = (int)std::min<long long>(groups / per, tokens);
-    const long long blocks = (tokens + tb - 1) / tb;
-    const long long waves = (blocks + slots - 1) / slots;
-    // work of all rows over the time of all waves, each as long as its heads and a start
-    const double e = (double)tokens * H / ((double)waves * slots * groups * (heads + 1.5));
-    if (e > best * 1.001) {
-      best = e;
-      S->per = per;
-      S->tb = tb;
+// How a block's groups are shared out: for m heads a group, ceil(H / m) groups of
+// each side to a token.  The angles, once in registers, serve m heads, and a tile
+// starts once for them, which counts as 1.5 heads; m is the one that takes the
+// least time over all waves of tiles (`slots` blocks run at a time).  The chunk of
+// 2640 tokens, 20 + 20 heads of 112 in bf16: m = 4, three tokens to a tile, 880
+// tiles for 444 slots; m = 5 would leave a second wave half empty.
+bool share_groups(int groups, int slots, NormRopeParams* P) {
+  double best = 0;
+  const int most = std::max(P->side[0].H, P->side[1].H);
+  for (int m = 1; m <= most; ++m) {
+    const int per0 = (P->side[0].H + m - 1) / m, per1 = (P->side[1].H + m - 1) / m;
+    if (per0 + per1 > groups) continue;
+    const unsigned tb = std::min<unsigned>(groups / (per0 + per1), P->tokens);
+    const unsigned tiles = (P->tokens + tb - 1) / tb;
+    const double time = (double)((tiles + slots - 1) / slots) * (m + 1.5);
+    if (best == 0 || time < best) {
+      best = time;
+      P->side[0].per = per0;
+      P->side[1].per = per1;
+      P->heads = m;
+      P->tb = tb;
+      P->tiles = tiles;
     }
+    if (m > 64 && best > 0) break;
   }
+  return best > 0;
 }
 
 template <typename T, int G>
-cudaError_t launch_g(NormRopeParams& P, bool backward, cudaStream_t stream) {
+cudaError_t launch_g(NormRopeParams& P, bool backward, cudaStream_t stream, unsigned* blocks) {
   constexpr int groups = kThreads / G;
-  const int sms = num_sms();
-  size_t smem = 0;
-  const int heads = P.side[0].H + P.side[1].H;
-  for (Side& S : P.side) {
-    S.blocks = 0;
-    S.per = S.tb = 1;
-    if (!S.H) continue;
-    // each side gets its part of the blocks that run at a time
-    const int slots = std::max(1, (backward ? 2 : 3) * sms * S.H / heads);
-    share_groups(groups, S.H, P.tokens, slots, &S);
-    const long long tiles = (P.tokens + S.tb - 1) / S.tb;
-    S.blocks = (unsigned)(backward ? std::min<long long>(tiles, slots) : tiles);
-    smem = std::max(smem, (size_t)S.tb * (P.R / 2) * sizeof(float2));
-  }
-  const unsigned grid = P.side[0].blocks + P.side[1].blocks;
+  const int slots = (backward ? 2 : 3) * num_sms();
+  if (!share_groups(groups, slots, &P)) return cudaErrorInvalidValue;
+  const unsigned grid = backward ? std::min<unsigned>(P.tiles, slots) : P.tiles;
+  size_t smem = (size_t)P.tb * (P.R / 2) * sizeof(float2);
+  if (backward) smem = std::max(smem, (size_t)groups * P.D * sizeof(float));
+  *blocks = grid;
   if (backward) {
     ProfileScope ps(stream, kKernNormRopeBwd);
     if (P.interleaved)
@@ -509,14 +512,14 @@ cudaError_t launch_g(NormRopeParams& P, bool backward, cudaStream_t stream) {
 }
 
 template <typename T>
-cudaError_t launch_t(NormRopeParams& P, bool backward, cudaStream_t stream) {
+cudaError_t launch_t(NormRopeParams& P, bool backward, cudaStream_t stream, unsigned* blocks) {
   // D / 16 pieces of two for bf16 (1 to 8), D / 8 for fp32 (2 to 16)
   constexpr int kLeast = Vec<T>::V == 8 ? 1 : 2;
   switch (lanes_per_row(P.D, Vec<T>::V) / kLeast) {
-    case 1: return launch_g<T, kLeast>(P, backward, stream);
-    case 2: return launch_g<T, 2 * kLeast>(P, backward, stream);
-    case 4: return launch_g<T, 4 * kLeast>(P, backward, stream);
-    default: return launch_g<T, 8 * kLeast>(P, backward, stream);
+    case 1: return launch_g<T, kLeast>(P, backward, stream, blocks);
+    case 2: return launch_g<T, 2 * kLeast>(P, backward, stream, blocks);
+    case 4: return launch_g<T, 4 * kLeast>(P, backward, stream, blocks);
+    default: return launch_g<T, 8 * kLeast>(P, backward, stream, blocks);
   }
 }
 
@@ -703,7 +706,7 @@ gdn_status run(const Call& c) {
   P.T = c.T;
   P.D = c.D;
   P.R = R;
-  P.tokens = (long long)c.B * c.T;
+  P.tokens = (unsigned)c.B * c.T;
   P.eps = c.eps;
   P.norm = c.norm;
   P.inverse = c.inverse;
@@ -718,20 +721,20 @@ gdn_status run(const Call& c) {
     P.amplitude = r->amplitude;
     P.interleaved = r->layout == GDN_ROPE_INTERLEAVED;
   }
+  unsigned blocks = 0;
   if (!c.backward) {
-    const cudaError_t e = c.dtype == GDN_BF16 ? launch_t<__nv_bfloat16>(P, false, stream)
-                                              : launch_t<float>(P, false, stream);
+    const cudaError_t e = c.dtype == GDN_BF16 ? launch_t<__nv_bfloat16>(P, false, stream, &blocks)
+                                              : launch_t<float>(P, false, stream, &blocks);
     return finish(stream, e, nullptr);
   }
   OpScratch sc;
   unsigned int* err = nullptr;
-  // a row of partial sums per block: at most two blocks an SM, and one a side
-  const gdn_status st =
-      op_scratch(dev, stream, (size_t)(2 * num_sms() + 2) * c.D * sizeof(float), &err, &sc);
+  // two rows of partial sums per block, at most two blocks an SM
+  const gdn_status st = op_scratch(dev, stream, (size_t)4 * num_sms() * c.D * sizeof(float), &err, &sc);
   if (st != GDN_OK) return st;
   P.partial = static_cast<float*>(sc.p);
-  cudaError_t e = c.dtype == GDN_BF16 ? launch_t<__nv_bfloat16>(P, true, stream)
-                                      : launch_t<float>(P, true, stream);
+  cudaError_t e = c.dtype == GDN_BF16 ? launch_t<__nv_bfloat16>(P, true, stream, &blocks)
+                                      : launch_t<float>(P, true, stream, &blocks);
   if (e == cudaSuccess && (c.dw[0] || c.dw[1])) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(c.D / kRedCols, 2);
@@ -743,8 +746,8 @@ gdn_status run(const Call& c) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     ProfileScope ps(stream, kKernNormRopeReduce);
-    e = cudaLaunchKernelEx(&cfg, gdn_norm_rope_reduce_kernel, (const float*)P.partial,
-                           P.side[0].blocks, P.side[1].blocks, c.D, c.dw[0], c.dw[1]);
+    e = cudaLaunchKernelEx(&cfg, gdn_norm_rope_reduce_kernel, (const float*)P.partial, blocks, c.D,
+                           c.dw[0], c.dw[1]);
     if (e == cudaSuccess) count_launches(1);
   }
   const cudaError_t f = op_scratch_done(sc);
