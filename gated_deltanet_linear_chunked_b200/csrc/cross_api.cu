@@ -44,7 +44,8 @@ gdn_status check_inputs(const gdn_rows* q, const gdn_rows* k, const gdn_rows* v,
                         gdn_dtype dtype, void* stream, Checked* o) {
   if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
   if (B < 0 || Tq < 0 || S < 0 || Hq < 0 || Hk < 0 || D < 0) return GDN_ERR_INVALID_ARG;
-  if (!(scale >= 0.f) || std::isinf(scale)) return GDN_ERR_INVALID_ARG;
+  // 0 times the -infinity of a masked score is no number
+  if (!(scale > 0.f) || !std::isnormal(scale) || !std::isnormal(scale * 1.5f)) return GDN_ERR_INVALID_ARG;
   if (mask_bs < 0 || mask_bs > kMaxStride) return GDN_ERR_INVALID_ARG;
   if (dtype != GDN_BF16 || !supported_dim(D)) return GDN_ERR_UNSUPPORTED;
   if (Hq > 0 && (Hk == 0 || Hq % Hk)) return GDN_ERR_INVALID_ARG;

@@ -62,14 +62,15 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kQTiles = 2;
 constexpr int kRows = 128;             // rows of a query tile, keys of a key tile
 constexpr int kHalf = kRows / 2;       // keys of a softmax thread
-constexpr int kSlots = 4;              // ring of K and V tiles
-constexpr int kSoftmaxWarps = 8 * kQTiles;  // two groups of four warps per query tile
-constexpr int kProducerWarp = kSoftmaxWarps;
-constexpr int kMmaWarp = kProducerWarp + 1;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+template <int NQ>  // query tiles of a CTA
+struct Roles {
+  static constexpr int softmax_warps = 8 * NQ;  // two groups of four warps per query tile
+  static constexpr int producer = softmax_warps, mma = producer + 1;
+  static constexpr int threads = 32 * (mma + 1);
+  static constexpr int slots = 2 * NQ;          // ring of K and V tiles
+};
 constexpr uint32_t kTileCols = 256;    // TMEM columns of a tile: S (and P) [0, 128) | O [128, 128 + D)
 constexpr uint32_t kBlock = kRows * 128;  // one 64-feature block of a 128-row tile, bytes
 constexpr int kMaskTiles = 128;        // key tiles of one CTA under a mask, at most
@@ -79,41 +80,42 @@ constexpr long long kDrainPolls = 1LL << 40;  // drains are bounded by the 2 s t
 struct CrossParams {
   int Tq, S, Hk, G, D;
   int tokens;            // query tokens per tile: 128 / G
-  int qtiles, groups;    // query tiles of a (b, key head); CTAs along them (nq tiles each)
-  int nq;
-  int ntiles, nsplit, per_split;  // key tiles, CTAs along them, tiles of each
+  int qtiles, groups;    // query tiles of a (b, key head); units along them (NQ tiles each)
+  int ntiles;            // key tiles
+  unsigned full;         // units that one CTA each takes whole; those behind them ...
+  int nsplit, per_split; // ... are split along the keys: CTAs of a unit, tiles of each
   int qb, kb, vb;        // batch coordinate factors: 0 for a broadcast batch
   const uint8_t* mask;
   long long mask_bs;
   float scale_log2;      // scale * log2(e)
   float* lse;            // [B, Hq, Tq] or nullptr
-  float* part_o;         // nsplit > 1: [nsplit][B, Tq, Hq][D] fp32
-  float* part_lse;       // nsplit > 1: [nsplit][B, Tq, Hq]
-  long long rows;        // B * Tq * Hq
+  float* part_o;         // [split units][nsplit][NQ * 128 rows][D] fp32
+  float* part_lse;       // [split units][nsplit][NQ * 128 rows]
   long long limit;
   unsigned* err;
 };
 
+template <int NQ>
 struct CrossAux {
   uint64_t q_full;
-  uint64_t full[kSlots], empty[kSlots];
-  uint64_t s_full[kQTiles], p_full[kQTiles][2], o_full[kQTiles], drain;
+  uint64_t full[Roles<NQ>::slots], empty[Roles<NQ>::slots];
+  uint64_t s_full[NQ], p_full[NQ][2], o_full[NQ], drain;
   uint32_t tmem;
   int abort;
   int count;                       // key tiles to walk
-  float row[kQTiles][2][kRows];    // a row's two halves exchange maxima, later sums
+  float row[NQ][2][kRows];    // a row's two halves exchange maxima, later sums
   uint32_t bits[kMaskTiles * 4];   // seen keys of each of the CTA's tiles (under a mask)
   uint8_t list[kMaskTiles];        // tiles with any
 };
 
 // Shared memory: Q tiles (later the output's), the ring, the barriers and mask.
-template <int NB>  // 64-feature blocks of a head
+template <int NB, int NQ>  // 64-feature blocks of a head, query tiles
 struct CrossLayout {
   static constexpr uint32_t tile = NB * kBlock;
   static constexpr uint32_t q = 0;
-  static constexpr uint32_t ring = kQTiles * tile;
-  static constexpr uint32_t aux = ring + kSlots * tile;
-  static constexpr uint32_t total = aux + (uint32_t)sizeof(CrossAux);
+  static constexpr uint32_t ring = NQ * tile;
+  static constexpr uint32_t aux = ring + Roles<NQ>::slots * tile;
+  static constexpr uint32_t total = aux + (uint32_t)sizeof(CrossAux<NQ>);
 };
 
 // 32 scores of a row, those of masked keys -inf whatever they were.
@@ -127,32 +129,36 @@ __device__ __forceinline__ void scores(uint32_t taddr, uint32_t seen, float (&s)
   }
 }
 
-template <int NB>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int NB, int NQ>
+__global__ void __launch_bounds__(Roles<NQ>::threads, 3 - NQ)
 gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_out,
                  const __grid_constant__ CrossParams P) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int D = P.D;
-  constexpr int nb = NB;
-  using L = CrossLayout<NB>;
-  CrossAux& aux = *reinterpret_cast<CrossAux*>(smem + L::aux);
+  constexpr int nb = NB, kSlots = Roles<NQ>::slots;
+  using L = CrossLayout<NB, NQ>;
+  CrossAux<NQ>& aux = *reinterpret_cast<CrossAux<NQ>*>(smem + L::aux);
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;  // uniform
-  // unit: ((b * Hk + hk) * groups + group) * nsplit + split
-  const int split = blockIdx.x % P.nsplit, u = blockIdx.x / P.nsplit;
+  // unit: (b * Hk + hk) * groups + group
+  const bool whole = blockIdx.x < P.full;
+  const unsigned x = blockIdx.x - P.full;
+  const int split = whole ? 0 : x % P.nsplit;
+  const unsigned u = whole ? blockIdx.x : P.full + x / P.nsplit;
   const int group = u % P.groups, bh = u / P.groups;
   const int b = bh / P.Hk, hk = bh - b * P.Hk;
-  const int tile0 = group * P.nq, nq = min(P.nq, P.qtiles - tile0);
-  const int k0 = split * P.per_split, kn = min(P.per_split, P.ntiles - k0);  // key tiles of the split
+  const int tile0 = group * NQ, nq = min(NQ, P.qtiles - tile0);
+  const int k0 = split * P.per_split;                               // key tiles k0 .. k0 + kn - 1
+  const int kn = whole ? P.ntiles : min(P.per_split, P.ntiles - k0);
   volatile int* abort_flag = &aux.abort;
 
-  if (tid == 0) {
+  if (warp == Roles<NQ>::producer && lane == 0) {
     mbar_init(&aux.q_full, 1);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&aux.full[s], 1);
       mbar_init(&aux.empty[s], 1);
     }
-    for (int g = 0; g < kQTiles; ++g) {
+    for (int g = 0; g < NQ; ++g) {
       mbar_init(&aux.s_full[g], 1);
       mbar_init(&aux.p_full[g][0], kRows);
       mbar_init(&aux.p_full[g][1], kRows);
@@ -162,14 +168,22 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     aux.abort = 0;
     aux.count = kn;
     fence_mbar_init();
+    // the queries are on their way while the CTA sets up and reads its mask
+    const uint32_t qbytes = (uint32_t)P.tokens * P.G * 128;  // of one 64-feature block
+    mbar_arrive_expect_tx(&aux.q_full, nq * nb * qbytes);
+    for (int g = 0; g < nq; ++g)
+      for (int c = 0; c < nb; ++c)
+        tma_load_5d(smem + L::q + g * L::tile + c * kBlock, &tm_q, &aux.q_full, c * 64, 0,
+                    (tile0 + g) * P.tokens, hk, b * P.qb);
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(&aux.tmem, kTileCols * kQTiles);
+  if (warp == Roles<NQ>::mma) {
+    tmem_alloc(&aux.tmem, kTileCols * NQ);
     tmem_relinquish();
   }
   if (P.mask) {
     const uint8_t* mrow = P.mask + b * P.mask_bs;
-    for (int w = warp; w < kn * 4; w += kThreads / 32) {
+    for (int w = warp; w < kn * 4; w += Roles<NQ>::softmax_warps) {
+      if (warp >= Roles<NQ>::softmax_warps) break;
       const long long key = (long long)(k0 * 4 + w) * 32 + lane;
       const uint32_t bits = __ballot_sync(~0u, key < P.S && mrow[key] != 0);
       if (lane == 0) aux.bits[w] = bits;
@@ -193,7 +207,8 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     __syncthreads();
   }
-  const uint32_t tm = 0;  // all 512 columns: the allocation starts at the first
+  // two tiles hold all 512 columns, an allocation that starts at the first
+  const uint32_t tm = NQ == 2 ? 0u : aux.tmem;
   const int n = aux.count;
   const bool masked = P.mask != nullptr;
   auto fail = [&]() {
@@ -204,14 +219,8 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   auto slot_ptr = [&](int i) { return smem + L::ring + (i % kSlots) * L::tile; };
   auto wait_full = [&](int i) { return mbar_wait(&aux.full[i % kSlots], (i / kSlots) & 1, P.limit); };
 
-  if (warp == kProducerWarp) {
-    if (lane == 0 && n > 0) {
-      const uint32_t qbytes = (uint32_t)P.tokens * P.G * 128;  // of one 64-feature block
-      mbar_arrive_expect_tx(&aux.q_full, nq * nb * qbytes);
-      for (int g = 0; g < nq; ++g)
-        for (int c = 0; c < nb; ++c)
-          tma_load_5d(smem + L::q + g * L::tile + c * kBlock, &tm_q, &aux.q_full, c * 64, 0,
-                      (tile0 + g) * P.tokens, hk, b * P.qb);
+  if (warp == Roles<NQ>::producer) {
+    if (lane == 0) {
       int issued = 0;
       for (int i = 0; i < 2 * n; ++i) {
         if (*abort_flag) break;
@@ -232,7 +241,7 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       for (int i = max(0, issued - kSlots); i < issued; ++i)
         mbar_wait(&aux.full[i % kSlots], (i / kSlots) & 1, kDrainPolls);
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == Roles<NQ>::mma) {
     if (n > 0) {  // the whole warp walks the loop, one elected lane issues
       const uint32_t idS = idesc_bf16(kRows, kRows, 0, 0), idO = idesc_bf16(kRows, D, 0, 1);
       const uint64_t dq = sdesc_sw128(smem_u32(smem + L::q), 16);
@@ -411,7 +420,8 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       f2_unpack(sa, rs0, rs1);
       l_run = l_run * alpha + (rs0 + rs1);
     }
-    if (ok && n > 0 && !__all_sync(~0u, mbar_wait(&aux.o_full[g], 0, P.limit))) {
+    // the last product; without any, the queries, whose buffer takes the zeros
+    if (ok && !__all_sync(~0u, mbar_wait(n > 0 ? &aux.o_full[g] : &aux.q_full, 0, P.limit))) {
       fail();
       ok = false;
     }
@@ -425,42 +435,47 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const bool row = r < P.tokens * P.G && t < P.Tq;
       const float lse = n > 0 ? (m_run + log2f(l_run)) * 0.6931471805599453f : -INFINITY;
       const float inv = n > 0 ? 1.f / l_run : 0.f;
-      if (P.nsplit > 1) {
-        const long long at = (long long)split * P.rows + ((long long)b * P.Tq + t) * Hq + head;
-        if (row && half == 0) P.part_lse[at] = lse;
+      if (!whole) {
+        const long long at = ((long long)x * NQ + g) * kRows + r;  // x: split unit * nsplit + split
+        if (half == 0) P.part_lse[at] = lse;
         if (n > 0) {
           for (int c0 = oc0; c0 < oc1; c0 += 16) {
             float o[16];
             tmem_ld16(tO + c0, o);
             tmem_wait_ld();
-            if (row) {
-              float4* to = reinterpret_cast<float4*>(P.part_o + at * D + c0);
+            float4* to = reinterpret_cast<float4*>(P.part_o + at * D + c0);
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                to[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
-            }
+            for (int e = 0; e < 4; ++e)
+              to[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
           }
         }
       } else {
         if (row && half == 0 && P.lse) P.lse[((long long)b * Hq + head) * P.Tq + t] = lse;
-        // every S MMA has completed (or none was issued and Q never loaded):
-        // the tile's Q buffer takes its output
+        // every S MMA has completed: the tile's Q buffer takes its output
         uint8_t* so = smem + L::q + g * L::tile + r * 128;
-        for (int c0 = oc0; c0 < oc1; c0 += 16) {
-          float o[16];
-          if (n > 0) {
-            tmem_ld16(tO + c0, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] *= inv;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = 0.f;
-          }
+        auto put = [&](int c0, const float* o) {  // 16 columns from c0
           uint8_t* blk = so + (c0 >> 6) * kBlock;
           const int c = (c0 & 63) >> 3;
           *reinterpret_cast<uint4*>(blk + ((c ^ (r & 7)) << 4)) = pack8_bf16(o);
           *reinterpret_cast<uint4*>(blk + (((c + 1) ^ (r & 7)) << 4)) = pack8_bf16(o + 8);
+        };
+        for (int c0 = oc0; c0 < oc1; c0 += 32) {
+          float o[32];
+          const bool two = c0 + 16 < oc1;
+          if (n > 0) {
+            if (two)
+              tmem_ld32(tO + c0, o);
+            else
+              tmem_ld16(tO + c0, *reinterpret_cast<float(*)[16]>(o));
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= inv;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
+          put(c0, o);
+          if (two) put(c0 + 16, o + 16);
         }
         fence_proxy_async_smem();
         named_barrier(1 + g, 2 * kRows);
@@ -468,57 +483,68 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           for (int c = 0; c < nb; ++c)
             tma_store_5d(&tm_out, smem + L::q + g * L::tile + c * kBlock, c * 64, 0, (tile0 + g) * P.tokens, hk, b);
           bulk_commit();
-          bulk_wait_all();
+          bulk_wait_read();  // shared memory may go; the writes land before the grid ends
         }
       }
     }
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == Roles<NQ>::mma) {
     tc_fence_after_sync();
-    tmem_dealloc(aux.tmem, kTileCols * kQTiles);
+    tmem_dealloc(aux.tmem, kTileCols * NQ);
   }
 }
 
 // Joins the splits: out = sum_i w_i o_i with w_i = e^(lse_i - lse).  A warp per
-// row, four features a lane.
+// row of the split units, four features a lane.
 constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads)
-gdn_cross_join_kernel(const __grid_constant__ CrossParams P, __nv_bfloat16* out) {
-  const long long row = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int nq, long long rows, __nv_bfloat16* out) {
+  const long long i = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (row >= P.rows) return;
+  if (i >= rows) return;
+  const int per = nq * kRows;                         // rows of a unit
+  const long long su = i / per;
+  const int ur = (int)(i - su * per), r = ur % kRows;
+  const long long u = P.full + su, bh = u / P.groups;
+  const int tile = (int)(u - bh * P.groups) * nq + ur / kRows;
+  const long long b = bh / P.Hk;
+  const int hk = (int)(bh - b * P.Hk), t = tile * P.tokens + r / P.G, head = hk * P.G + r % P.G;
+  if (r >= P.tokens * P.G || t >= P.Tq) return;       // no row
+  const long long at = su * P.nsplit * per + ur;      // of split 0, then every `per`
   float top = -INFINITY;
-  for (int i = 0; i < P.nsplit; ++i) top = fmaxf(top, P.part_lse[i * P.rows + row]);
+  for (int s = 0; s < P.nsplit; ++s) top = fmaxf(top, P.part_lse[at + (long long)s * per]);
   const bool any = top > -INFINITY;
   float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
   const int f = lane * 4;
-  for (int i = 0; any && i < P.nsplit; ++i) {
-    const float w = expf(P.part_lse[i * P.rows + row] - top);
+  for (int s = 0; any && s < P.nsplit; ++s) {
+    const float w = expf(P.part_lse[at + (long long)s * per] - top);
     sum += w;
     if (w > 0.f && f < P.D) {  // a split that saw nothing left no part
-      const float4 x = *reinterpret_cast<const float4*>(P.part_o + (i * P.rows + row) * P.D + f);
-      o[0] += w * x.x;
-      o[1] += w * x.y;
-      o[2] += w * x.z;
-      o[3] += w * x.w;
+      const float4 v = *reinterpret_cast<const float4*>(P.part_o + (at + (long long)s * per) * P.D + f);
+      o[0] += w * v.x;
+      o[1] += w * v.y;
+      o[2] += w * v.z;
+      o[3] += w * v.w;
     }
   }
   const float inv = any ? 1.f / sum : 0.f;
-  if (f < P.D) {
-    uint2 u = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-    *reinterpret_cast<uint2*>(out + row * P.D + f) = u;
-  }
-  if (lane == 0 && P.lse) {
-    const int Hq = P.Hk * P.G;
-    const long long bt = row / Hq, b = bt / P.Tq;
-    P.lse[(b * Hq + (row - bt * Hq)) * P.Tq + (bt - b * P.Tq)] = any ? top + logf(sum) : -INFINITY;
-  }
+  const int Hq = P.Hk * P.G;
+  if (f < P.D)
+    *reinterpret_cast<uint2*>(out + ((b * P.Tq + t) * Hq + head) * P.D + f) =
+        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+  if (lane == 0 && P.lse) P.lse[(b * Hq + head) * P.Tq + t] = any ? top + logf(sum) : -INFINITY;
 }
 
-// The shape of a call: tiles, CTAs along queries and splits along keys.
-void cross_shape(const CrossCall& c, CrossParams* P) {
+#ifdef CROSS_FORCE
+int cross_force() { const char* s = getenv("CROSS_NQ"); return s ? atoi(s) : 4; }
+#else
+int cross_force() { return 4; }
+#endif
+// The shape of a call: query tiles of a CTA, units, splits along the keys.
+// Returns the query tiles of a CTA.
+int cross_shape(const CrossCall& c, CrossParams* P) {
   P->Tq = c.Tq;
   P->S = c.S;
   P->Hk = c.Hk;
@@ -526,27 +552,42 @@ void cross_shape(const CrossCall& c, CrossParams* P) {
   P->D = c.D;
   P->tokens = kRows / P->G;
   P->qtiles = (c.Tq + P->tokens - 1) / P->tokens;
-  P->nq = std::min(kQTiles, P->qtiles);
-  P->groups = (P->qtiles + P->nq - 1) / P->nq;
   P->ntiles = (c.S + kRows - 1) / kRows;
-  P->rows = (long long)c.B * c.Tq * c.Hq;
-  // split the keys while a CTA keeps at least two tiles and the GPU has room
+  const int nq = P->ntiles <= cross_force() ? 1 : 2;
+  P->groups = (P->qtiles + nq - 1) / nq;
   const long long units = (long long)c.B * c.Hk * P->groups;
-  long long n = std::max<long long>(1, std::min<long long>(num_sms() / units, P->ntiles / 2));
-  if (c.mask) n = std::max<long long>(n, (P->ntiles + kMaskTiles - 1) / kMaskTiles);
+  const long long slots = num_sms() * (3 - nq);  // CTAs that run at a time
+  // Units of a last, partial wave are split along the keys while a CTA keeps at
+  // least two tiles, so that the wave is full and shorter; with fewer units than
+  // slots that is all of them.
+  const long long rest = units % slots;
+  long long n = rest ? std::max<long long>(1, std::min<long long>(slots / rest, P->ntiles / 2)) : 1;
+  P->full = n > 1 ? (unsigned)(units - rest) : (unsigned)units;
+  if (c.mask && P->ntiles > kMaskTiles) {  // what a CTA can list
+    n = std::max<long long>(n, (P->ntiles + kMaskTiles - 1) / kMaskTiles);
+    P->full = 0;
+  }
   P->per_split = (int)std::max<long long>(1, (P->ntiles + n - 1) / n);
   P->nsplit = std::max(1, (P->ntiles + P->per_split - 1) / P->per_split);
+  return nq;
 }
 
-template <int NB>
+// CTAs of the split units.
+long long split_blocks(const CrossCall& c, const CrossParams& P) {
+  return ((long long)c.B * c.Hk * P.groups - P.full) * P.nsplit;
+}
+
+template <int NB, int NQ>
 cudaError_t launch_nb(unsigned grid, cudaStream_t stream, const CUtensorMap& mq, const CUtensorMap& mk,
                       const CUtensorMap& mv, const CUtensorMap& mo, const CrossParams& P) {
-  // more than half an SM's shared memory: one CTA (all of TMEM) per SM
-  constexpr int bytes = CrossLayout<NB>::total > 116 * 1024 ? CrossLayout<NB>::total : 116 * 1024;
-  const cudaError_t e = allow_smem(gdn_cross_kernel<NB>, bytes);
+  // more than a third (half) of an SM's shared memory: two CTAs (one) per SM, as
+  // many as tensor memory has columns for
+  constexpr int least = NQ == 1 ? 80 * 1024 : 116 * 1024;
+  constexpr int bytes = CrossLayout<NB, NQ>::total > least ? CrossLayout<NB, NQ>::total : least;
+  const cudaError_t e = allow_smem(gdn_cross_kernel<NB, NQ>, bytes);
   if (e != cudaSuccess) return e;
   ProfileScope ps(stream, kKernCross);
-  gdn_cross_kernel<NB><<<grid, kThreads, bytes, stream>>>(mq, mk, mv, mo, P);
+  gdn_cross_kernel<NB, NQ><<<grid, Roles<NQ>::threads, bytes, stream>>>(mq, mk, mv, mo, P);
   return cudaSuccess;
 }
 
@@ -554,19 +595,20 @@ cudaError_t launch_nb(unsigned grid, cudaStream_t stream, const CUtensorMap& mq,
 
 size_t cross_workspace_bytes(const CrossCall& c) {
   CrossParams P = {};
-  cross_shape(c, &P);
-  return P.nsplit > 1 ? (size_t)P.nsplit * P.rows * (c.D + 1) * sizeof(float) : 0;
+  const int nq = cross_shape(c, &P);
+  return (size_t)split_blocks(c, P) * nq * kRows * (c.D + 1) * sizeof(float);
 }
 
 cudaError_t launch_cross(const CrossCall& c, void* ws) {
   CrossParams P = {};
-  cross_shape(c, &P);
+  const int nq = cross_shape(c, &P);
+  const long long parts = split_blocks(c, P);
   P.mask = c.mask;
   P.mask_bs = c.mask_bs;
   P.scale_log2 = c.scale * 1.4426950408889634f;
   P.lse = c.lse;
   P.part_o = static_cast<float*>(ws);
-  P.part_lse = P.part_o + (size_t)P.nsplit * P.rows * c.D;
+  P.part_lse = P.part_o + (size_t)parts * nq * kRows * c.D;
   P.limit = c.limit;
   P.err = c.err;
   P.qb = c.q.batch_stride != 0;
@@ -586,17 +628,22 @@ cudaError_t launch_cross(const CrossCall& c, void* ws) {
                              c.v.token_stride, kRows)) {
     return cudaErrorInvalidValue;
   }
-  const unsigned grid = (unsigned)((long long)c.B * c.Hk * P.groups * P.nsplit);
-  cudaError_t e = c.D > 64 ? launch_nb<2>(grid, c.stream, mq, mk, mv, mo, P)
-                           : launch_nb<1>(grid, c.stream, mq, mk, mv, mo, P);
-  if (e != cudaSuccess) return e;
-  e = cudaGetLastError();
+  const unsigned grid = (unsigned)(P.full + parts);
+  cudaError_t e;
+  if (nq == 1)
+    e = c.D > 64 ? launch_nb<2, 1>(grid, c.stream, mq, mk, mv, mo, P)
+                 : launch_nb<1, 1>(grid, c.stream, mq, mk, mv, mo, P);
+  else
+    e = c.D > 64 ? launch_nb<2, 2>(grid, c.stream, mq, mk, mv, mo, P)
+                 : launch_nb<1, 2>(grid, c.stream, mq, mk, mv, mo, P);
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   count_launches(1);
-  if (P.nsplit > 1) {
+  if (parts > 0) {
     ProfileScope ps(c.stream, kKernCrossJoin);
-    const unsigned blocks = (unsigned)((P.rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
-    gdn_cross_join_kernel<<<blocks, kJoinThreads, 0, c.stream>>>(P, static_cast<__nv_bfloat16*>(c.out));
+    const long long rows = parts / P.nsplit * nq * kRows;
+    gdn_cross_join_kernel<<<(unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)), kJoinThreads, 0,
+                            c.stream>>>(P, nq, rows, static_cast<__nv_bfloat16*>(c.out));
     e = cudaGetLastError();
     if (e == cudaSuccess) count_launches(1);
   }

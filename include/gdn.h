@@ -415,7 +415,7 @@ GDN_API gdn_status gdn_qk_norm_rope_backward(const gdn_rows* q, const gdn_rows* 
  *   lse                    [B, Hq, Tq] fp32, or NULL; the backward needs it
  *
  * Requirements: dtype GDN_BF16 and D a multiple of 16 in [16, 128] (else
- * GDN_ERR_UNSUPPORTED); Hq a multiple of Hk, scale finite and not negative (else
+ * GDN_ERR_UNSUPPORTED); Hq a multiple of Hk, scale a positive normal number (else
  * GDN_ERR_INVALID_ARG); Hq / Hk at most 128, sizes whose products of a launch
  * stay below 2^31 (else GDN_ERR_UNSUPPORTED).  out and lse must not overlap
  * anything (GDN_ERR_ALIAS).  B, Tq or Hq zero: nothing to do.  Errors and the
