@@ -86,6 +86,8 @@ def library_path() -> str:
 def load() -> ctypes.CDLL:
     """Load libgdn.so (building it first if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -102,7 +104,7 @@ def load() -> ctypes.CDLL:
             fn = getattr(lib, name)  # AttributeError if the symbol is missing
             fn.restype = res
             fn.argtypes = args
-        _lib = lib
+        _lib = lib  # complete from here on: read without the lock
         return lib
 
 

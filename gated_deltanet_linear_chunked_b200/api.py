@@ -190,6 +190,7 @@ def sink_window_attention(q, k, v, k_cache, v_cache, chunk_index, n_sink, window
 
 _LAYOUTS = {"half": _lib.GDN_ROPE_HALF, "interleaved": _lib.GDN_ROPE_INTERLEAVED}
 _POSITION_BYTES = {torch.int32: 4, torch.int64: 8}
+_pack_rows = _lib.ROWS.pack
 
 
 def _raw_stream(stream, device):
@@ -199,20 +200,19 @@ def _raw_stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _fresh(stream, make, *args, **kw):
-    """A new tensor from `make`, from the memory of the stream it is used on."""
+def _fresh(stream, like, shape, dtype=None):
+    """A new tensor on `like`'s device, from the memory of the stream it is used on."""
     if stream is None:
-        return make(*args, **kw)
+        return like.new_empty(shape, dtype=dtype) if dtype is not None else like.new_empty(shape)
     with torch.cuda.stream(stream):
-        return make(*args, **kw)
+        return like.new_empty(shape, dtype=dtype or like.dtype)
 
 
 def _used_on(stream, *tensors):
     """Keeps tensors of another stream alive until `stream` is done with them."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _view(t, name, dtype, shape):
@@ -227,9 +227,9 @@ def _view(t, name, dtype, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     sb, st, sh, sd = t.stride()
     B, T, H, D = shape
-    if B * T * H and (sd != 1 or (H > 1 and sh != D)):
+    if (sd != 1 or (sh != D and H > 1)) and B * T * H:
         raise ValueError(f"{name} must have contiguous heads and features")
-    return _lib.ROWS.pack(t.data_ptr(), sb if B > 1 else 0, st if T > 1 else 0)
+    return _pack_rows(t.data_ptr(), sb if B > 1 else 0, st if T > 1 else 0)
 
 
 def rope_frequencies(dim, base=10000.0, sections=None, scaling="none", factor=1.0,
@@ -331,11 +331,13 @@ def _weight(w, name, D):
     return _ptr(w)
 
 
-def _out_view(t, name, dtype, shape, stream, device):
-    """`t`, or a new tensor where it is None, and its gdn_rows."""
-    if t is None:
-        t = _fresh(stream, torch.empty, shape, dtype=dtype, device=device)
-    return t, _view(t, name, dtype, shape)
+def _out_view(t, name, like, shape, stream):
+    """`t`, or a new tensor like `like` where it is None, and its gdn_rows."""
+    if t is not None:
+        return t, _view(t, name, like.dtype, shape)
+    t = _fresh(stream, like, shape)
+    B, T, H, D = shape
+    return t, _pack_rows(t.data_ptr(), T * H * D, H * D)
 
 
 def _turn(q, k, positions, inv_freq, sections, layout, amplitude, inverse, q_out, k_out, stream):
@@ -345,14 +347,15 @@ def _turn(q, k, positions, inv_freq, sections, layout, amplitude, inverse, q_out
     rot = _rotation(positions, inv_freq, sections, layout, amplitude, B, T)
     if rot is None:
         raise ValueError("rope needs positions and inv_freq")
-    q_out, oq = _out_view(q_out, "q_out", dt, qs, stream, dev)
+    q_out, oq = _out_view(q_out, "q_out", q, qs, stream)
     ok = None
     if k is not None:
-        k_out, ok = _out_view(k_out, "k_out", dt, ks, stream, dev)
+        k_out, ok = _out_view(k_out, "k_out", q, ks, stream)
     st = _lib.load().gdn_rope(vq, vk, rot, inverse, oq, ok, B, T, Hq, Hk, D, code,
                               _raw_stream(stream, dev))
     _lib.check(st, "gdn_rope")
-    _used_on(stream, q, k, positions, inv_freq, q_out, k_out)
+    if stream is not None:
+        _used_on(stream, q, k, positions, inv_freq, q_out, k_out)
     return q_out, k_out
 
 
@@ -387,14 +390,15 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=No
     vq, vk = _view(q, "q", dt, qs), None if k is None else _view(k, "k", dt, ks)
     wq, wk = _weight(q_weight, "q_weight", D), _weight(k_weight, "k_weight", D)
     rot = _rotation(positions, inv_freq, sections, layout, amplitude, B, T)
-    q_out, oq = _out_view(q_out, "q_out", dt, qs, stream, dev)
+    q_out, oq = _out_view(q_out, "q_out", q, qs, stream)
     ok = None
     if k is not None:
-        k_out, ok = _out_view(k_out, "k_out", dt, ks, stream, dev)
+        k_out, ok = _out_view(k_out, "k_out", q, ks, stream)
     st = _lib.load().gdn_qk_norm_rope(vq, vk, wq, wk, rot, oq, ok, B, T, Hq, Hk, D, eps, code,
                                       _raw_stream(stream, dev))
     _lib.check(st, "gdn_qk_norm_rope")
-    _used_on(stream, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out)
+    if stream is not None:
+        _used_on(stream, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out)
     return q_out, k_out
 
 
@@ -411,17 +415,18 @@ def qk_norm_rope_backward(q, k, q_weight, k_weight, dq_out, dk_out, positions=No
     rot = _rotation(positions, inv_freq, sections, layout, amplitude, B, T)
     gq = _view(dq_out, "dq_out", dt, qs)
     gk = None if k is None else _view(dk_out, "dk_out", dt, ks)
-    dq, oq = _out_view(dq, "dq", dt, qs, stream, dev)
-    dqw = _fresh(stream, torch.empty, (D,), dtype=torch.float32, device=dev)
+    dq, oq = _out_view(dq, "dq", q, qs, stream)
+    dqw = _fresh(stream, q, (D,), torch.float32)
     ok = dkw = None
     if k is not None:
-        dk, ok = _out_view(dk, "dk", dt, ks, stream, dev)
-        dkw = _fresh(stream, torch.empty, (D,), dtype=torch.float32, device=dev)
+        dk, ok = _out_view(dk, "dk", q, ks, stream)
+        dkw = _fresh(stream, q, (D,), torch.float32)
     st = _lib.load().gdn_qk_norm_rope_backward(vq, vk, wq, wk, rot, gq, gk, oq, ok, dqw.data_ptr(),
                                                _ptr(dkw), B, T, Hq, Hk, D, eps, code,
                                                _raw_stream(stream, dev))
     _lib.check(st, "gdn_qk_norm_rope_backward")
-    _used_on(stream, q, k, q_weight, k_weight, positions, inv_freq, dq_out, dk_out, dq, dk, dqw, dkw)
+    if stream is not None:
+        _used_on(stream, q, k, q_weight, k_weight, positions, inv_freq, dq_out, dk_out, dq, dk, dqw, dkw)
     return {"dq": dq, "dk": dk, "dq_weight": dqw, "dk_weight": dkw}
 
 
@@ -464,16 +469,17 @@ def cross_attention(q, k, v, key_mask=None, *, scale=None, out=None, return_lse=
     B, Tq, S, Hq, Hk, D, vq, vk, vv, mp, ms, scale = _cross_args(q, k, v, key_mask, scale)
     dev = q.device
     if out is None:
-        out = _fresh(stream, torch.empty, (B, Tq, Hq, D), dtype=torch.bfloat16, device=dev)
+        out = _fresh(stream, q, (B, Tq, Hq, D))
     else:
         _check_tensor(out, "out", torch.bfloat16, (B, Tq, Hq, D))
     lse = None
     if return_lse:
-        lse = _fresh(stream, torch.empty, (B, Hq, Tq), dtype=torch.float32, device=dev)
+        lse = _fresh(stream, q, (B, Hq, Tq), torch.float32)
     st = _lib.load().gdn_cross_attention(vq, vk, vv, mp, ms, out.data_ptr(), _ptr(lse), B, Tq, S, Hq,
                                          Hk, D, scale, _lib.GDN_BF16, _raw_stream(stream, dev))
     _lib.check(st, "gdn_cross_attention")
-    _used_on(stream, q, k, v, key_mask, out, lse)
+    if stream is not None:
+        _used_on(stream, q, k, v, key_mask, out, lse)
     return (out, lse) if return_lse else out
 
 
@@ -486,15 +492,16 @@ def cross_attention_backward(q, k, v, out, lse, d_out, key_mask=None, *, scale=N
     _check_tensor(out, "out", torch.bfloat16, (B, Tq, Hq, D))
     _check_tensor(lse, "lse", torch.float32, (B, Hq, Tq))
     _check_tensor(d_out, "d_out", torch.bfloat16, (B, Tq, Hq, D))
-    dq = _fresh(stream, torch.empty, (B, Tq, Hq, D), dtype=torch.bfloat16, device=dev)
-    dk = _fresh(stream, torch.empty, (B, S, Hk, D), dtype=torch.bfloat16, device=dev)
-    dv = _fresh(stream, torch.empty, (B, S, Hk, D), dtype=torch.bfloat16, device=dev)
+    dq = _fresh(stream, q, (B, Tq, Hq, D))
+    dk = _fresh(stream, q, (B, S, Hk, D))
+    dv = _fresh(stream, q, (B, S, Hk, D))
     st = _lib.load().gdn_cross_attention_backward(
         vq, vk, vv, mp, ms, out.data_ptr(), lse.data_ptr(), d_out.data_ptr(), dq.data_ptr(),
         dk.data_ptr(), dv.data_ptr(), B, Tq, S, Hq, Hk, D, scale, _lib.GDN_BF16,
         _raw_stream(stream, dev))
     _lib.check(st, "gdn_cross_attention_backward")
-    _used_on(stream, q, k, v, key_mask, out, lse, d_out, dq, dk, dv)
+    if stream is not None:
+        _used_on(stream, q, k, v, key_mask, out, lse, d_out, dq, dk, dv)
     return {"dq": dq, "dk": dk, "dv": dv}
 
 

@@ -180,6 +180,7 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     tmem_alloc(&aux.tmem, kTileCols * NQ);
     tmem_relinquish();
   }
+  pdl_trigger();  // the join's blocks may take their places; they wait for this grid
   if (P.mask) {
     const uint8_t* mrow = P.mask + b * P.mask_bs;
     for (int w = warp; w < kn * 4; w += Roles<NQ>::softmax_warps) {
@@ -513,21 +514,24 @@ gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int nq, long long r
   const int hk = (int)(bh - b * P.Hk), t = tile * P.tokens + r / P.G, head = hk * P.G + r % P.G;
   if (r >= P.tokens * P.G || t >= P.Tq) return;       // no row
   const long long at = su * P.nsplit * per + ur;      // of split 0, then every `per`
+  pdl_wait();
   float top = -INFINITY;
   for (int s = 0; s < P.nsplit; ++s) top = fmaxf(top, P.part_lse[at + (long long)s * per]);
   const bool any = top > -INFINITY;
   float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
   const int f = lane * 4;
-  for (int s = 0; any && s < P.nsplit; ++s) {
-    const float w = expf(P.part_lse[at + (long long)s * per] - top);
+#pragma unroll 4
+  for (int s = 0; s < P.nsplit; ++s) {
+    const long long x = at + (long long)s * per;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (f < P.D) v = *reinterpret_cast<const float4*>(P.part_o + x * P.D + f);
+    const float w = any ? expf(P.part_lse[x] - top) : 0.f;
+    const bool on = w > 0.f;  // a split that saw nothing left no part
     sum += w;
-    if (w > 0.f && f < P.D) {  // a split that saw nothing left no part
-      const float4 v = *reinterpret_cast<const float4*>(P.part_o + (at + (long long)s * per) * P.D + f);
-      o[0] += w * v.x;
-      o[1] += w * v.y;
-      o[2] += w * v.z;
-      o[3] += w * v.w;
-    }
+    o[0] += on ? w * v.x : 0.f;
+    o[1] += on ? w * v.y : 0.f;
+    o[2] += on ? w * v.z : 0.f;
+    o[3] += on ? w * v.w : 0.f;
   }
   const float inv = any ? 1.f / sum : 0.f;
   const int Hq = P.Hk * P.G;
@@ -537,11 +541,6 @@ gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int nq, long long r
   if (lane == 0 && P.lse) P.lse[(b * Hq + head) * P.Tq + t] = any ? top + logf(sum) : -INFINITY;
 }
 
-#ifdef CROSS_FORCE
-int cross_force() { const char* s = getenv("CROSS_NQ"); return s ? atoi(s) : 4; }
-#else
-int cross_force() { return 4; }
-#endif
 // The shape of a call: query tiles of a CTA, units, splits along the keys.
 // Returns the query tiles of a CTA.
 int cross_shape(const CrossCall& c, CrossParams* P) {
@@ -553,7 +552,12 @@ int cross_shape(const CrossCall& c, CrossParams* P) {
   P->tokens = kRows / P->G;
   P->qtiles = (c.Tq + P->tokens - 1) / P->tokens;
   P->ntiles = (c.S + kRows - 1) / kRows;
-  const int nq = P->ntiles <= cross_force() ? 1 : 2;
+  // Up to 16 key tiles two CTAs of one query tile each share an SM, their starts
+  // and ends under each other's work; beyond, one CTA of two tiles halves the keys
+  // and values that are loaded.  2640 queries, 20 heads of 112 (pair / single, us):
+  // 128 keys 15.1 / 12.3, 300 22.0 / 19.7, 1024 45.6 / 44.9, 2640 78.2 / 77.2,
+  // 7920 181 / 188.
+  const int nq = P->ntiles <= 16 ? 1 : 2;
   P->groups = (P->qtiles + nq - 1) / nq;
   const long long units = (long long)c.B * c.Hk * P->groups;
   const long long slots = num_sms() * (3 - nq);  // CTAs that run at a time
@@ -642,9 +646,9 @@ cudaError_t launch_cross(const CrossCall& c, void* ws) {
   if (parts > 0) {
     ProfileScope ps(c.stream, kKernCrossJoin);
     const long long rows = parts / P.nsplit * nq * kRows;
-    gdn_cross_join_kernel<<<(unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)), kJoinThreads, 0,
-                            c.stream>>>(P, nq, rows, static_cast<__nv_bfloat16*>(c.out));
-    e = cudaGetLastError();
+    const unsigned blocks = (unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
+    e = launch_after(gdn_cross_join_kernel, blocks, kJoinThreads, 0, c.stream, P, nq, rows,
+                     static_cast<__nv_bfloat16*>(c.out));
     if (e == cudaSuccess) count_launches(1);
   }
   return e;

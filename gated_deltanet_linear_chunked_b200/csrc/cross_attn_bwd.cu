@@ -5,7 +5,7 @@
 // the last two summed over the query heads of a key head as well: they are rows
 // of the same products, packed as in the forward (row = token * G + head).
 //
-// Two kernels instead of one over the same tiles.  One pass that makes all three
+// Two passes instead of one over the same tiles.  One pass that makes all three
 // gradients needs five products per tile but has to add dQ (or dK and dV) up
 // across CTAs, by atomics, whose order changes the result, or through partial
 // sums of full size; two passes take seven products and every sum stays in a
@@ -13,12 +13,12 @@
 //   gdn_cross_stat_kernel  (lse log2 e, delta) of every packed row; +inf for the
 //                  rows that are none (past the tokens, or with no key), for
 //                  which 2^(s - inf) = 0.
-//   gdn_cross_dq_kernel    a CTA per query tile walks the key tiles.
-//   gdn_cross_dkv_kernel   a CTA per key tile and share of the query tiles; the
+//   gdn_cross_bwd_kernel   dQ: a CTA per query tile walks the key tiles.
+//                  dK, dV: a CTA per key tile and share of the query tiles; the
 //                  products are transposed, S^T = K Q^T and dP^T = V dO^T, so that
 //                  a TMEM lane is a key, P^T and dS^T are left operands out of
-//                  TMEM, and dK and dV add up there.  gdn_cross_dkv_join_kernel
-//                  adds the shares up where there are several.
+//                  TMEM, and dK and dV add up there.
+//   gdn_cross_dkv_join_kernel  adds the shares up where there are several.
 // No maximum is searched and no row's threads meet: lse is known.  16 warps take
 // a 128 x 128 tile, 32 columns a thread; one warp copies, one issues products.
 #include <cuda.h>
@@ -52,6 +52,7 @@ struct BwdParams {
   int Tq, S, Hk, G, D;
   int tokens, qtiles, ntiles;   // tokens and tiles of queries, tiles of keys
   int nsplit, per_split;        // dkv: shares of the query tiles, tiles of each
+  unsigned dkv_blocks;          // ntiles * nsplit of every (b, key head)
   int qb, kb, vb;
   const uint32_t* bits;         // under a mask: seen keys, [B][ntiles][4], one bit each
   const int* list;              // ... and [B][ntiles + 1]: the tiles with any, their number last
@@ -99,47 +100,56 @@ __device__ __forceinline__ uint32_t word_of(const uint4& w, int c) {
 }
 
 // ---------------------------------------------------------------- row stats
-// A warp per packed row: delta from 4 features a lane.  Under a mask, the last B
-// blocks turn the rows of the mask into bits and lists instead.
+// Sixteen lanes per packed row, 8 features a lane; four rows of a group are loaded
+// before any is summed.  Under a mask, the last B blocks turn the rows of the mask
+// into bits and lists instead.
+constexpr int kStatRows = 4;
+constexpr int kStatBlockRows = kStatThreads / 16 * kStatRows;
 __global__ void __launch_bounds__(kStatThreads)
 gdn_cross_stat_kernel(const __nv_bfloat16* out, const __nv_bfloat16* d_out, const float* lse, float2* stat,
                       long long rows, unsigned row_blocks, const uint8_t* mask, long long mask_bs,
                       const __grid_constant__ BwdParams P) {
+  pdl_trigger();
   if (blockIdx.x >= row_blocks) {
     const int b = blockIdx.x - row_blocks;
     mask_lists(mask + b * mask_bs, P.S, P.ntiles, const_cast<uint32_t*>(P.bits) + (long long)b * P.ntiles * 4,
                const_cast<int*>(P.list) + (long long)b * (P.ntiles + 1));
     return;
   }
-  const int Tq = P.Tq, Hk = P.Hk, G = P.G, D = P.D, tokens = P.tokens, qtiles = P.qtiles;
-  const long long row = (long long)blockIdx.x * (kStatThreads / 32) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  const int r = (int)(row % kRows);
-  const long long tile = row / kRows, bh = tile / qtiles;
-  const int qt = (int)(tile - bh * qtiles), hk = (int)(bh % Hk);
-  const long long b = bh / Hk;
-  const int t = qt * tokens + r / G, head = hk * G + r % G;
-  float2 s = make_float2(INFINITY, 0.f);
-  if (r < tokens * G && t < Tq) {  // uniform over the warp
-    const int Hq = Hk * G;
-    const long long at = ((b * Tq + t) * Hq + head) * D + lane * 4;
-    float d = 0.f;
-    if (lane * 4 < D) {
-      float x[4], y[4];
-      const uint2 u = *reinterpret_cast<const uint2*>(out + at), v = *reinterpret_cast<const uint2*>(d_out + at);
-      unpack_bf16x2(u.x, x[0], x[1]);
-      unpack_bf16x2(u.y, x[2], x[3]);
-      unpack_bf16x2(v.x, y[0], y[1]);
-      unpack_bf16x2(v.y, y[2], y[3]);
-      d = x[0] * y[0] + x[1] * y[1] + (x[2] * y[2] + x[3] * y[3]);
-    }
+  const int l = threadIdx.x & 15, Hq = P.Hk * P.G;
+  const long long first = (long long)blockIdx.x * kStatBlockRows + threadIdx.x / 16;
+  uint4 x[kStatRows], y[kStatRows];
+  float lg[kStatRows];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(~0u, d, o);
-    const float l = lse[(b * Hq + head) * Tq + t];
-    if (l > -INFINITY) s = make_float2(l * 1.4426950408889634f, d);
+  for (int i = 0; i < kStatRows; ++i) {
+    x[i] = y[i] = make_uint4(0, 0, 0, 0);
+    lg[i] = -INFINITY;
+    const long long row = first + i * (kStatThreads / 16);
+    const int r = (int)(row % kRows);
+    const unsigned tile = (unsigned)(row / kRows), bh = tile / P.qtiles, qt = tile - bh * P.qtiles;
+    const unsigned b = bh / P.Hk, hk = bh - b * P.Hk;
+    const int t = qt * P.tokens + r / P.G, head = hk * P.G + r % P.G;
+    if (row >= rows || r >= P.tokens * P.G || t >= P.Tq) continue;
+    const long long at = (((long long)b * P.Tq + t) * Hq + head) * P.D + l * 8;
+    if (l * 8 < P.D) {
+      x[i] = *reinterpret_cast<const uint4*>(out + at);
+      y[i] = *reinterpret_cast<const uint4*>(d_out + at);
+    }
+    lg[i] = lse[((long long)b * Hq + head) * P.Tq + t];
   }
-  if (lane == 0) stat[row] = s;
+#pragma unroll
+  for (int i = 0; i < kStatRows; ++i) {
+    float u[8], v[8], d = 0.f;
+    unpack8_bf16(x[i], u);
+    unpack8_bf16(y[i], v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d = fmaf(u[e], v[e], d);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(~0u, d, o);
+    const long long row = first + i * (kStatThreads / 16);
+    const bool on = lg[i] > -INFINITY;
+    if (l == 0 && row < rows) stat[row] = on ? make_float2(lg[i] * 1.4426950408889634f, d) : make_float2(INFINITY, 0.f);
+  }
 }
 
 // ----------------------------------------------------------------------- dQ
@@ -161,15 +171,14 @@ struct DqLayout {
 };
 
 template <int NB>
-__global__ void __launch_bounds__(kThreads, 1)
-gdn_cross_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                    const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ BwdParams P) {
-  extern __shared__ __align__(1024) uint8_t smem[];
+__device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUtensorMap& tm_q,
+                                        const CUtensorMap& tm_do, const CUtensorMap& tm_k,
+                                        const CUtensorMap& tm_v, const CUtensorMap& tm_dq,
+                                        const BwdParams& P) {
   using L = DqLayout<NB>;
   DqAux& aux = *reinterpret_cast<DqAux*>(smem + L::aux);
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
-  const int qt = blockIdx.x % P.qtiles, bh = blockIdx.x / P.qtiles;
+  const int qt = block % P.qtiles, bh = block / P.qtiles;
   const int b = bh / P.Hk, hk = bh - b * P.Hk;
   const int D = P.D;
   volatile int* abort_flag = &aux.abort;
@@ -379,7 +388,7 @@ gdn_cross_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         for (int c = 0; c < NB; ++c)
           tma_store_5d(&tm_dq, smem + L::q + c * kBlock, c * 64, 0, qt * P.tokens, hk, b);
         bulk_commit();
-        bulk_wait_all();
+        bulk_wait_read();  // shared memory may go; the writes land before the grid ends
       }
     }
   }
@@ -412,17 +421,15 @@ struct DkvLayout {
 };
 
 template <int NB>
-__global__ void __launch_bounds__(kThreads, 1)
-gdn_cross_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
-                     const __grid_constant__ BwdParams P) {
-  extern __shared__ __align__(1024) uint8_t smem[];
+__device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CUtensorMap& tm_q,
+                                         const CUtensorMap& tm_do, const CUtensorMap& tm_k,
+                                         const CUtensorMap& tm_v, const CUtensorMap& tm_dk,
+                                         const CUtensorMap& tm_dv, const BwdParams& P) {
   using L = DkvLayout<NB>;
   DkvAux& aux = *reinterpret_cast<DkvAux*>(smem + L::aux);
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
   // unit: ((b * Hk + hk) * ntiles + tile) * nsplit + split
-  const int split = blockIdx.x % P.nsplit, u = blockIdx.x / P.nsplit;
+  const int split = block % P.nsplit, u = block / P.nsplit;
   const int kt = u % P.ntiles, bh = u / P.ntiles;
   const int b = bh / P.Hk, hk = bh - b * P.Hk;
   const int i0 = split * P.per_split, i1 = min(P.qtiles, i0 + P.per_split);
@@ -645,7 +652,7 @@ gdn_cross_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             tma_store_5d(&tm_dv, smem + L::v + c * kBlock, c * 64, 0, kt * kRows, hk, b);
           }
           bulk_commit();
-          bulk_wait_all();
+          bulk_wait_read();
         }
       }
     }
@@ -658,19 +665,39 @@ gdn_cross_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   }
 }
 
+// One grid for both: the dK, dV tiles first, which are longer, then the dQ tiles,
+// so that neither's last wave leaves SMs idle.
+template <int NB>
+__global__ void __launch_bounds__(kThreads, 1)
+gdn_cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_dk,
+                     const __grid_constant__ CUtensorMap tm_dv, const __grid_constant__ BwdParams P) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  pdl_wait();  // the row statistics and mask lists
+  pdl_trigger();
+  if (blockIdx.x < P.dkv_blocks)
+    dkv_tile<NB>(smem, blockIdx.x, tm_q, tm_do, tm_k, tm_v, tm_dk, tm_dv, P);
+  else
+    dq_tile<NB>(smem, blockIdx.x - P.dkv_blocks, tm_q, tm_do, tm_k, tm_v, tm_dq, P);
+}
+
 // dK, dV = the sum of the shares, in their order.  A thread per four features.
 __global__ void __launch_bounds__(256)
 gdn_cross_dkv_join_kernel(const float* part, long long part_rows, int nsplit, int S, int Hk, int ntiles, int D,
                           long long total, __nv_bfloat16* dk, __nv_bfloat16* dv) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= total) return;
+  pdl_wait();
+  const long long j = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (j >= 2 * total) return;
+  const int which = j >= total;
+  const long long i = which ? j - total : j;
   const int q = D / 4;
   const long long row = i / q;  // ((b * S) + s) * Hk + hk
   const int f = (int)(i - row * q) * 4, hk = (int)(row % Hk), s = (int)(row / Hk % S);
   const long long b = row / Hk / S;
   const long long prow = (b * Hk + hk) * ntiles * kRows + s;
-  const int which = blockIdx.y;
   float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
   for (int x = 0; x < nsplit; ++x) {
     const float4 v = *reinterpret_cast<const float4*>(part + ((2 * x + which) * part_rows + prow) * D + f);
     o[0] += v.x;
@@ -708,6 +735,7 @@ void bwd_shape(const CrossCall& c, BwdParams* P) {
   }
   P->per_split = (P->qtiles + P->nsplit - 1) / P->nsplit;
   P->nsplit = (P->qtiles + P->per_split - 1) / P->per_split;
+  P->dkv_blocks = (unsigned)(units * P->nsplit);
 }
 
 // Scratch: the row stats, under a mask its bits and lists, then the shares' parts.
@@ -729,23 +757,13 @@ cudaError_t launch_nb(const CrossCall& c, const BwdParams& P, const CUtensorMap&
                       const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdq,
                       const CUtensorMap& mdk, const CUtensorMap& mdv) {
   // more than half an SM's shared memory: one CTA (all of TMEM) per SM
-  constexpr int dq_bytes = DqLayout<NB>::total > 116 * 1024 ? DqLayout<NB>::total : 116 * 1024;
-  constexpr int dkv_bytes = DkvLayout<NB>::total > 116 * 1024 ? DkvLayout<NB>::total : 116 * 1024;
-  cudaError_t e = allow_smem(gdn_cross_dq_kernel<NB>, dq_bytes);
-  if (e == cudaSuccess) e = allow_smem(gdn_cross_dkv_kernel<NB>, dkv_bytes);
+  constexpr int bytes = std::max({(int)DqLayout<NB>::total, (int)DkvLayout<NB>::total, 116 * 1024});
+  cudaError_t e = allow_smem(gdn_cross_bwd_kernel<NB>, bytes);
   if (e != cudaSuccess) return e;
-  {
-    ProfileScope ps(c.stream, kKernCrossDq);
-    gdn_cross_dq_kernel<NB><<<(unsigned)(c.B * c.Hk * P.qtiles), kThreads, dq_bytes, c.stream>>>(mq, mg, mk, mv,
-                                                                                               mdq, P);
-  }
-  {
-    ProfileScope ps(c.stream, kKernCrossDkv);
-    gdn_cross_dkv_kernel<NB><<<(unsigned)(c.B * c.Hk * P.ntiles * P.nsplit), kThreads, dkv_bytes, c.stream>>>(
-        mq, mg, mk, mv, mdk, mdv, P);
-  }
-  e = cudaGetLastError();
-  if (e == cudaSuccess) count_launches(2);
+  ProfileScope ps(c.stream, kKernCrossBwd);
+  e = launch_after(gdn_cross_bwd_kernel<NB>, P.dkv_blocks + (unsigned)(c.B * c.Hk * P.qtiles), kThreads, bytes,
+                   c.stream, mq, mg, mk, mv, mdq, mdk, mdv, P);
+  if (e == cudaSuccess) count_launches(1);
   return e;
 }
 
@@ -789,7 +807,7 @@ cudaError_t launch_cross_backward(const CrossCall& c, void* ws) {
   const long long rows = (long long)c.B * c.Hk * P.qtiles * kRows;
   {
     ProfileScope ps(c.stream, kKernCrossStat);
-    const unsigned blocks = (unsigned)((rows + kStatThreads / 32 - 1) / (kStatThreads / 32));
+    const unsigned blocks = (unsigned)((rows + kStatBlockRows - 1) / kStatBlockRows);
     gdn_cross_stat_kernel<<<blocks + (c.mask ? c.B : 0), kStatThreads, 0, c.stream>>>(
         static_cast<const __nv_bfloat16*>(c.out), static_cast<const __nv_bfloat16*>(c.d_out), c.lse,
         static_cast<float2*>(ws), rows, blocks, c.mask, c.mask_bs, P);
@@ -802,10 +820,9 @@ cudaError_t launch_cross_backward(const CrossCall& c, void* ws) {
   if (e != cudaSuccess || P.nsplit == 1) return e;
   ProfileScope ps(c.stream, kKernCrossDkvJoin);
   const long long total = (long long)c.B * c.S * c.Hk * (c.D / 4);
-  gdn_cross_dkv_join_kernel<<<dim3((unsigned)((total + 255) / 256), 2), 256, 0, c.stream>>>(
-      P.part, P.part_rows, P.nsplit, c.S, c.Hk, P.ntiles, c.D, total, static_cast<__nv_bfloat16*>(c.dk),
-      static_cast<__nv_bfloat16*>(c.dv));
-  e = cudaGetLastError();
+  e = launch_after(gdn_cross_dkv_join_kernel, (unsigned)((2 * total + 255) / 256), 256, 0, c.stream,
+                   (const float*)P.part, P.part_rows, P.nsplit, c.S, c.Hk, P.ntiles, c.D, total,
+                   static_cast<__nv_bfloat16*>(c.dk), static_cast<__nv_bfloat16*>(c.dv));
   if (e == cudaSuccess) count_launches(1);
   return e;
 }

@@ -781,8 +781,7 @@ const char* gdn_kernel_name(int id) {
     case gdn::kKernNormRopeReduce: return "gdn_norm_rope_reduce_kernel";
     case gdn::kKernCross: return "gdn_cross_kernel";
     case gdn::kKernCrossJoin: return "gdn_cross_join_kernel";
-    case gdn::kKernCrossDq: return "gdn_cross_dq_kernel";
-    case gdn::kKernCrossDkv: return "gdn_cross_dkv_kernel";
+    case gdn::kKernCrossBwd: return "gdn_cross_bwd_kernel";
     case gdn::kKernCrossDkvJoin: return "gdn_cross_dkv_join_kernel";
     case gdn::kKernCrossStat: return "gdn_cross_stat_kernel";
   }

@@ -71,11 +71,10 @@ enum KernelId : int {
   kKernNormRopeReduce = 13,
   kKernCross = 14,
   kKernCrossJoin = 15,
-  kKernCrossDq = 16,
-  kKernCrossDkv = 17,
-  kKernCrossDkvJoin = 18,
-  kKernCrossStat = 19,
-  kNumKernelIds = 20,
+  kKernCrossBwd = 16,
+  kKernCrossDkvJoin = 17,
+  kKernCrossStat = 18,
+  kNumKernelIds = 19,
 };
 
 // While profiling is armed, records CUDA events around one launch.
@@ -205,6 +204,24 @@ cudaError_t allow_smem(K kernel, int bytes) {
   const cudaError_t s = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (s == cudaSuccess && i < 4) seen[dev][i] = f;
   return s;
+}
+
+// Launches a kernel whose blocks may take their places before the kernel in front
+// of it on the stream has ended (it calls pdl_wait before it touches its results).
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
+                         cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
 }
 
 // Streaming multiprocessors of the current device (cached per device).
