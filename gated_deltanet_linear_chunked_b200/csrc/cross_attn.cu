@@ -80,6 +80,7 @@ constexpr long long kDrainPolls = 1LL << 40;  // drains are bounded by the 2 s t
 struct CrossParams {
   int Tq, S, Hk, G, D;
   int tokens;            // query tokens per tile: 128 / G
+  int gmul;              // r / G = r * gmul >> 16 for rows r < 128
   int qtiles, groups;    // query tiles of a (b, key head); units along them (NQ tiles each)
   int ntiles;            // key tiles
   unsigned full;         // units that one CTA each takes whole; those behind them ...
@@ -88,6 +89,7 @@ struct CrossParams {
   const uint8_t* mask;
   long long mask_bs;
   float scale_log2;      // scale * log2(e)
+  __nv_bfloat16* out;    // [B, Tq, Hq, D]
   float* lse;            // [B, Hq, Tq] or nullptr
   float* part_o;         // [split units][nsplit][NQ * 128 rows][D] fp32
   float* part_lse;       // [split units][nsplit][NQ * 128 rows]
@@ -108,7 +110,7 @@ struct CrossAux {
   uint8_t list[kMaskTiles];        // tiles with any
 };
 
-// Shared memory: Q tiles (later the output's), the ring, the barriers and mask.
+// Shared memory: Q tiles, the ring, the barriers and mask.
 template <int NB, int NQ>  // 64-feature blocks of a head, query tiles
 struct CrossLayout {
   static constexpr uint32_t tile = NB * kBlock;
@@ -132,7 +134,7 @@ __device__ __forceinline__ void scores(uint32_t taddr, uint32_t seen, float (&s)
 template <int NB, int NQ>
 __global__ void __launch_bounds__(Roles<NQ>::threads, 3 - NQ)
 gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_out,
+                 const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ CrossParams P) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int D = P.D;
@@ -153,6 +155,9 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   volatile int* abort_flag = &aux.abort;
 
   if (warp == Roles<NQ>::producer && lane == 0) {
+    prefetch_map(&tm_q);
+    prefetch_map(&tm_k);
+    prefetch_map(&tm_v);
     mbar_init(&aux.q_full, 1);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&aux.full[s], 1);
@@ -303,6 +308,10 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const uint32_t tO = tS + kRows;
     const int oc0 = half ? (D / 32 + (D / 16) % 2) * 16 : 0;  // this half's columns of O
     const int oc1 = half ? D : (D / 32 + (D / 16) % 2) * 16;
+    const int Hq = P.Hk * P.G, tok0 = (tile0 + g) * P.tokens;
+    const int t = tok0 + (r * P.gmul >> 16), head = hk * P.G + r - (r * P.gmul >> 16) * P.G;
+    const bool row = r < P.tokens * P.G && t < P.Tq;
+    __nv_bfloat16* const out0 = P.out + (((long long)b * P.Tq + tok0) * Hq + hk * P.G) * D;
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
@@ -421,8 +430,7 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       f2_unpack(sa, rs0, rs1);
       l_run = l_run * alpha + (rs0 + rs1);
     }
-    // the last product; without any, the queries, whose buffer takes the zeros
-    if (ok && !__all_sync(~0u, mbar_wait(n > 0 ? &aux.o_full[g] : &aux.q_full, 0, P.limit))) {
+    if (ok && n > 0 && !__all_sync(~0u, mbar_wait(&aux.o_full[g], 0, P.limit))) {
       fail();
       ok = false;
     }
@@ -431,60 +439,46 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (ok) {
       tc_fence_after_sync();
       l_run += aux.row[g][half ^ 1][r];
-      const int Hq = P.Hk * P.G;
-      const int t = (tile0 + g) * P.tokens + r / P.G, head = hk * P.G + r % P.G;
-      const bool row = r < P.tokens * P.G && t < P.Tq;
       const float lse = n > 0 ? (m_run + log2f(l_run)) * 0.6931471805599453f : -INFINITY;
       const float inv = n > 0 ? 1.f / l_run : 0.f;
-      if (!whole) {
-        const long long at = ((long long)x * NQ + g) * kRows + r;  // x: split unit * nsplit + split
-        if (half == 0) P.part_lse[at] = lse;
+      if (row && half == 0 && P.lse && whole) P.lse[((long long)b * Hq + head) * P.Tq + t] = lse;
+      const long long part = ((long long)x * NQ + g) * kRows;  // x: split unit * nsplit + split
+      if (half == 0 && !whole) P.part_lse[part + r] = lse;
+      // every S MMA has completed: the tile's Q buffer takes its rows, 4 KB a warp
+      uint8_t* stage = smem + L::q + g * L::tile + (warp & 7) * (L::tile / 8);
+      const int r0 = (warp & 3) * 32;
+      for (int c0 = oc0; c0 < oc1; c0 += 32) {
+        float o[32];
+        const int cols = min(32, oc1 - c0);
         if (n > 0) {
-          for (int c0 = oc0; c0 < oc1; c0 += 16) {
-            float o[16];
-            tmem_ld16(tO + c0, o);
-            tmem_wait_ld();
-            float4* to = reinterpret_cast<float4*>(P.part_o + at * D + c0);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              to[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
-          }
+          if (cols == 32)
+            tmem_ld32(tO + c0, o);
+          else
+            tmem_ld16(tO + c0, *reinterpret_cast<float(*)[16]>(o));
+          tmem_wait_ld();
         }
-      } else {
-        if (row && half == 0 && P.lse) P.lse[((long long)b * Hq + head) * P.Tq + t] = lse;
-        // every S MMA has completed: the tile's Q buffer takes its output
-        uint8_t* so = smem + L::q + g * L::tile + r * 128;
-        auto put = [&](int c0, const float* o) {  // 16 columns from c0
-          uint8_t* blk = so + (c0 >> 6) * kBlock;
-          const int c = (c0 & 63) >> 3;
-          *reinterpret_cast<uint4*>(blk + ((c ^ (r & 7)) << 4)) = pack8_bf16(o);
-          *reinterpret_cast<uint4*>(blk + (((c + 1) ^ (r & 7)) << 4)) = pack8_bf16(o + 8);
-        };
-        for (int c0 = oc0; c0 < oc1; c0 += 32) {
-          float o[32];
-          const bool two = c0 + 16 < oc1;
-          if (n > 0) {
-            if (two)
-              tmem_ld32(tO + c0, o);
-            else
-              tmem_ld16(tO + c0, *reinterpret_cast<float(*)[16]>(o));
-            tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= inv;
-          } else {
+        for (int e = 0; e < 32; ++e) o[e] = n > 0 ? o[e] * inv : 0.f;
+        if (whole) {
+          const uint4 v[4] = {pack8_bf16(o), pack8_bf16(o + 8), pack8_bf16(o + 16), pack8_bf16(o + 24)};
+          store_rows<4>(stage, lane, v, cols / 8, [&](int i) -> void* {
+            const int q = r0 + i, dt = q * P.gmul >> 16, dh = q - dt * P.G;  // row = token * G + head
+            return dt < P.tokens && tok0 + dt < P.Tq ? out0 + ((long long)dt * Hq + dh) * D + c0 : nullptr;
+          });
+        } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          for (int h = 0; h < 2; ++h) {
+            uint4 v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float* f = o + 16 * h + 4 * e;
+              v[e] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                __float_as_uint(f[3]));
+            }
+            if (16 * h < cols)
+              store_rows<4>(stage, lane, v, 4,
+                            [&](int i) -> void* { return P.part_o + (part + r0 + i) * D + c0 + 16 * h; });
           }
-          put(c0, o);
-          if (two) put(c0 + 16, o + 16);
-        }
-        fence_proxy_async_smem();
-        named_barrier(1 + g, 2 * kRows);
-        if (r == 0 && half == 0) {
-          for (int c = 0; c < nb; ++c)
-            tma_store_5d(&tm_out, smem + L::q + g * L::tile + c * kBlock, c * 64, 0, (tile0 + g) * P.tokens, hk, b);
-          bulk_commit();
-          bulk_wait_read();  // shared memory may go; the writes land before the grid ends
         }
       }
     }
@@ -501,7 +495,7 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 // row of the split units, four features a lane.
 constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads)
-gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int nq, long long rows, __nv_bfloat16* out) {
+gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int nq, long long rows) {
   const long long i = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (i >= rows) return;
@@ -536,7 +530,7 @@ gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int nq, long long r
   const float inv = any ? 1.f / sum : 0.f;
   const int Hq = P.Hk * P.G;
   if (f < P.D)
-    *reinterpret_cast<uint2*>(out + ((b * P.Tq + t) * Hq + head) * P.D + f) =
+    *reinterpret_cast<uint2*>(P.out + ((b * P.Tq + t) * Hq + head) * P.D + f) =
         make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
   if (lane == 0 && P.lse) P.lse[(b * Hq + head) * P.Tq + t] = any ? top + logf(sum) : -INFINITY;
 }
@@ -550,6 +544,7 @@ int cross_shape(const CrossCall& c, CrossParams* P) {
   P->G = c.Hq / c.Hk;
   P->D = c.D;
   P->tokens = kRows / P->G;
+  P->gmul = 65536 / P->G + 1;
   P->qtiles = (c.Tq + P->tokens - 1) / P->tokens;
   P->ntiles = (c.S + kRows - 1) / kRows;
   // Up to 16 key tiles two CTAs of one query tile each share an SM, their starts
@@ -583,7 +578,7 @@ long long split_blocks(const CrossCall& c, const CrossParams& P) {
 
 template <int NB, int NQ>
 cudaError_t launch_nb(unsigned grid, cudaStream_t stream, const CUtensorMap& mq, const CUtensorMap& mk,
-                      const CUtensorMap& mv, const CUtensorMap& mo, const CrossParams& P) {
+                      const CUtensorMap& mv, const CrossParams& P) {
   // more than a third (half) of an SM's shared memory: two CTAs (one) per SM, as
   // many as tensor memory has columns for
   constexpr int least = NQ == 1 ? 80 * 1024 : 116 * 1024;
@@ -591,7 +586,7 @@ cudaError_t launch_nb(unsigned grid, cudaStream_t stream, const CUtensorMap& mq,
   const cudaError_t e = allow_smem(gdn_cross_kernel<NB, NQ>, bytes);
   if (e != cudaSuccess) return e;
   ProfileScope ps(stream, kKernCross);
-  gdn_cross_kernel<NB, NQ><<<grid, Roles<NQ>::threads, bytes, stream>>>(mq, mk, mv, mo, P);
+  gdn_cross_kernel<NB, NQ><<<grid, Roles<NQ>::threads, bytes, stream>>>(mq, mk, mv, P);
   return cudaSuccess;
 }
 
@@ -610,6 +605,7 @@ cudaError_t launch_cross(const CrossCall& c, void* ws) {
   P.mask = c.mask;
   P.mask_bs = c.mask_bs;
   P.scale_log2 = c.scale * 1.4426950408889634f;
+  P.out = static_cast<__nv_bfloat16*>(c.out);
   P.lse = c.lse;
   P.part_o = static_cast<float*>(ws);
   P.part_lse = P.part_o + (size_t)parts * nq * kRows * c.D;
@@ -618,11 +614,9 @@ cudaError_t launch_cross(const CrossCall& c, void* ws) {
   P.qb = c.q.batch_stride != 0;
   P.kb = c.k.batch_stride != 0;
   P.vb = c.v.batch_stride != 0;
-  CUtensorMap mq, mk, mv, mo;
-  const long long ots = (long long)c.Hq * c.D;
+  CUtensorMap mq, mk, mv;
   if (!make_heads_map(&mq, c.q.data, P.qb ? c.B : 1, c.Tq, c.Hk, P.G, c.D, c.q.batch_stride,
-                      c.q.token_stride, P.tokens) ||
-      !make_heads_map(&mo, c.out, c.B, c.Tq, c.Hk, P.G, c.D, c.Tq * ots, ots, P.tokens))
+                      c.q.token_stride, P.tokens))
     return cudaErrorInvalidValue;
   if (c.S == 0) {
     mk = mv = mq;  // no key tile is ever loaded
@@ -635,11 +629,11 @@ cudaError_t launch_cross(const CrossCall& c, void* ws) {
   const unsigned grid = (unsigned)(P.full + parts);
   cudaError_t e;
   if (nq == 1)
-    e = c.D > 64 ? launch_nb<2, 1>(grid, c.stream, mq, mk, mv, mo, P)
-                 : launch_nb<1, 1>(grid, c.stream, mq, mk, mv, mo, P);
+    e = c.D > 64 ? launch_nb<2, 1>(grid, c.stream, mq, mk, mv, P)
+                 : launch_nb<1, 1>(grid, c.stream, mq, mk, mv, P);
   else
-    e = c.D > 64 ? launch_nb<2, 2>(grid, c.stream, mq, mk, mv, mo, P)
-                 : launch_nb<1, 2>(grid, c.stream, mq, mk, mv, mo, P);
+    e = c.D > 64 ? launch_nb<2, 2>(grid, c.stream, mq, mk, mv, P)
+                 : launch_nb<1, 2>(grid, c.stream, mq, mk, mv, P);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   count_launches(1);
@@ -647,8 +641,7 @@ cudaError_t launch_cross(const CrossCall& c, void* ws) {
     ProfileScope ps(c.stream, kKernCrossJoin);
     const long long rows = parts / P.nsplit * nq * kRows;
     const unsigned blocks = (unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
-    e = launch_after(gdn_cross_join_kernel, blocks, kJoinThreads, 0, c.stream, P, nq, rows,
-                     static_cast<__nv_bfloat16*>(c.out));
+    e = launch_after(gdn_cross_join_kernel, blocks, kJoinThreads, 0, c.stream, P, nq, rows);
     if (e == cudaSuccess) count_launches(1);
   }
   return e;

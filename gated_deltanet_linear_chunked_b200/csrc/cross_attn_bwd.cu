@@ -51,12 +51,14 @@ constexpr long long kDrainPolls = 1LL << 40;
 struct BwdParams {
   int Tq, S, Hk, G, D;
   int tokens, qtiles, ntiles;   // tokens and tiles of queries, tiles of keys
+  int gmul;                     // r / G = r * gmul >> 16 for rows r < 128
   int nsplit, per_split;        // dkv: shares of the query tiles, tiles of each
   unsigned dkv_blocks;          // ntiles * nsplit of every (b, key head)
   int qb, kb, vb;
   const uint32_t* bits;         // under a mask: seen keys, [B][ntiles][4], one bit each
   const int* list;              // ... and [B][ntiles + 1]: the tiles with any, their number last
   float scale, scale_log2;
+  __nv_bfloat16 *dq, *dk, *dv;
   const float2* stat;           // [B * Hk][qtiles][128]
   float* part;                  // nsplit > 1: [nsplit][2 (dk, dv)][B * Hk][ntiles][128][D]
   long long part_rows;          // B * Hk * ntiles * 128
@@ -125,10 +127,10 @@ gdn_cross_stat_kernel(const __nv_bfloat16* out, const __nv_bfloat16* d_out, cons
     x[i] = y[i] = make_uint4(0, 0, 0, 0);
     lg[i] = -INFINITY;
     const long long row = first + i * (kStatThreads / 16);
-    const int r = (int)(row % kRows);
+    const int r = (int)(row % kRows), dt = r * P.gmul >> 16;
     const unsigned tile = (unsigned)(row / kRows), bh = tile / P.qtiles, qt = tile - bh * P.qtiles;
     const unsigned b = bh / P.Hk, hk = bh - b * P.Hk;
-    const int t = qt * P.tokens + r / P.G, head = hk * P.G + r % P.G;
+    const int t = qt * P.tokens + dt, head = hk * P.G + r - dt * P.G;
     if (row >= rows || r >= P.tokens * P.G || t >= P.Tq) continue;
     const long long at = (((long long)b * P.Tq + t) * Hq + head) * P.D + l * 8;
     if (l * 8 < P.D) {
@@ -149,6 +151,38 @@ gdn_cross_stat_kernel(const __nv_bfloat16* out, const __nv_bfloat16* d_out, cons
     const long long row = first + i * (kStatThreads / 16);
     const bool on = lg[i] > -INFINITY;
     if (l == 0 && row < rows) stat[row] = on ? make_float2(lg[i] * 1.4426950408889634f, d) : make_float2(INFINITY, 0.f);
+  }
+}
+
+// Columns [c0, c0 + n) (n 16 or 32) of a warp's 32 rows out of TMEM, times `mul`
+// (zeros if there is nothing), as bf16 to dst(row) or as fp32 to part(row).
+template <typename Dst, typename Part>
+__device__ __forceinline__ void put_columns(uint32_t src, int n, bool any, float mul, uint8_t* stage, int lane,
+                                            bool whole, Dst dst, Part part) {
+  float o[kCols];
+  if (any) {
+    if (n == kCols)
+      tmem_ld32(src, o);
+    else
+      tmem_ld16(src, *reinterpret_cast<float(*)[16]>(o));
+    tmem_wait_ld();
+  }
+#pragma unroll
+  for (int e = 0; e < kCols; ++e) o[e] = any ? o[e] * mul : 0.f;
+  if (whole) {
+    const uint4 v[4] = {pack8_bf16(o), pack8_bf16(o + 8), pack8_bf16(o + 16), pack8_bf16(o + 24)};
+    store_rows<4>(stage, lane, v, n / 8, dst);
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint4 v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float* f = o + 16 * h + 4 * e;
+      v[e] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+    if (16 * h < n) store_rows<4>(stage, lane, v, 4, [&](int r) -> void* { return part(r) + 16 * h; });
   }
 }
 
@@ -173,8 +207,7 @@ struct DqLayout {
 template <int NB>
 __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUtensorMap& tm_q,
                                         const CUtensorMap& tm_do, const CUtensorMap& tm_k,
-                                        const CUtensorMap& tm_v, const CUtensorMap& tm_dq,
-                                        const BwdParams& P) {
+                                        const CUtensorMap& tm_v, const BwdParams& P) {
   using L = DqLayout<NB>;
   DqAux& aux = *reinterpret_cast<DqAux*>(smem + L::aux);
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
@@ -364,32 +397,18 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
     ok = named_barrier_and(1, kSoftmaxThreads, ok && *abort_flag == 0);
     if (ok) {
       tc_fence_after_sync();
-      // every product has completed: Q's buffer takes dQ
-      uint8_t* so = smem + L::q + r * 128;
-      for (int c0 = kCols * cg; c0 < min(D, kCols * (cg + 1)); c0 += 16) {
-        float o[16];
-        if (n > 0) {
-          tmem_ld16(trow + tDQ + c0, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] *= P.scale;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = 0.f;
-        }
-        uint8_t* blk = so + (c0 >> 6) * kBlock;
-        const int c = (c0 & 63) >> 3;
-        *reinterpret_cast<uint4*>(blk + ((c ^ (r & 7)) << 4)) = pack8_bf16(o);
-        *reinterpret_cast<uint4*>(blk + (((c + 1) ^ (r & 7)) << 4)) = pack8_bf16(o + 8);
-      }
-      fence_proxy_async_smem();
-      named_barrier(1, kSoftmaxThreads);
-      if (tid == 0) {
-        for (int c = 0; c < NB; ++c)
-          tma_store_5d(&tm_dq, smem + L::q + c * kBlock, c * 64, 0, qt * P.tokens, hk, b);
-        bulk_commit();
-        bulk_wait_read();  // shared memory may go; the writes land before the grid ends
-      }
+      // every product has completed: Q's (and dO's) buffer takes the rows, 2 KB a warp
+      const int Hq = P.Hk * P.G, tok0 = qt * P.tokens, c0 = kCols * cg, r0 = (warp & 3) * 32;
+      __nv_bfloat16* to = P.dq + (((long long)b * P.Tq + tok0) * Hq + hk * P.G) * D + c0;
+      if (c0 < D)
+        put_columns(
+            trow + tDQ + c0, min(kCols, D - c0), n > 0, P.scale, smem + L::q + warp * 2048, lane,
+            true,
+            [&](int i) -> void* {
+              const int q = r0 + i, dt = q * P.gmul >> 16, dh = q - dt * P.G;  // row = token * G + head
+              return dt < P.tokens && tok0 + dt < P.Tq ? to + ((long long)dt * Hq + dh) * D : nullptr;
+            },
+            [](int) -> float* { return nullptr; });
     }
   }
   tc_fence_before_sync();
@@ -423,8 +442,7 @@ struct DkvLayout {
 template <int NB>
 __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CUtensorMap& tm_q,
                                          const CUtensorMap& tm_do, const CUtensorMap& tm_k,
-                                         const CUtensorMap& tm_v, const CUtensorMap& tm_dk,
-                                         const CUtensorMap& tm_dv, const BwdParams& P) {
+                                         const CUtensorMap& tm_v, const BwdParams& P) {
   using L = DkvLayout<NB>;
   DkvAux& aux = *reinterpret_cast<DkvAux*>(smem + L::aux);
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
@@ -560,7 +578,7 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
     }
     __syncwarp();
   } else {
-    const int r = (warp & 3) * 32 + lane, cg = warp >> 2;  // key; queries [32 cg, 32 cg + 32)
+    const int cg = warp >> 2;  // a key per lane; queries [32 cg, 32 cg + 32)
     const uint32_t trow = tm + ((uint32_t)((warp & 3) * 32) << 16);
     const bool seen = word_of(keys, warp & 3) >> lane & 1;
     bool ok = true;
@@ -613,47 +631,19 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
     ok = named_barrier_and(1, kSoftmaxThreads, ok && *abort_flag == 0);
     if (ok) {
       tc_fence_after_sync();
-      // dK, then dV: to the share's part, or as bf16 over K and V (all products done)
+      // dK, then dV: to the share's part, or as bf16 where they belong; every product
+      // has completed, so K's (and V's) buffer takes the rows, 2 KB a warp
+      const int c0 = kCols * cg, r0 = (warp & 3) * 32;
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
-        const float mul = which ? 1.f : P.scale;
-        const uint32_t src = trow + (which ? tDV : tDK);
-        for (int c0 = kCols * cg; c0 < min(D, kCols * (cg + 1)); c0 += 16) {
-          float o[16];
-          if (n > 0) {
-            tmem_ld16(src + c0, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] *= mul;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = 0.f;
-          }
-          if (P.nsplit > 1) {
-            const long long row = ((long long)bh * P.ntiles + kt) * kRows + r;
-            float4* to = reinterpret_cast<float4*>(
-                P.part + ((2 * split + which) * P.part_rows + row) * D + c0);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) to[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          } else {
-            uint8_t* blk = smem + which * L::tile + r * 128 + (c0 >> 6) * kBlock;
-            const int c = (c0 & 63) >> 3;
-            *reinterpret_cast<uint4*>(blk + ((c ^ (r & 7)) << 4)) = pack8_bf16(o);
-            *reinterpret_cast<uint4*>(blk + (((c + 1) ^ (r & 7)) << 4)) = pack8_bf16(o + 8);
-          }
-        }
-      }
-      if (P.nsplit == 1) {
-        fence_proxy_async_smem();
-        named_barrier(1, kSoftmaxThreads);
-        if (tid == 0) {
-          for (int c = 0; c < NB; ++c) {
-            tma_store_5d(&tm_dk, smem + L::k + c * kBlock, c * 64, 0, kt * kRows, hk, b);
-            tma_store_5d(&tm_dv, smem + L::v + c * kBlock, c * 64, 0, kt * kRows, hk, b);
-          }
-          bulk_commit();
-          bulk_wait_read();
-        }
+        if (c0 >= D) break;
+        __nv_bfloat16* to = (which ? P.dv : P.dk) + (((long long)b * P.S + kt * kRows) * P.Hk + hk) * D + c0;
+        float* part = P.part + ((2 * split + which) * P.part_rows + ((long long)bh * P.ntiles + kt) * kRows) * D + c0;
+        put_columns(
+            trow + (which ? tDV : tDK) + c0, min(kCols, D - c0), n > 0, which ? 1.f : P.scale,
+            smem + L::k + warp * 2048, lane, P.nsplit == 1,
+            [&](int i) -> void* { return kt * kRows + r0 + i < P.S ? to + (long long)(r0 + i) * P.Hk * D : nullptr; },
+            [&](int i) { return part + (long long)(r0 + i) * D; });
       }
     }
   }
@@ -671,15 +661,20 @@ template <int NB>
 __global__ void __launch_bounds__(kThreads, 1)
 gdn_cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_dk,
-                     const __grid_constant__ CUtensorMap tm_dv, const __grid_constant__ BwdParams P) {
+                     const __grid_constant__ BwdParams P) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  if (threadIdx.x == 0) {
+    prefetch_map(&tm_q);
+    prefetch_map(&tm_do);
+    prefetch_map(&tm_k);
+    prefetch_map(&tm_v);
+  }
   pdl_wait();  // the row statistics and mask lists
   pdl_trigger();
   if (blockIdx.x < P.dkv_blocks)
-    dkv_tile<NB>(smem, blockIdx.x, tm_q, tm_do, tm_k, tm_v, tm_dk, tm_dv, P);
+    dkv_tile<NB>(smem, blockIdx.x, tm_q, tm_do, tm_k, tm_v, P);
   else
-    dq_tile<NB>(smem, blockIdx.x - P.dkv_blocks, tm_q, tm_do, tm_k, tm_v, tm_dq, P);
+    dq_tile<NB>(smem, blockIdx.x - P.dkv_blocks, tm_q, tm_do, tm_k, tm_v, P);
 }
 
 // dK, dV = the sum of the shares, in their order.  A thread per four features.
@@ -716,6 +711,7 @@ void bwd_shape(const CrossCall& c, BwdParams* P) {
   P->G = c.Hq / c.Hk;
   P->D = c.D;
   P->tokens = kRows / P->G;
+  P->gmul = 65536 / P->G + 1;
   P->qtiles = (c.Tq + P->tokens - 1) / P->tokens;
   P->ntiles = (c.S + kRows - 1) / kRows;
   P->part_rows = (long long)c.B * c.Hk * P->ntiles * kRows;
@@ -754,15 +750,14 @@ BwdScratch bwd_scratch(const CrossCall& c, const BwdParams& P) {
 
 template <int NB>
 cudaError_t launch_nb(const CrossCall& c, const BwdParams& P, const CUtensorMap& mq, const CUtensorMap& mg,
-                      const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdq,
-                      const CUtensorMap& mdk, const CUtensorMap& mdv) {
+                      const CUtensorMap& mk, const CUtensorMap& mv) {
   // more than half an SM's shared memory: one CTA (all of TMEM) per SM
   constexpr int bytes = std::max({(int)DqLayout<NB>::total, (int)DkvLayout<NB>::total, 116 * 1024});
   cudaError_t e = allow_smem(gdn_cross_bwd_kernel<NB>, bytes);
   if (e != cudaSuccess) return e;
   ProfileScope ps(c.stream, kKernCrossBwd);
   e = launch_after(gdn_cross_bwd_kernel<NB>, P.dkv_blocks + (unsigned)(c.B * c.Hk * P.qtiles), kThreads, bytes,
-                   c.stream, mq, mg, mk, mv, mdq, mdk, mdv, P);
+                   c.stream, mq, mg, mk, mv, P);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
@@ -782,6 +777,9 @@ cudaError_t launch_cross_backward(const CrossCall& c, void* ws) {
   uint8_t* base = static_cast<uint8_t*>(ws);
   P.bits = c.mask ? reinterpret_cast<const uint32_t*>(base + at.bits) : nullptr;
   P.list = c.mask ? reinterpret_cast<const int*>(base + at.list) : nullptr;
+  P.dq = static_cast<__nv_bfloat16*>(c.dq);
+  P.dk = static_cast<__nv_bfloat16*>(c.dk);
+  P.dv = static_cast<__nv_bfloat16*>(c.dv);
   P.scale = c.scale;
   P.scale_log2 = c.scale * 1.4426950408889634f;
   P.stat = static_cast<const float2*>(ws);
@@ -791,18 +789,15 @@ cudaError_t launch_cross_backward(const CrossCall& c, void* ws) {
   P.qb = c.q.batch_stride != 0;
   P.kb = c.k.batch_stride != 0;
   P.vb = c.v.batch_stride != 0;
-  CUtensorMap mq, mg, mk, mv, mdq, mdk, mdv;
-  const long long ots = (long long)c.Hq * c.D, kts = (long long)c.Hk * c.D;
+  CUtensorMap mq, mg, mk, mv;
+  const long long ots = (long long)c.Hq * c.D;
   if (!make_heads_map(&mq, c.q.data, P.qb ? c.B : 1, c.Tq, c.Hk, P.G, c.D, c.q.batch_stride, c.q.token_stride,
                       P.tokens) ||
       !make_heads_map(&mg, c.d_out, c.B, c.Tq, c.Hk, P.G, c.D, c.Tq * ots, ots, P.tokens) ||
       !make_heads_map(&mk, c.k.data, P.kb ? c.B : 1, c.S, c.Hk, 1, c.D, c.k.batch_stride, c.k.token_stride,
                       kRows) ||
       !make_heads_map(&mv, c.v.data, P.vb ? c.B : 1, c.S, c.Hk, 1, c.D, c.v.batch_stride, c.v.token_stride,
-                      kRows) ||
-      !make_heads_map(&mdq, c.dq, c.B, c.Tq, c.Hk, P.G, c.D, c.Tq * ots, ots, P.tokens) ||
-      !make_heads_map(&mdk, c.dk, c.B, c.S, c.Hk, 1, c.D, c.S * kts, kts, kRows) ||
-      !make_heads_map(&mdv, c.dv, c.B, c.S, c.Hk, 1, c.D, c.S * kts, kts, kRows))
+                      kRows))
     return cudaErrorInvalidValue;
   const long long rows = (long long)c.B * c.Hk * P.qtiles * kRows;
   {
@@ -815,8 +810,8 @@ cudaError_t launch_cross_backward(const CrossCall& c, void* ws) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   count_launches(1);
-  e = c.D > 64 ? launch_nb<2>(c, P, mq, mg, mk, mv, mdq, mdk, mdv)
-               : launch_nb<1>(c, P, mq, mg, mk, mv, mdq, mdk, mdv);
+  e = c.D > 64 ? launch_nb<2>(c, P, mq, mg, mk, mv)
+               : launch_nb<1>(c, P, mq, mg, mk, mv);
   if (e != cudaSuccess || P.nsplit == 1) return e;
   ProfileScope ps(c.stream, kKernCrossDkvJoin);
   const long long total = (long long)c.B * c.S * c.Hk * (c.D / 4);

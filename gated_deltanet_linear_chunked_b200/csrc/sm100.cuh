@@ -493,6 +493,34 @@ __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x) {
                  __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23)));
 }
 
+// 32 rows of a warp to global memory: lane l holds N 16-byte pieces of row l, and
+// dst(row) is where row's pieces go (nullptr: nowhere).  The pieces cross `stage`
+// (32 * 16 * LPR bytes of the warp's own, LPR >= N a power of two of at most 8)
+// so that LPR lanes store one row's: a lane that stored its own row would touch 32
+// rows per instruction, which the load-store unit takes one at a time.
+template <int LPR, typename Dst>
+__device__ __forceinline__ void store_rows(uint8_t* stage, int lane, const uint4* v, int n, Dst dst) {
+  uint8_t* mine = stage + lane * 16 * LPR;
+#pragma unroll
+  for (int c = 0; c < LPR; ++c)
+    if (c < n) *reinterpret_cast<uint4*>(mine + ((c ^ (lane & (LPR - 1))) << 4)) = v[c];
+  __syncwarp();
+  const int c = lane & (LPR - 1);
+#pragma unroll
+  for (int r0 = 0; r0 < 32; r0 += 32 / LPR) {
+    const int r = r0 + lane / LPR;
+    uint8_t* to = static_cast<uint8_t*>(dst(r));
+    if (c < n && to)
+      *reinterpret_cast<uint4*>(to + c * 16) =
+          *reinterpret_cast<const uint4*>(stage + r * 16 * LPR + ((c ^ (r & (LPR - 1))) << 4));
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // ------------------------------------------------------------ bf16 packing
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;
