@@ -7,8 +7,9 @@ is absent, the import fails with an error that says so.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
-import struct
 import threading
 
 from . import build as _build
@@ -24,12 +25,6 @@ GDN_ERR_SCRATCH_LIMIT = 6
 GDN_F32 = 0
 GDN_BF16 = 1
 
-GDN_ROPE_HALF = 0
-GDN_ROPE_INTERLEAVED = 1
-
-# struct formats of gdn_rows and gdn_rotation
-ROWS = struct.Struct("Pqq")
-ROTATION = struct.Struct("PPqiiiiiiif")
 
 # name -> (restype, argtypes), mirroring include/gdn.h
 _vp, _fp, _i, _ll = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
@@ -106,6 +101,37 @@ def load() -> ctypes.CDLL:
             fn.argtypes = args
         _lib = lib  # complete from here on: read without the lock
         return lib
+
+
+_bind = None
+_BOUND = ("gdn_rope", "gdn_qk_norm_rope", "gdn_qk_norm_rope_backward", "gdn_cross_attention",
+          "gdn_cross_attention_backward")
+
+
+def bind():
+    """The compiled torch binding (building it first if it is missing or stale),
+    connected to the loaded library's entry points.  No fallback either."""
+    global _bind
+    if _bind is not None:
+        return _bind
+    lib = load()
+    with _lock:
+        if _bind is not None:
+            return _bind
+        if _build.bind_is_stale():
+            try:
+                _build.build_bind()
+            except Exception as e:
+                if not os.path.exists(_build.BIND_PATH):
+                    raise RuntimeError(
+                        f"_gdn_torch.so is missing and could not be built (g++ is required): {e}") from e
+        loader = importlib.machinery.ExtensionFileLoader("_gdn_torch", _build.BIND_PATH)
+        spec = importlib.util.spec_from_file_location("_gdn_torch", _build.BIND_PATH, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        module.connect({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _BOUND})
+        _bind = module
+        return module
 
 
 def status_string(status: int) -> str:

@@ -188,48 +188,16 @@ def sink_window_attention(q, k, v, k_cache, v_cache, chunk_index, n_sink, window
     return out
 
 
-_LAYOUTS = {"half": _lib.GDN_ROPE_HALF, "interleaved": _lib.GDN_ROPE_INTERLEAVED}
-_POSITION_BYTES = {torch.int32: 4, torch.int64: 8}
-_pack_rows = _lib.ROWS.pack
-
-
-def _raw_stream(stream, device):
-    """The cudaStream_t to launch on: `stream`'s, or the device's current one."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _fresh(stream, like, shape, dtype=None):
-    """A new tensor on `like`'s device, from the memory of the stream it is used on."""
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype) if dtype is not None else like.new_empty(shape)
+def _on(stream, call, tensors):
+    """Runs `call` with `stream` current: new tensors come from its memory, the
+    launch goes to it, and the tensors of other streams stay alive until it is done
+    with them."""
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype or like.dtype)
-
-
-def _used_on(stream, *tensors):
-    """Keeps tensors of another stream alive until `stream` is done with them."""
-    for t in tensors:
+        got = call()
+    for t in (*tensors, *got[1:]):
         if t is not None:
             t.record_stream(stream)
-
-
-def _view(t, name, dtype, shape):
-    """A [B, T, H, D] tensor whose heads and features are contiguous, as gdn_rows."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    sb, st, sh, sd = t.stride()
-    B, T, H, D = shape
-    if (sd != 1 or (sh != D and H > 1)) and B * T * H:
-        raise ValueError(f"{name} must have contiguous heads and features")
-    return _pack_rows(t.data_ptr(), sb if B > 1 else 0, st if T > 1 else 0)
+    return got
 
 
 def rope_frequencies(dim, base=10000.0, sections=None, scaling="none", factor=1.0,
@@ -275,87 +243,12 @@ def rope_frequencies(dim, base=10000.0, sections=None, scaling="none", factor=1.
     return torch.cat(parts).to(device or "cuda"), amplitude
 
 
-def _rotation(positions, inv_freq, sections, layout, amplitude, B, T):
-    """gdn_rotation of a call, or None without positions."""
-    if positions is None and inv_freq is None:
-        return None
-    if positions is None or inv_freq is None:
-        raise ValueError("positions and inv_freq go together")
-    if layout not in _LAYOUTS:
-        raise ValueError("layout must be 'half' or 'interleaved'")
-    pairs = inv_freq.numel()
-    sections = (pairs,) if sections is None else sections
-    axes = len(sections)
-    if not 1 <= axes <= 3:
-        raise ValueError("sections must name 1 to 3 position axes")
-    for t, name in ((positions, "positions"), (inv_freq, "inv_freq")):
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise TypeError("inv_freq must be a contiguous float64 vector")
-    if positions.dtype not in _POSITION_BYTES:
-        raise TypeError("positions must be int32 or int64")
-    shape, stride = positions.shape, positions.stride()
-    if axes == 1 and (shape == (T,) or shape == (B, T)):  # the one axis left out
-        shape, stride = (*shape, 1), (*stride, 1)
-    if shape == (T, axes):
-        bs, st = 0, stride
-    elif shape == (B, T, axes):
-        bs, st = stride[0] if B > 1 else 0, stride[1:]
-    else:
-        raise ValueError(f"positions must be [T], [B, T] (one axis), [T, {axes}] or "
-                         f"[B, T, {axes}], got {tuple(positions.shape)}")
-    if B * T and ((axes > 1 and st[1] != 1) or (T > 1 and st[0] != axes)):
-        raise ValueError("positions must be contiguous over tokens and axes")
-    s = (*sections, 0, 0)
-    return _lib.ROTATION.pack(positions.data_ptr(), inv_freq.data_ptr(), bs,
-                              _POSITION_BYTES[positions.dtype], axes, s[0], s[1], s[2], 2 * pairs,
-                              _LAYOUTS[layout], amplitude)
-
-
-def _heads(q, k):
-    """B, T, Hq, Hk, D, dtype code and the shapes of q and k (k may be None)."""
-    if q.dim() != 4 or (k is not None and k.dim() != 4):
-        raise ValueError("q, k must be [B,T,H,D]")
-    B, T, Hq, D = q.shape
-    Hk = 0 if k is None else k.shape[2]
-    code = _DTYPES.get(q.dtype)
-    if code is None:
-        raise TypeError(f"q, k must be bfloat16 or float32, got {q.dtype}")
-    return B, T, Hq, Hk, D, code, (B, T, Hq, D), (B, T, Hk, D)
-
-
-def _weight(w, name, D):
-    if w is not None:
-        _check_tensor(w, name, torch.float32, (D,))
-    return _ptr(w)
-
-
-def _out_view(t, name, like, shape, stream):
-    """`t`, or a new tensor like `like` where it is None, and its gdn_rows."""
-    if t is not None:
-        return t, _view(t, name, like.dtype, shape)
-    t = _fresh(stream, like, shape)
-    B, T, H, D = shape
-    return t, _pack_rows(t.data_ptr(), T * H * D, H * D)
-
-
-def _turn(q, k, positions, inv_freq, sections, layout, amplitude, inverse, q_out, k_out, stream):
-    B, T, Hq, Hk, D, code, qs, ks = _heads(q, k)
-    dt, dev = q.dtype, q.device
-    vq, vk = _view(q, "q", dt, qs), None if k is None else _view(k, "k", dt, ks)
-    rot = _rotation(positions, inv_freq, sections, layout, amplitude, B, T)
-    if rot is None:
-        raise ValueError("rope needs positions and inv_freq")
-    q_out, oq = _out_view(q_out, "q_out", q, qs, stream)
-    ok = None
-    if k is not None:
-        k_out, ok = _out_view(k_out, "k_out", q, ks, stream)
-    st = _lib.load().gdn_rope(vq, vk, rot, inverse, oq, ok, B, T, Hq, Hk, D, code,
-                              _raw_stream(stream, dev))
-    _lib.check(st, "gdn_rope")
-    if stream is not None:
-        _used_on(stream, q, k, positions, inv_freq, q_out, k_out)
+def _rope(q, k, positions, inv_freq, sections, layout, amplitude, inverse, q_out, k_out, stream):
+    def call():
+        return _lib.bind().rope(q, k, positions, inv_freq, sections, layout, amplitude, inverse, q_out, k_out)
+    st, q_out, k_out = call() if stream is None else _on(stream, call, (q, k, positions, inv_freq))
+    if st:
+        _lib.check(st, "gdn_rope")
     return q_out, k_out
 
 
@@ -369,14 +262,14 @@ def rope(q, k, positions, inv_freq, *, sections=None, layout="half", amplitude=1
     axis.  q and k may be views of one projection; ``q_out`` and ``k_out`` may be
     q and k themselves (in place) or, say, a slot of a cache.  Returns
     ``(q_out, k_out)``."""
-    return _turn(q, k, positions, inv_freq, sections, layout, amplitude, 0, q_out, k_out, stream)
+    return _rope(q, k, positions, inv_freq, sections, layout, amplitude, False, q_out, k_out, stream)
 
 
 def rope_backward(dq_out, dk_out, positions, inv_freq, *, sections=None, layout="half",
                   amplitude=1.0, dq=None, dk=None, stream=None):
     """Gradients of ``rope``: a dict with dq and dk (None without keys), the
     inverse turn of the gradients of its outputs."""
-    dq, dk = _turn(dq_out, dk_out, positions, inv_freq, sections, layout, amplitude, 1, dq, dk, stream)
+    dq, dk = _rope(dq_out, dk_out, positions, inv_freq, sections, layout, amplitude, True, dq, dk, stream)
     return {"dq": dq, "dk": dk}
 
 
@@ -385,21 +278,14 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=No
     """RMS norm over the features of every head of q and k (k may be None), times
     the fp32 weights [D] (None: ones), and the rotary positions of ``rope``
     (none without ``positions``), in one pass.  Returns ``(q_out, k_out)``."""
-    B, T, Hq, Hk, D, code, qs, ks = _heads(q, k)
-    dt, dev = q.dtype, q.device
-    vq, vk = _view(q, "q", dt, qs), None if k is None else _view(k, "k", dt, ks)
-    wq, wk = _weight(q_weight, "q_weight", D), _weight(k_weight, "k_weight", D)
-    rot = _rotation(positions, inv_freq, sections, layout, amplitude, B, T)
-    q_out, oq = _out_view(q_out, "q_out", q, qs, stream)
-    ok = None
-    if k is not None:
-        k_out, ok = _out_view(k_out, "k_out", q, ks, stream)
-    st = _lib.load().gdn_qk_norm_rope(vq, vk, wq, wk, rot, oq, ok, B, T, Hq, Hk, D, eps, code,
-                                      _raw_stream(stream, dev))
-    _lib.check(st, "gdn_qk_norm_rope")
-    if stream is not None:
-        _used_on(stream, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out)
-    return q_out, k_out
+    def call():
+        return _lib.bind().qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps, sections, layout,
+                                        amplitude, q_out, k_out)
+    st, oq, ok = call() if stream is None else _on(
+        stream, call, (q, k, q_weight, k_weight, positions, inv_freq))
+    if st:
+        _lib.check(st, "gdn_qk_norm_rope")
+    return oq, ok
 
 
 def qk_norm_rope_backward(q, k, q_weight, k_weight, dq_out, dk_out, positions=None, inv_freq=None,
@@ -408,54 +294,14 @@ def qk_norm_rope_backward(q, k, q_weight, k_weight, dq_out, dk_out, positions=No
     """Gradients of ``qk_norm_rope`` given its inputs and the gradients of its
     outputs: a dict with dq, dk (q's dtype) and dq_weight, dk_weight (fp32 [D]);
     those of the keys are None without keys."""
-    B, T, Hq, Hk, D, code, qs, ks = _heads(q, k)
-    dt, dev = q.dtype, q.device
-    vq, vk = _view(q, "q", dt, qs), None if k is None else _view(k, "k", dt, ks)
-    wq, wk = _weight(q_weight, "q_weight", D), _weight(k_weight, "k_weight", D)
-    rot = _rotation(positions, inv_freq, sections, layout, amplitude, B, T)
-    gq = _view(dq_out, "dq_out", dt, qs)
-    gk = None if k is None else _view(dk_out, "dk_out", dt, ks)
-    dq, oq = _out_view(dq, "dq", q, qs, stream)
-    dqw = _fresh(stream, q, (D,), torch.float32)
-    ok = dkw = None
-    if k is not None:
-        dk, ok = _out_view(dk, "dk", q, ks, stream)
-        dkw = _fresh(stream, q, (D,), torch.float32)
-    st = _lib.load().gdn_qk_norm_rope_backward(vq, vk, wq, wk, rot, gq, gk, oq, ok, dqw.data_ptr(),
-                                               _ptr(dkw), B, T, Hq, Hk, D, eps, code,
-                                               _raw_stream(stream, dev))
-    _lib.check(st, "gdn_qk_norm_rope_backward")
-    if stream is not None:
-        _used_on(stream, q, k, q_weight, k_weight, positions, inv_freq, dq_out, dk_out, dq, dk, dqw, dkw)
-    return {"dq": dq, "dk": dk, "dq_weight": dqw, "dk_weight": dkw}
-
-
-def _cross_args(q, k, v, key_mask, scale):
-    """Shapes, views, mask pointer and stride, and scale of a cross-attention call."""
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q must be [B,Tq,Hq,D] and k, v [B,S,Hk,D]")
-    B, Tq, Hq, D = q.shape
-    S, Hk = k.shape[1], k.shape[2]
-    if q.dtype != torch.bfloat16:
-        raise TypeError(f"q, k, v must be bfloat16, got {q.dtype}")
-    qs, ks = (B, Tq, Hq, D), (B, S, Hk, D)
-    vq = _view(q, "q", torch.bfloat16, qs)
-    vk, vv = _view(k, "k", torch.bfloat16, ks), _view(v, "v", torch.bfloat16, ks)
-    mp, ms = None, 0
-    if key_mask is not None:
-        if not key_mask.is_cuda:
-            raise ValueError("key_mask must be a CUDA tensor")
-        if key_mask.dtype != torch.bool and key_mask.dtype != torch.uint8:
-            raise TypeError(f"key_mask must be bool or uint8, got {key_mask.dtype}")
-        if key_mask.shape != (B, S):
-            raise ValueError(f"key_mask must have shape {(B, S)}, got {tuple(key_mask.shape)}")
-        ms, step = key_mask.stride()
-        if S > 1 and step != 1:
-            raise ValueError("key_mask must be contiguous over the keys")
-        mp, ms = key_mask.data_ptr(), ms if B > 1 else 0
-    if scale is None:
-        scale = D ** -0.5 if D else 1.0
-    return B, Tq, S, Hq, Hk, D, vq, vk, vv, mp, ms, scale
+    def call():
+        return _lib.bind().qk_norm_rope_backward(q, k, q_weight, k_weight, dq_out, dk_out, positions, inv_freq,
+                                                 eps, sections, layout, amplitude, dq, dk)
+    st, gq, gk, wq, wk = call() if stream is None else _on(
+        stream, call, (q, k, q_weight, k_weight, dq_out, dk_out, positions, inv_freq))
+    if st:
+        _lib.check(st, "gdn_qk_norm_rope_backward")
+    return {"dq": gq, "dk": gk, "dq_weight": wq, "dk_weight": wk}
 
 
 def cross_attention(q, k, v, key_mask=None, *, scale=None, out=None, return_lse=False, stream=None):
@@ -466,42 +312,23 @@ def cross_attention(q, k, v, key_mask=None, *, scale=None, out=None, return_lse=
     views of one projection, or expanded over the batch.  Returns ``out``
     [B,Tq,Hq,D], or ``(out, lse)`` with lse [B,Hq,Tq] fp32, which
     ``cross_attention_backward`` takes."""
-    B, Tq, S, Hq, Hk, D, vq, vk, vv, mp, ms, scale = _cross_args(q, k, v, key_mask, scale)
-    dev = q.device
-    if out is None:
-        out = _fresh(stream, q, (B, Tq, Hq, D))
-    else:
-        _check_tensor(out, "out", torch.bfloat16, (B, Tq, Hq, D))
-    lse = None
-    if return_lse:
-        lse = _fresh(stream, q, (B, Hq, Tq), torch.float32)
-    st = _lib.load().gdn_cross_attention(vq, vk, vv, mp, ms, out.data_ptr(), _ptr(lse), B, Tq, S, Hq,
-                                         Hk, D, scale, _lib.GDN_BF16, _raw_stream(stream, dev))
-    _lib.check(st, "gdn_cross_attention")
-    if stream is not None:
-        _used_on(stream, q, k, v, key_mask, out, lse)
-    return (out, lse) if return_lse else out
+    def call():
+        return _lib.bind().cross_attention(q, k, v, key_mask, scale, out, return_lse)
+    st, o, lse = call() if stream is None else _on(stream, call, (q, k, v, key_mask))
+    if st:
+        _lib.check(st, "gdn_cross_attention")
+    return (o, lse) if return_lse else o
 
 
 def cross_attention_backward(q, k, v, out, lse, d_out, key_mask=None, *, scale=None, stream=None):
     """Gradients of ``cross_attention`` given its inputs, its results ``out`` and
     ``lse`` and the gradient of ``out``: a dict with dq, dk and dv (bf16).  For k, v
     expanded over the batch dk and dv hold each batch row's share."""
-    B, Tq, S, Hq, Hk, D, vq, vk, vv, mp, ms, scale = _cross_args(q, k, v, key_mask, scale)
-    dev = q.device
-    _check_tensor(out, "out", torch.bfloat16, (B, Tq, Hq, D))
-    _check_tensor(lse, "lse", torch.float32, (B, Hq, Tq))
-    _check_tensor(d_out, "d_out", torch.bfloat16, (B, Tq, Hq, D))
-    dq = _fresh(stream, q, (B, Tq, Hq, D))
-    dk = _fresh(stream, q, (B, S, Hk, D))
-    dv = _fresh(stream, q, (B, S, Hk, D))
-    st = _lib.load().gdn_cross_attention_backward(
-        vq, vk, vv, mp, ms, out.data_ptr(), lse.data_ptr(), d_out.data_ptr(), dq.data_ptr(),
-        dk.data_ptr(), dv.data_ptr(), B, Tq, S, Hq, Hk, D, scale, _lib.GDN_BF16,
-        _raw_stream(stream, dev))
-    _lib.check(st, "gdn_cross_attention_backward")
-    if stream is not None:
-        _used_on(stream, q, k, v, key_mask, out, lse, d_out, dq, dk, dv)
+    def call():
+        return _lib.bind().cross_attention_backward(q, k, v, out, lse, d_out, key_mask, scale)
+    st, dq, dk, dv = call() if stream is None else _on(stream, call, (q, k, v, out, lse, d_out, key_mask))
+    if st:
+        _lib.check(st, "gdn_cross_attention_backward")
     return {"dq": dq, "dk": dk, "dv": dv}
 
 

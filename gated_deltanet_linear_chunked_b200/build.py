@@ -1,4 +1,4 @@
-"""Build libgdn.so in-tree with nvcc for sm_100a.
+"""Build libgdn.so in-tree with nvcc for sm_100a, and the compiled torch binding.
 
     python -m gated_deltanet_linear_chunked_b200.build [--force]
 
@@ -7,6 +7,10 @@ Compiles every ``csrc/*.cu`` into one shared library beside this file
 runtime is linked statically, so the library loads on a machine without a
 GPU (the ABI tests use that); the CUDA driver API (tensor maps) is reached at run
 time through ``cudaGetDriverEntryPoint``.
+
+``csrc/torch_bind.cpp``, the argument marshalling of the softmax blocks'
+operators, becomes ``_gdn_torch.so`` with g++ against the installed torch; it does
+not link libgdn.so (the loader hands it the entry points' addresses).
 """
 from __future__ import annotations
 
@@ -20,6 +24,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libgdn.so")
+BIND_SRC = os.path.join(CSRC, "torch_bind.cpp")
+BIND_PATH = os.path.join(PKG, "_gdn_torch.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -60,5 +66,37 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB_PATH
 
 
+def bind_is_stale() -> bool:
+    if not os.path.exists(BIND_PATH):
+        return True
+    t = os.path.getmtime(BIND_PATH)
+    return any(os.path.getmtime(p) > t for p in (BIND_SRC, os.path.join(INCLUDE, "gdn.h")))
+
+
+def build_bind(force: bool = False, verbose: bool = False) -> str:
+    """Compile _gdn_torch.so if it is missing or older than its source."""
+    if not force and not bind_is_stale():
+        return BIND_PATH
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    tmp = BIND_PATH + ".tmp.%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-DTORCH_EXTENSION_NAME=_gdn_torch",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi()),
+           "-I", INCLUDE, "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", cuda, "-isystem", sysconfig.get_paths()["include"], BIND_SRC, "-o", tmp,
+           "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True, cwd=PKG)
+    os.replace(tmp, BIND_PATH)
+    return BIND_PATH
+
+
 if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose=True)
+    build_bind(force="--force" in sys.argv, verbose=True)

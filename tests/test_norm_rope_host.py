@@ -3,6 +3,7 @@ the binding's refusals, and the C entry's argument checks (fake pointers: every
 refusal here happens before any CUDA call)."""
 import ctypes
 import math
+import struct
 
 import pytest
 import torch
@@ -11,6 +12,7 @@ import gated_deltanet_linear_chunked_b200 as gdn
 from gated_deltanet_linear_chunked_b200 import _lib
 
 BASE = 0x7F0000000000
+ROWS, ROTATION = struct.Struct("Pqq"), struct.Struct("PPqiiiiiiif")  # gdn_rows, gdn_rotation
 
 
 def fake(i):
@@ -74,11 +76,11 @@ def test_binding_refuses_cpu_tensors_and_other_types():
 # ------------------------------------------------------------------ C entry
 def rows(i, H=2, D=64, T=8, off=0, bs=None, ts=None):
     ts = H * D if ts is None else ts
-    return _lib.ROWS.pack(fake(i) + off, T * ts if bs is None else bs, ts)
+    return ROWS.pack(fake(i) + off, T * ts if bs is None else bs, ts)
 
 
 def rot(pos=fake(20), freq=fake(21), bs=8, pb=8, axes=1, sec=(16, 0, 0), R=32, layout=0, amp=1.0):
-    return _lib.ROTATION.pack(pos, freq, bs, pb, axes, *sec, R, layout, amp)
+    return ROTATION.pack(pos, freq, bs, pb, axes, *sec, R, layout, amp)
 
 
 def call(q=rows(0), k=rows(1), wq=fake(2), wk=fake(3), r=rot(), qo=rows(4), ko=rows(5), B=2, T=8, Hq=2,
@@ -97,7 +99,7 @@ REACHES_DEVICE = (_lib.GDN_ERR_CUDA, _lib.GDN_ERR_INVALID_ARG)
 
 
 def test_struct_sizes():
-    assert _lib.ROWS.size == 24 and _lib.ROTATION.size == 56
+    assert ROWS.size == 24 and ROTATION.size == 56
 
 
 def test_sizes_and_types():
@@ -126,7 +128,7 @@ def test_rotation_checks():
 def test_pointers_and_strides():
     for name in ("q", "k", "qo", "ko"):
         assert call(**{name: None}) == _lib.GDN_ERR_INVALID_ARG, name
-        assert call(**{name: _lib.ROWS.pack(0, 1024, 128)}) == _lib.GDN_ERR_INVALID_ARG, name
+        assert call(**{name: ROWS.pack(0, 1024, 128)}) == _lib.GDN_ERR_INVALID_ARG, name
         assert call(**{name: rows(9, off=8)}) == _lib.GDN_ERR_INVALID_ARG, name
         assert call(**{name: rows(9, ts=132)}) == _lib.GDN_ERR_INVALID_ARG, name
         assert call(**{name: rows(9, ts=-128)}) == _lib.GDN_ERR_INVALID_ARG, name
@@ -144,8 +146,8 @@ def test_overlaps():
     assert call(ko=rows(4)) == _lib.GDN_ERR_ALIAS                   # both outputs in one place
     assert call(qo=rows(4, ts=64)) == _lib.GDN_ERR_ALIAS            # rows of the output overlap
     assert call(qo=rows(4, bs=0)) == _lib.GDN_ERR_ALIAS             # one output for two batch rows
-    assert call(qo=_lib.ROWS.pack(fake(2), 1024, 128)) == _lib.GDN_ERR_ALIAS   # over a weight
-    assert call(qo=_lib.ROWS.pack(fake(20), 1024, 128)) == _lib.GDN_ERR_ALIAS  # over the positions
+    assert call(qo=ROWS.pack(fake(2), 1024, 128)) == _lib.GDN_ERR_ALIAS   # over a weight
+    assert call(qo=ROWS.pack(fake(20), 1024, 128)) == _lib.GDN_ERR_ALIAS  # over the positions
     # q, k side by side in one projection, in place
     p = dict(ts=384, bs=8 * 384)
     assert call(q=rows(0, **p), k=rows(0, off=256, **p), qo=rows(0, **p),
