@@ -54,6 +54,7 @@
 #include <cmath>
 #include <mutex>
 
+#include "cross_attn.cuh"
 #include "gdn_internal.h"
 #include "sm100.cuh"
 
@@ -76,26 +77,6 @@ constexpr uint32_t kBlock = kRows * 128;  // one 64-feature block of a 128-row t
 constexpr int kMaskTiles = 128;        // key tiles of one CTA under a mask, at most
 constexpr float kRescaleLog2 = 8.f;
 constexpr long long kDrainPolls = 1LL << 40;  // drains are bounded by the 2 s timer
-
-struct CrossParams {
-  int Tq, S, Hk, G, D;
-  int tokens;            // query tokens per tile: 128 / G
-  int gmul;              // r / G = r * gmul >> 16 for rows r < 128
-  int qtiles, groups;    // query tiles of a (b, key head); units along them (NQ tiles each)
-  int ntiles;            // key tiles
-  unsigned full;         // units that one CTA each takes whole; those behind them ...
-  int nsplit, per_split; // ... are split along the keys: CTAs of a unit, tiles of each
-  int qb, kb, vb;        // batch coordinate factors: 0 for a broadcast batch
-  const uint8_t* mask;
-  long long mask_bs;
-  float scale_log2;      // scale * log2(e)
-  __nv_bfloat16* out;    // [B, Tq, Hq, D]
-  float* lse;            // [B, Hq, Tq] or nullptr
-  float* part_o;         // [split units][nsplit][NQ * 128 rows][D] fp32
-  float* part_lse;       // [split units][nsplit][NQ * 128 rows]
-  long long limit;
-  unsigned* err;
-};
 
 template <int NQ>
 struct CrossAux {
@@ -409,7 +390,7 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           uint64_t p2;
           float a, e;
           if ((i & 7) == 6) {
-            p2 = exp2_poly2(x);
+            p2 = exp2_poly2_fine(x);
             f2_unpack(p2, a, e);
           } else {
             f2_unpack(x, a, e);
@@ -495,15 +476,14 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 // row of the split units, four features a lane.
 constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads)
-gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int nq, long long rows) {
+gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int per, long long rows) {
   const long long i = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (i >= rows) return;
-  const int per = nq * kRows;                         // rows of a unit
-  const long long su = i / per;
+  const long long su = i / per;                       // per: rows of a unit, in whole tiles or one of few
   const int ur = (int)(i - su * per), r = ur % kRows;
   const long long u = P.full + su, bh = u / P.groups;
-  const int tile = (int)(u - bh * P.groups) * nq + ur / kRows;
+  const int tile = ((int)(u - bh * P.groups) * per + ur) / kRows;
   const long long b = bh / P.Hk;
   const int hk = (int)(bh - b * P.Hk), t = tile * P.tokens + r / P.G, head = hk * P.G + r % P.G;
   if (r >= P.tokens * P.G || t >= P.Tq) return;       // no row
@@ -535,16 +515,24 @@ gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int nq, long long r
   if (lane == 0 && P.lse) P.lse[(b * Hq + head) * P.Tq + t] = any ? top + logf(sum) : -INFINITY;
 }
 
-// The shape of a call: query tiles of a CTA, units, splits along the keys.
-// Returns the query tiles of a CTA.
+// The shape of a call: units, splits along the keys.  Returns the rows of a unit:
+// one or two tiles, or kFewRows for the kernel of few rows.
 int cross_shape(const CrossCall& c, CrossParams* P) {
   P->Tq = c.Tq;
   P->S = c.S;
   P->Hk = c.Hk;
   P->G = c.Hq / c.Hk;
   P->D = c.D;
-  P->tokens = kRows / P->G;
   P->gmul = 65536 / P->G + 1;
+  if ((long long)c.Tq * P->G <= kFewRows) {
+    const int units = c.B * c.Hk;
+    P->tokens = c.Tq;
+    P->qtiles = P->groups = 1;
+    P->nsplit = few_splits(c.B, c.Hk, c.S);
+    P->full = P->nsplit > 1 ? 0 : units;
+    return kFewRows;
+  }
+  P->tokens = kRows / P->G;
   P->qtiles = (c.Tq + P->tokens - 1) / P->tokens;
   P->ntiles = (c.S + kRows - 1) / kRows;
   // Up to 16 key tiles two CTAs of one query tile each share an SM, their starts
@@ -568,7 +556,7 @@ int cross_shape(const CrossCall& c, CrossParams* P) {
   }
   P->per_split = (int)std::max<long long>(1, (P->ntiles + n - 1) / n);
   P->nsplit = std::max(1, (P->ntiles + P->per_split - 1) / P->per_split);
-  return nq;
+  return nq * kRows;
 }
 
 // CTAs of the split units.
@@ -590,17 +578,43 @@ cudaError_t launch_nb(unsigned grid, cudaStream_t stream, const CUtensorMap& mq,
   return cudaSuccess;
 }
 
+cudaError_t launch_tiles(const CrossCall& c, CrossParams* P, int nq, unsigned grid) {
+  P->qb = c.q.batch_stride != 0;
+  P->kb = c.k.batch_stride != 0;
+  P->vb = c.v.batch_stride != 0;
+  CUtensorMap mq, mk, mv;
+  if (!make_heads_map(&mq, c.q.data, P->qb ? c.B : 1, c.Tq, c.Hk, P->G, c.D, c.q.batch_stride, c.q.token_stride,
+                      P->tokens))
+    return cudaErrorInvalidValue;
+  if (c.S == 0) {
+    mk = mv = mq;  // no key tile is ever loaded
+  } else if (!make_heads_map(&mk, c.k.data, P->kb ? c.B : 1, c.S, c.Hk, 1, c.D, c.k.batch_stride,
+                             c.k.token_stride, kRows) ||
+             !make_heads_map(&mv, c.v.data, P->vb ? c.B : 1, c.S, c.Hk, 1, c.D, c.v.batch_stride,
+                             c.v.token_stride, kRows)) {
+    return cudaErrorInvalidValue;
+  }
+  cudaError_t e;
+  if (nq == 1)
+    e = c.D > 64 ? launch_nb<2, 1>(grid, c.stream, mq, mk, mv, *P) : launch_nb<1, 1>(grid, c.stream, mq, mk, mv, *P);
+  else
+    e = c.D > 64 ? launch_nb<2, 2>(grid, c.stream, mq, mk, mv, *P) : launch_nb<1, 2>(grid, c.stream, mq, mk, mv, *P);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e == cudaSuccess) count_launches(1);
+  return e;
+}
+
 }  // namespace
 
 size_t cross_workspace_bytes(const CrossCall& c) {
   CrossParams P = {};
-  const int nq = cross_shape(c, &P);
-  return (size_t)split_blocks(c, P) * nq * kRows * (c.D + 1) * sizeof(float);
+  const int per = cross_shape(c, &P);
+  return (size_t)split_blocks(c, P) * per * (c.D + 1) * sizeof(float);
 }
 
 cudaError_t launch_cross(const CrossCall& c, void* ws) {
   CrossParams P = {};
-  const int nq = cross_shape(c, &P);
+  const int per = cross_shape(c, &P);
   const long long parts = split_blocks(c, P);
   P.mask = c.mask;
   P.mask_bs = c.mask_bs;
@@ -608,40 +622,16 @@ cudaError_t launch_cross(const CrossCall& c, void* ws) {
   P.out = static_cast<__nv_bfloat16*>(c.out);
   P.lse = c.lse;
   P.part_o = static_cast<float*>(ws);
-  P.part_lse = P.part_o + (size_t)parts * nq * kRows * c.D;
+  P.part_lse = P.part_o + (size_t)parts * per * c.D;
   P.limit = c.limit;
   P.err = c.err;
-  P.qb = c.q.batch_stride != 0;
-  P.kb = c.k.batch_stride != 0;
-  P.vb = c.v.batch_stride != 0;
-  CUtensorMap mq, mk, mv;
-  if (!make_heads_map(&mq, c.q.data, P.qb ? c.B : 1, c.Tq, c.Hk, P.G, c.D, c.q.batch_stride,
-                      c.q.token_stride, P.tokens))
-    return cudaErrorInvalidValue;
-  if (c.S == 0) {
-    mk = mv = mq;  // no key tile is ever loaded
-  } else if (!make_heads_map(&mk, c.k.data, P.kb ? c.B : 1, c.S, c.Hk, 1, c.D, c.k.batch_stride,
-                             c.k.token_stride, kRows) ||
-             !make_heads_map(&mv, c.v.data, P.vb ? c.B : 1, c.S, c.Hk, 1, c.D, c.v.batch_stride,
-                             c.v.token_stride, kRows)) {
-    return cudaErrorInvalidValue;
-  }
-  const unsigned grid = (unsigned)(P.full + parts);
-  cudaError_t e;
-  if (nq == 1)
-    e = c.D > 64 ? launch_nb<2, 1>(grid, c.stream, mq, mk, mv, P)
-                 : launch_nb<1, 1>(grid, c.stream, mq, mk, mv, P);
-  else
-    e = c.D > 64 ? launch_nb<2, 2>(grid, c.stream, mq, mk, mv, P)
-                 : launch_nb<1, 2>(grid, c.stream, mq, mk, mv, P);
-  if (e == cudaSuccess) e = cudaGetLastError();
+  cudaError_t e = per == kFewRows ? launch_cross_few(c, P) : launch_tiles(c, &P, per / kRows, (unsigned)(P.full + parts));
   if (e != cudaSuccess) return e;
-  count_launches(1);
   if (parts > 0) {
     ProfileScope ps(c.stream, kKernCrossJoin);
-    const long long rows = parts / P.nsplit * nq * kRows;
+    const long long rows = parts / P.nsplit * per;
     const unsigned blocks = (unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
-    e = launch_after(gdn_cross_join_kernel, blocks, kJoinThreads, 0, c.stream, P, nq, rows);
+    e = launch_after(gdn_cross_join_kernel, blocks, kJoinThreads, 0, c.stream, P, per, rows);
     if (e == cudaSuccess) count_launches(1);
   }
   return e;

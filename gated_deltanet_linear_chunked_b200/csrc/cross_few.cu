@@ -1,0 +1,320 @@
+// cross_few.cu -- the attention to the encoder's states for a few query rows: at
+// most 16 of them, tokens times the query heads of a key head, as when one token is
+// generated at a time.
+//
+// Nothing but the keys and values is large, so the kernel is a stream over them: a
+// warp takes every W-th group of 16 keys of its (b, key head), W being all warps on
+// it, and keeps three groups of K and V on their way into its own piece of shared
+// memory (16-byte asynchronous copies, no barrier between warps).  The 16 rows are
+// one mma.sync tile (m16n8k16: S = Q K^T over the features, then O += P V), with
+// the running maximum and sum of each row in registers; a 128-row tcgen05 tile would
+// spend its time on 112 rows that are none.  Masked keys are not copied: their rows
+// arrive as zeros (so that 0 * NaN never arises), their scores become -inf, and
+// groups without any seen key are skipped.  The warps of a CTA join in shared
+// memory, CTAs of one (b, key head) through gdn_cross_join_kernel.
+// 8 queries of 16 heads over 4096 keys of 4 heads, 128 wide, an eighth masked: see
+// the figures in the launch rule.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "cross_attn.cuh"
+#include "gdn_internal.h"
+#include "sm100.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace sm100;
+
+constexpr int kWarps = 4;
+constexpr int kKeys = 16;     // keys of a group
+constexpr int kDepth = 3;     // groups on their way per warp
+
+// 16 bytes to shared memory, zeros where `on` is false (then nothing is read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+struct FewParams {
+  CrossParams c;
+  const __nv_bfloat16 *q, *k, *v;
+  long long q_bs, q_ts, k_bs, k_ts, v_bs, v_ts;
+};
+
+// Shared memory of a warp: kDepth x (K, V) groups of 16 rows of D features, 16-byte
+// piece c of row r at piece c ^ (r & 7) (rows of D / 8 pieces; D = 16 has two).
+template <int NK>
+struct FewLayout {
+  static constexpr int pieces = 2 * NK;                    // of a row
+  static constexpr uint32_t group = kKeys * pieces * 16;   // K or V of a group, bytes
+  static constexpr uint32_t warp = kDepth * 2 * group;
+  // the joined rows: [kWarps][16][D] fp32 and the rows' maxima and sums
+  static constexpr uint32_t join = kWarps * 16 * (16 * NK) * 4;
+  static constexpr uint32_t total = (kWarps * warp > join ? kWarps * warp : join) + kWarps * 16 * 8;
+};
+
+template <int NK>  // D / 16
+__global__ void __launch_bounds__(32 * kWarps, 2)
+gdn_cross_few_kernel(const __grid_constant__ FewParams F) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  using L = FewLayout<NK>;
+  constexpr int D = 16 * NK, kPieces = L::pieces;
+  const CrossParams& P = F.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = blockIdx.x % P.nsplit, bh = blockIdx.x / P.nsplit;
+  const int b = bh / P.Hk, hk = bh - b * P.Hk;
+  const int rows = P.tokens * P.G;  // of the 16
+  const int Hq = P.Hk * P.G;
+  pdl_trigger();
+
+  // piece c of row r of a group: swizzled within aligned runs of eight pieces, or of
+  // the whole row where it has fewer; rows of 6, 10, 12, 14 pieces keep their tail
+  auto piece = [&](int r, int c) -> uint32_t {
+    constexpr int run = kPieces >= 8 ? 8 : kPieces >= 4 ? 4 : 2;
+    const int base = c & ~(run - 1);
+    const int cc = base + run <= kPieces ? base + ((c ^ r) & (run - 1)) : c;
+    return (uint32_t)(r * kPieces + cc) * 16;
+  };
+
+  // Q as left operands, row r = token * G + head, straight from memory
+  uint32_t qa[NK][4];
+  {
+    const int g = lane >> 2, t2 = (lane & 3) * 2;
+    const __nv_bfloat16* row[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = g + 8 * i, dt = r * P.gmul >> 16, dh = r - dt * P.G;
+      row[i] = r < rows ? F.q + b * F.q_bs + dt * F.q_ts + (hk * P.G + dh) * D : nullptr;
+    }
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat16* p = row[i & 1];
+        qa[ks][i] = p ? *reinterpret_cast<const uint32_t*>(p + 16 * ks + t2 + 8 * (i >> 1)) : 0u;
+      }
+  }
+
+  const int workers = P.nsplit * kWarps, me = split * kWarps + warp;
+  const int groups = (P.S + kKeys - 1) / kKeys;
+  const uint8_t* mrow = P.mask ? P.mask + b * P.mask_bs : nullptr;
+  const __nv_bfloat16* kbase = F.k + b * F.k_bs + hk * D;
+  const __nv_bfloat16* vbase = F.v + b * F.v_bs + hk * D;
+  const uint32_t base = smem_u32(smem) + warp * L::warp;
+
+  // which of the 16 keys of group i are seen
+  auto seen_of = [&](int i) -> uint32_t {
+    const long long key = (long long)i * kKeys + (lane & 15);
+    const bool on = i < groups && key < P.S && (!mrow || mrow[key] != 0);
+    return __ballot_sync(~0u, on) & 0xFFFFu;
+  };
+  auto fetch = [&](int i, uint32_t seen, int slot) {
+    if (seen) {
+      const uint32_t dk = base + slot * 2 * L::group, dv = dk + L::group;
+#pragma unroll
+      for (int x = 0; x < kKeys * kPieces; x += 32) {
+        const int y = x + lane, r = y / kPieces, c = y - r * kPieces;
+        if (kKeys * kPieces % 32 == 0 || y < kKeys * kPieces) {
+          const bool on = seen >> r & 1;
+          const long long key = on ? (long long)i * kKeys + r : 0;
+          copy16(dk + piece(r, c), kbase + key * F.k_ts + c * 8, on);
+          copy16(dv + piece(r, c), vbase + key * F.v_ts + c * 8, on);
+        }
+      }
+    }
+    copy_commit();
+  };
+
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float o[2 * NK][4];
+#pragma unroll
+  for (int i = 0; i < 2 * NK; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+  // seen bits of the groups in flight, and of the one to be fetched next
+  uint32_t seen[kDepth];
+#pragma unroll
+  for (int s = 0; s < kDepth - 1; ++s) {
+    seen[s] = seen_of(me + s * workers);
+    fetch(me + s * workers, seen[s], s);
+  }
+  seen[kDepth - 1] = 0;
+  uint32_t coming = seen_of(me + (kDepth - 1) * workers);
+
+  int slot = 0;
+  for (int i = me; i < groups; i += workers) {
+    // the slot used two groups ago takes the group two ahead
+    const int into = slot >= 1 ? slot - 1 : kDepth - 1;
+    const uint32_t next = coming;
+    __syncwarp();  // every lane is done with that slot
+    fetch(i + (kDepth - 1) * workers, next, into);
+    coming = seen_of(i + kDepth * workers);
+    copy_wait<kDepth - 1>();
+    __syncwarp();
+    const uint32_t now = seen[0];
+#pragma unroll
+    for (int s = 0; s + 1 < kDepth; ++s) seen[s] = seen[s + 1];
+    seen[kDepth - 2] = next;
+    if (now) {
+      const uint32_t tk = base + slot * 2 * L::group, tv = tk + L::group;
+      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+      const int mat = lane >> 3, mr = lane & 7;
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks) {
+        uint32_t kb[4];  // keys 0-7: features 0-7, 8-15; keys 8-15: the same
+        ldmatrix_x4(tk + piece(mr + 8 * (mat >> 1), 2 * ks + (mat & 1)), kb);
+        mma_16816(s0, qa[ks], kb[0], kb[1]);
+        mma_16816(s1, qa[ks], kb[2], kb[3]);
+      }
+      // lane: rows lane / 4 and that + 8, keys 2 (lane % 4) + {0, 1} and those + 8
+      const int t2 = (lane & 3) * 2;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const bool a = now >> (t2 + e) & 1, c = now >> (t2 + 8 + e) & 1;
+        s0[e] = a ? s0[e] * P.scale_log2 : -INFINITY;
+        s0[2 + e] = a ? s0[2 + e] * P.scale_log2 : -INFINITY;
+        s1[e] = c ? s1[e] * P.scale_log2 : -INFINITY;
+        s1[2 + e] = c ? s1[2 + e] * P.scale_log2 : -INFINITY;
+      }
+      uint32_t pa[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float mx = fmaxf(fmaxf(s0[2 * h], s0[2 * h + 1]), fmaxf(s1[2 * h], s1[2 * h + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
+        const float mn = fmaxf(m[h], mx);  // finite: the group has a seen key
+        const float alpha = exp2f(m[h] - mn);
+        m[h] = mn;
+        const float p0 = exp2f(s0[2 * h] - mn), p1 = exp2f(s0[2 * h + 1] - mn);
+        const float p2 = exp2f(s1[2 * h] - mn), p3 = exp2f(s1[2 * h + 1] - mn);
+        l[h] = l[h] * alpha + ((p0 + p1) + (p2 + p3));  // this lane's four keys
+        pa[h] = pack_bf16x2(p0, p1);
+        pa[2 + h] = pack_bf16x2(p2, p3);
+#pragma unroll
+        for (int f = 0; f < 2 * NK; ++f) {
+          o[f][2 * h] *= alpha;
+          o[f][2 * h + 1] *= alpha;
+        }
+      }
+#pragma unroll
+      for (int f = 0; f < NK; ++f) {
+        uint32_t vb[4];  // features 0-7: keys 0-7, 8-15; features 8-15: the same
+        ldmatrix_x4_trans(tv + piece(mr + 8 * (mat & 1), 2 * f + (mat >> 1)), vb);
+        mma_16816(o[2 * f], pa, vb[0], vb[1]);
+        mma_16816(o[2 * f + 1], pa, vb[2], vb[3]);
+      }
+    }
+    slot = slot + 1 == kDepth ? 0 : slot + 1;
+  }
+  copy_wait<0>();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    l[h] += __shfl_xor_sync(~0u, l[h], 1);
+    l[h] += __shfl_xor_sync(~0u, l[h], 2);
+  }
+
+  // join the CTA's warps: rows and their (m, l) over the groups' memory
+  __syncthreads();
+  float* ow = reinterpret_cast<float*>(smem) + warp * 16 * D;
+  float2* ml = reinterpret_cast<float2*>(smem + L::total - kWarps * 16 * 8);
+  {
+    const int g = lane >> 2, t2 = (lane & 3) * 2;
+#pragma unroll
+    for (int f = 0; f < 2 * NK; ++f) {
+      *reinterpret_cast<float2*>(ow + g * D + 8 * f + t2) = make_float2(o[f][0], o[f][1]);
+      *reinterpret_cast<float2*>(ow + (g + 8) * D + 8 * f + t2) = make_float2(o[f][2], o[f][3]);
+    }
+    if ((lane & 3) == 0) {
+      ml[warp * 16 + g] = make_float2(m[0], l[0]);
+      ml[warp * 16 + g + 8] = make_float2(m[1], l[1]);
+    }
+  }
+  __syncthreads();
+  for (int x = threadIdx.x; x < rows * (D / 4); x += 32 * kWarps) {
+    const int r = x / (D / 4), f = (x - r * (D / 4)) * 4;
+    float top = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * 16 + r].x);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 v = ml[w * 16 + r];
+      const float a = v.x > -INFINITY ? exp2f(v.x - top) : 0.f;
+      const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) + (w * 16 + r) * D + f);
+      sum += a * v.y;
+      acc[0] += a * y.x;
+      acc[1] += a * y.y;
+      acc[2] += a * y.z;
+      acc[3] += a * y.w;
+    }
+    const bool any = top > -INFINITY;
+    const float inv = any ? 1.f / sum : 0.f;
+    const float lse = any ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    if (P.nsplit > 1) {
+      const long long at = (long long)blockIdx.x * kFewRows + r;
+      if (f == 0) P.part_lse[at] = lse;
+      *reinterpret_cast<float4*>(P.part_o + at * D + f) =
+          make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+    } else {
+      const int dt = r * P.gmul >> 16, head = hk * P.G + r - dt * P.G;
+      const long long at = ((long long)b * P.Tq + dt) * Hq + head;
+      if (f == 0 && P.lse) P.lse[((long long)b * Hq + head) * P.Tq + dt] = lse;
+      *reinterpret_cast<uint2*>(P.out + at * D + f) =
+          make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    }
+  }
+}
+
+template <int NK>
+cudaError_t launch_nk(const FewParams& F, unsigned grid, cudaStream_t stream) {
+  constexpr int bytes = FewLayout<NK>::total;
+  const cudaError_t e = allow_smem(gdn_cross_few_kernel<NK>, bytes);
+  if (e != cudaSuccess) return e;
+  ProfileScope ps(stream, kKernCrossFew);
+  gdn_cross_few_kernel<NK><<<grid, 32 * kWarps, bytes, stream>>>(F);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Two CTAs an SM, each warp at least two groups of keys.
+int few_splits(int B, int Hk, int S) {
+  const long long units = (long long)B * Hk;
+  const long long most = ((S + kKeys - 1) / kKeys) / (2 * kWarps);
+  return (int)std::max<long long>(1, std::min<long long>(2 * num_sms() / units, most));
+}
+
+cudaError_t launch_cross_few(const CrossCall& c, const CrossParams& P) {
+  FewParams F;
+  F.c = P;
+  F.q = static_cast<const __nv_bfloat16*>(c.q.data);
+  F.k = static_cast<const __nv_bfloat16*>(c.k.data);
+  F.v = static_cast<const __nv_bfloat16*>(c.v.data);
+  F.q_bs = c.B > 1 ? c.q.batch_stride : 0;
+  F.q_ts = c.q.token_stride;
+  F.k_bs = c.B > 1 ? c.k.batch_stride : 0;
+  F.k_ts = c.k.token_stride;
+  F.v_bs = c.B > 1 ? c.v.batch_stride : 0;
+  F.v_ts = c.v.token_stride;
+  const unsigned grid = (unsigned)(c.B * c.Hk * P.nsplit);
+  cudaError_t e;
+  switch (c.D / 16) {
+    case 1: e = launch_nk<1>(F, grid, c.stream); break;
+    case 2: e = launch_nk<2>(F, grid, c.stream); break;
+    case 3: e = launch_nk<3>(F, grid, c.stream); break;
+    case 4: e = launch_nk<4>(F, grid, c.stream); break;
+    case 5: e = launch_nk<5>(F, grid, c.stream); break;
+    case 6: e = launch_nk<6>(F, grid, c.stream); break;
+    case 7: e = launch_nk<7>(F, grid, c.stream); break;
+    default: e = launch_nk<8>(F, grid, c.stream); break;
+  }
+  if (e == cudaSuccess) count_launches(1);
+  return e;
+}
+
+}  // namespace gdn

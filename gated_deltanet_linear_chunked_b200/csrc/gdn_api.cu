@@ -784,6 +784,7 @@ const char* gdn_kernel_name(int id) {
     case gdn::kKernCrossBwd: return "gdn_cross_bwd_kernel";
     case gdn::kKernCrossDkvJoin: return "gdn_cross_dkv_join_kernel";
     case gdn::kKernCrossStat: return "gdn_cross_stat_kernel";
+    case gdn::kKernCrossFew: return "gdn_cross_few_kernel";
   }
   return "unknown";
 }

@@ -74,7 +74,8 @@ enum KernelId : int {
   kKernCrossBwd = 16,
   kKernCrossDkvJoin = 17,
   kKernCrossStat = 18,
-  kNumKernelIds = 19,
+  kKernCrossFew = 19,
+  kNumKernelIds = 20,
 };
 
 // While profiling is armed, records CUDA events around one launch.

@@ -493,6 +493,28 @@ __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x) {
                  __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23)));
 }
 
+// The same with a polynomial of degree 5, fitted the same way: largest relative
+// error 7.5e-8, 2.0e-7 as evaluated in fp32.  For sums of exponentials that leave
+// as fp32 (a log-sum-exp), which the shorter one would limit to 1e-5.
+__device__ __forceinline__ uint64_t exp2_poly2_fine(uint64_t x) {
+  float x0, x1;
+  f2_unpack(x, x0, x1);
+  const uint64_t xc = f2_pack(fmaxf(x0, -125.f), fmaxf(x1, -125.f));
+  const uint64_t t = f2_add(xc, f2_pack(12582912.f, 12582912.f));  // n in the low bits
+  const uint64_t n = f2_add(t, f2_pack(-12582912.f, -12582912.f));
+  const uint64_t f = f2_fma(n, f2_pack(-1.f, -1.f), xc);           // x - n
+  uint64_t p = f2_fma(f2_pack(1.327647245e-3f, 1.327647245e-3f), f, f2_pack(9.675547481e-3f, 9.675547481e-3f));
+  p = f2_fma(p, f, f2_pack(0.05550713465f, 0.05550713465f));
+  p = f2_fma(p, f, f2_pack(0.2402212024f, 0.2402212024f));
+  p = f2_fma(p, f, f2_pack(0.693146944f, 0.693146944f));
+  p = f2_fma(p, f, f2_pack(1.000000119f, 1.000000119f));
+  float p0, p1, t0, t1;
+  f2_unpack(p, p0, p1);
+  f2_unpack(t, t0, t1);
+  return f2_pack(__uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23)),
+                 __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23)));
+}
+
 // 32 rows of a warp to global memory: lane l holds N 16-byte pieces of row l, and
 // dst(row) is where row's pieces go (nullptr: nowhere).  The pieces cross `stage`
 // (32 * 16 * LPR bytes of the warp's own, LPR >= N a power of two of at most 8)

@@ -483,7 +483,7 @@ GDN_API unsigned long long gdn_launch_count(void);
  * backward's pre, chain and gradient passes, 11 / 12 / 13 the norm and rotary
  * pass, its gradients and their reduction, 14 / 15 the cross attention and the
  * join of its splits, 16 / 17 / 18 its gradients, the join of their shares
- * and the row statistics; names from gdn_kernel_name.  Not thread-safe against concurrent calls on other
+ * and the row statistics, 19 the cross attention of a few rows; names from gdn_kernel_name.  Not thread-safe against concurrent calls on other
  * threads; meant for benchmarks.
  */
 GDN_API gdn_status gdn_profile_begin(int max_launches);

@@ -139,6 +139,13 @@ CASES = [
     (2, 257, 64, 1, 5, 64, "holes"),
     (1, 129, 20000, 1, 1, 32, "holes"),
     (1, 300, 4000, 1, 1, 128, "none"),
+    # at most 16 rows of a key head
+    (2, 16, 50, 1, 1, 48, "holes"),
+    (1, 1, 5000, 1, 16, 80, "none"),
+    (3, 2, 333, 2, 7, 64, "tail"),
+    (2, 5, 100, 1, 3, 32, "none"),
+    (1, 4, 17, 2, 4, 96, "holes"),
+    (9, 1, 700, 40, 1, 112, "tail"),
 ]
 
 
