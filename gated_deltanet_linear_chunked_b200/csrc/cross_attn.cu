@@ -195,8 +195,8 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     __syncthreads();
   }
   // two tiles hold all 512 columns, an allocation that starts at the first
-  const uint32_t tm = NQ == 2 ? 0u : aux.tmem;
-  const int n = aux.count;
+  const uint32_t tm = NQ == 2 ? 0u : __reduce_max_sync(~0u, aux.tmem);  // (a reduction's result is uniform)
+  const int n = __reduce_max_sync(~0u, aux.count);
   const bool masked = P.mask != nullptr;
   auto fail = [&]() {
     *abort_flag = 1;

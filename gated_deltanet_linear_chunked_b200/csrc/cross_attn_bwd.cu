@@ -10,9 +10,9 @@
 // across CTAs, by atomics, whose order changes the result, or through partial
 // sums of full size; two passes take seven products and every sum stays in a
 // CTA's TMEM, in a fixed order.
-//   gdn_cross_stat_kernel  (lse log2 e, delta) of every packed row; +inf for the
-//                  rows that are none (past the tokens, or with no key), for
-//                  which 2^(s - inf) = 0.
+//   gdn_cross_stat_kernel  -lse log2 e and -delta of every packed row; -inf and 0
+//                  for the rows that are none (past the tokens, or with no key),
+//                  for which 2^(s - inf) = 0.
 //   gdn_cross_bwd_kernel   dQ: a CTA per query tile walks the key tiles.
 //                  dK, dV: a CTA per key tile and share of the query tiles; the
 //                  products are transposed, S^T = K Q^T and dP^T = V dO^T, so that
@@ -44,7 +44,6 @@ constexpr int kProducerWarp = kSoftmaxWarps;
 constexpr int kMmaWarp = kProducerWarp + 1;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr uint32_t kBlock = kRows * 128;
-constexpr int kStages = 2;
 constexpr int kStatThreads = 256;
 constexpr long long kDrainPolls = 1LL << 40;
 
@@ -59,7 +58,7 @@ struct BwdParams {
   const int* list;              // ... and [B][ntiles + 1]: the tiles with any, their number last
   float scale, scale_log2;
   __nv_bfloat16 *dq, *dk, *dv;
-  const float2* stat;           // [B * Hk][qtiles][128]
+  const float* stat;            // [B * Hk][qtiles][2][128]: -lse log2 e, -delta
   float* part;                  // nsplit > 1: [nsplit][2 (dk, dv)][B * Hk][ntiles][128][D]
   long long part_rows;          // B * Hk * ntiles * 128
   long long limit;
@@ -108,7 +107,7 @@ __device__ __forceinline__ uint32_t word_of(const uint4& w, int c) {
 constexpr int kStatRows = 4;
 constexpr int kStatBlockRows = kStatThreads / 16 * kStatRows;
 __global__ void __launch_bounds__(kStatThreads)
-gdn_cross_stat_kernel(const __nv_bfloat16* out, const __nv_bfloat16* d_out, const float* lse, float2* stat,
+gdn_cross_stat_kernel(const __nv_bfloat16* out, const __nv_bfloat16* d_out, const float* lse, float* stat,
                       long long rows, unsigned row_blocks, const uint8_t* mask, long long mask_bs,
                       const __grid_constant__ BwdParams P) {
   pdl_trigger();
@@ -150,8 +149,19 @@ gdn_cross_stat_kernel(const __nv_bfloat16* out, const __nv_bfloat16* d_out, cons
     for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(~0u, d, o);
     const long long row = first + i * (kStatThreads / 16);
     const bool on = lg[i] > -INFINITY;
-    if (l == 0 && row < rows) stat[row] = on ? make_float2(lg[i] * 1.4426950408889634f, d) : make_float2(INFINITY, 0.f);
+    if (l == 0 && row < rows) {
+      float* to = stat + row / kRows * (2 * kRows) + row % kRows;
+      to[0] = on ? lg[i] * -1.4426950408889634f : -INFINITY;
+      to[kRows] = on ? -d : 0.f;
+    }
   }
+}
+
+// 2^x of a pair, x <= 0 up to rounding.
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t x, int) {
+  float a, e;
+  f2_unpack(x, a, e);
+  return f2_pack(ex2_approx(a), ex2_approx(e));
 }
 
 // Columns [c0, c0 + n) (n 16 or 32) of a warp's 32 rows out of TMEM, times `mul`
@@ -190,8 +200,10 @@ __device__ __forceinline__ void put_columns(uint32_t src, int n, bool any, float
 // TMEM: S of even and odd key tiles [0, 128), [128, 256) (dS over them), dP
 // [256, 384), dQ [384, 384 + D).  With two S the product for the next tile runs
 // under this one's exponentials.
+// K tiles have three places, V tiles two: K is needed until its dQ, V only until dP.
+constexpr int kKs = 3, kVs = 2;
 struct DqAux {
-  uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages];
+  uint64_t q_full, k_full[kKs], k_empty[kKs], v_full[kVs], v_empty[kVs];
   uint64_t s_full[2], dp_full, dp_free, ds_full[2], dq_full, drain;
   uint32_t tmem;
   int abort;
@@ -199,8 +211,8 @@ struct DqAux {
 template <int NB>
 struct DqLayout {
   static constexpr uint32_t tile = NB * kBlock;
-  static constexpr uint32_t q = 0, g = tile, k = 2 * tile, v = k + kStages * tile;
-  static constexpr uint32_t aux = v + kStages * tile;
+  static constexpr uint32_t q = 0, g = tile, k = 2 * tile, v = k + kKs * tile;
+  static constexpr uint32_t aux = v + kVs * tile;
   static constexpr uint32_t total = aux + (uint32_t)sizeof(DqAux);
 };
 
@@ -217,10 +229,13 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
   volatile int* abort_flag = &aux.abort;
   if (tid == 0) {
     mbar_init(&aux.q_full, 1);
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kKs; ++s) {
       mbar_init(&aux.k_full[s], 1);
       mbar_init(&aux.k_empty[s], 1);
+    }
+    for (int s = 0; s < kVs; ++s) {
       mbar_init(&aux.v_full[s], 1);
+      mbar_init(&aux.v_empty[s], 1);
     }
     mbar_init(&aux.s_full[0], 1);
     mbar_init(&aux.s_full[1], 1);
@@ -243,7 +258,8 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
   constexpr uint32_t tm = 0;  // all 512 columns: the allocation starts at the first
   constexpr uint32_t tDP = tm + 256, tDQ = tm + 384;
   const int* list = P.bits ? P.list + (long long)b * (P.ntiles + 1) : nullptr;
-  const int n = list ? list[P.ntiles] : P.ntiles;
+  // (a reduction's result is uniform: the issuing warp's loop stays in uniform registers)
+  const int n = __reduce_max_sync(~0u, list ? list[P.ntiles] : P.ntiles);
   auto fail = [&]() {
     *abort_flag = 1;
     atomicOr(P.err, kErrTimeout);
@@ -260,28 +276,25 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
       int j = 0;
       for (; j < n; ++j) {
         if (*abort_flag) break;
-        const int s = j % kStages, t = list ? list[j] : j;
-        const uint32_t ph = (j / kStages - 1) & 1;
-        if (j >= kStages && !mbar_wait(&aux.k_empty[s], ph, P.limit)) {
+        const int ks = j % kKs, vs = j % kVs, t = list ? list[j] : j;
+        if ((j >= kKs && !mbar_wait(&aux.k_empty[ks], (j / kKs - 1) & 1, P.limit)) ||
+            (j >= kVs && !mbar_wait(&aux.v_empty[vs], (j / kVs - 1) & 1, P.limit))) {
           fail();
           break;
         }
-        mbar_arrive_expect_tx(&aux.k_full[s], L::tile);
+        mbar_arrive_expect_tx(&aux.k_full[ks], L::tile);
         for (int c = 0; c < NB; ++c)
-          tma_load_5d(smem + L::k + s * L::tile + c * kBlock, &tm_k, &aux.k_full[s], c * 64, 0, t * kRows, hk,
+          tma_load_5d(smem + L::k + ks * L::tile + c * kBlock, &tm_k, &aux.k_full[ks], c * 64, 0, t * kRows, hk,
                       b * P.kb);
-        // (dP of tile j - 2, V's reader, came before its dQ, K's last one)
-        mbar_arrive_expect_tx(&aux.v_full[s], L::tile);
+        mbar_arrive_expect_tx(&aux.v_full[vs], L::tile);
         for (int c = 0; c < NB; ++c)
-          tma_load_5d(smem + L::v + s * L::tile + c * kBlock, &tm_v, &aux.v_full[s], c * 64, 0, t * kRows, hk,
+          tma_load_5d(smem + L::v + vs * L::tile + c * kBlock, &tm_v, &aux.v_full[vs], c * 64, 0, t * kRows, hk,
                       b * P.vb);
       }
       // every load has landed before shared memory goes
       mbar_wait(&aux.q_full, 0, kDrainPolls);
-      for (int i = max(0, j - kStages); i < j; ++i) {
-        mbar_wait(&aux.k_full[i % kStages], (i / kStages) & 1, kDrainPolls);
-        mbar_wait(&aux.v_full[i % kStages], (i / kStages) & 1, kDrainPolls);
-      }
+      for (int i = max(0, j - kKs); i < j; ++i) mbar_wait(&aux.k_full[i % kKs], (i / kKs) & 1, kDrainPolls);
+      for (int i = max(0, j - kVs); i < j; ++i) mbar_wait(&aux.v_full[i % kVs], (i / kVs) & 1, kDrainPolls);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
@@ -299,20 +312,21 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
       }
     };
     auto issue_s = [&](int j) {
-      const int s = j % kStages;
-      if (!all(&aux.k_full[s], (j / kStages) & 1)) return false;
+      const int s = j % kKs;
+      if (!all(&aux.k_full[s], (j / kKs) & 1)) return false;
       tc_fence_after_sync();
       product(tm + (j & 1) * 128, dq, dk + (s * L::tile >> 4));
       mma_commit_elect(&aux.s_full[j & 1]);
       return true;
     };
     auto issue_dp = [&](int j) {
-      const int s = j % kStages;
-      if (!all(&aux.v_full[s], (j / kStages) & 1)) return false;
+      const int s = j % kVs;
+      if (!all(&aux.v_full[s], (j / kVs) & 1)) return false;
       if (j > 0 && !all(&aux.dp_free, (j - 1) & 1)) return false;
       tc_fence_after_sync();
       product(tDP, dg, dv + (s * L::tile >> 4));
       mma_commit_elect(&aux.dp_full);
+      mma_commit_elect(&aux.v_empty[s]);
       return true;
     };
     bool ok = true;
@@ -324,7 +338,7 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
       tc_fence_after_sync();
       // dQ += dS K: dS in TMEM (8 columns per 16 keys, 32 keys over their own
       // scores' columns), K MN-major
-      const int s = j % kStages;
+      const int s = j % kKs;
 #pragma unroll
       for (int ks = 0; ks < kRows / 16; ++ks)
         mma_bf16_ts_elect(tDQ, tm + (j & 1) * 128 + (ks >> 1) * 32 + (ks & 1) * 8,
@@ -339,7 +353,9 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
   } else {
     const int r = (warp & 3) * 32 + lane, cg = warp >> 2;  // row; columns [32 cg, 32 cg + 32)
     const uint32_t trow = tm + ((uint32_t)((warp & 3) * 32) << 16);
-    const float2 st = P.stat[((long long)bh * P.qtiles + qt) * kRows + r];
+    const float* st = P.stat + ((long long)bh * P.qtiles + qt) * (2 * kRows) + r;
+    const uint64_t c2 = f2_pack(P.scale_log2, P.scale_log2);
+    const uint64_t nl = f2_pack(st[0], st[0]), nd = f2_pack(st[kRows], st[kRows]);
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const uint4 keys = seen_keys(P, b, list ? list[j] : j);
@@ -350,36 +366,39 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
       tc_fence_after_sync();
       const uint32_t ts = trow + (j & 1) * 128 + kCols * cg;
       const uint32_t seen = word_of(keys, cg);
-      float p[kCols], dp[kCols];
-      tmem_ld32(ts, p);
+      float x[kCols];
+      uint64_t p[kCols / 2];
+      tmem_ld32(ts, x);
       tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) p[i] = ex2_approx(fmaf(p[i], P.scale_log2, -st.x));
+      for (int i = 0; i < kCols / 2; ++i) p[i] = exp2_pair(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), c2, nl), i);
       if (!__all_sync(~0u, mbar_wait(&aux.dp_full, j & 1, P.limit))) {
         ok = false;
         break;
       }
       tc_fence_after_sync();
-      tmem_ld32(trow + tDP + kCols * cg, dp);
+      tmem_ld32(trow + tDP + kCols * cg, x);
       tmem_wait_ld();
       tc_fence_before_sync();
       mbar_arrive(&aux.dp_free);
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) p[i] *= dp[i] - st.y;
-      if (seen != ~0u) {
-#pragma unroll
-        for (int i = 0; i < kCols; ++i)
-          if (!(seen >> i & 1)) p[i] = 0.f;
-      }
       uint32_t pk[kCols / 2];
 #pragma unroll
-      for (int i = 0; i < kCols / 2; ++i) pk[i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
+      for (int i = 0; i < kCols / 2; ++i) {
+        float a, e;
+        f2_unpack(f2_mul(p[i], f2_add(f2_pack(x[2 * i], x[2 * i + 1]), nd)), a, e);
+        pk[i] = pack_bf16x2(a, e);
+      }
+      if (seen != ~0u) {  // dS of masked keys is 0 whatever their scores and values are
+#pragma unroll
+        for (int i = 0; i < kCols / 2; ++i)
+          pk[i] &= (seen >> (2 * i) & 1 ? 0xFFFFu : 0u) | (seen >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
+      }
       tmem_st16u(ts, pk);
       if (P.bits && (keys.x & keys.y & keys.z & keys.w) != ~0u) {
         // clear the masked rows of K (its product with Q is done): 0 * NaN would reach dQ
         const int key = tid >> 2, part = tid & 3;  // four threads a row
         if (!(word_of(keys, key >> 5) >> (key & 31) & 1)) {
-          uint8_t* row = smem + L::k + (j % kStages) * L::tile + key * 128 + part * 32;
+          uint8_t* row = smem + L::k + (j % kKs) * L::tile + key * 128 + part * 32;
 #pragma unroll
           for (int c = 0; c < NB; ++c) {
             *reinterpret_cast<uint4*>(row + c * kBlock) = make_uint4(0, 0, 0, 0);
@@ -424,18 +443,21 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
 // [256, 256 + D), dK [384, 384 + D).  P^T is handed on before dP^T is looked at:
 // dV += P^T dO and the next S^T run under the second half of the softmax, and
 // dK += dS^T Q and the next dP^T under the first half of the next.
+// Q and dO tiles take turns through a ring of five places, Q_i the item 2 i and dO_i
+// the item 2 i + 1: Q_i+2 is on its way one step early.
+constexpr int kRing = 5;
 struct DkvAux {
-  uint64_t kv_full, q_full[kStages], q_empty[kStages];
+  uint64_t kv_full, full[kRing], empty[kRing];
   uint64_t s_full, p_full, dp_full, ds_full, out_full, drain;
   uint32_t tmem;
   int abort;
-  __align__(16) float2 stat[kStages][kRows];
+  __align__(16) float nl[2][kRows], nd[2][kRows];  // -lse log2 e and -delta of two query tiles
 };
 template <int NB>
 struct DkvLayout {
   static constexpr uint32_t tile = NB * kBlock;
-  static constexpr uint32_t k = 0, v = tile, q = 2 * tile, g = q + kStages * tile;
-  static constexpr uint32_t aux = g + kStages * tile;
+  static constexpr uint32_t k = 0, v = tile, ring = 2 * tile;
+  static constexpr uint32_t aux = ring + kRing * tile;
   static constexpr uint32_t total = aux + (uint32_t)sizeof(DkvAux);
 };
 
@@ -455,9 +477,9 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
   volatile int* abort_flag = &aux.abort;
   if (tid == 0) {
     mbar_init(&aux.kv_full, 1);
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&aux.q_full[s], 1);
-      mbar_init(&aux.q_empty[s], 1);
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(&aux.full[s], 1);
+      mbar_init(&aux.empty[s], 1);
     }
     mbar_init(&aux.s_full, 1);
     mbar_init(&aux.p_full, kSoftmaxThreads);
@@ -476,8 +498,8 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
   // rows of Q and dO past the packed ones are never loaded, and a product runs
   // over them: they have to be numbers
   for (int i = P.tokens * P.G * 8 + tid; i < kRows * 8; i += kThreads)
-    for (int c = 0; c < 2 * kStages * NB; ++c)
-      *reinterpret_cast<uint4*>(smem + L::q + c * kBlock + i * 16) = make_uint4(0, 0, 0, 0);
+    for (int c = 0; c < kRing * NB; ++c)
+      *reinterpret_cast<uint4*>(smem + L::ring + c * kBlock + i * 16) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   tc_fence_before_sync();
   __syncthreads();
@@ -485,7 +507,7 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
   constexpr uint32_t tm = 0;
   constexpr uint32_t tDP = tm + 128, tDV = tm + 256, tDK = tm + 384;
   const bool any = (keys.x | keys.y | keys.z | keys.w) != 0;
-  const int n = any ? i1 - i0 : 0;
+  const int n = __reduce_max_sync(~0u, any ? i1 - i0 : 0);  // uniform, as for dQ
   auto fail = [&]() {
     *abort_flag = 1;
     atomicOr(P.err, kErrTimeout);
@@ -499,34 +521,30 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
         tma_load_5d(smem + L::v + c * kBlock, &tm_v, &aux.kv_full, c * 64, 0, kt * kRows, hk, b * P.vb);
       }
       const uint32_t bytes = (uint32_t)P.tokens * P.G * 128 * NB;
-      int i = 0;
-      for (; i < n; ++i) {
+      int x = 0;
+      for (; x < 2 * n; ++x) {
         if (*abort_flag) break;
-        const int s = i % kStages, qt = i0 + i;
-        if (i >= kStages && !mbar_wait(&aux.q_empty[s], (i / kStages - 1) & 1, P.limit)) {
+        const int s = x % kRing, qt = i0 + x / 2;
+        if (x >= kRing && !mbar_wait(&aux.empty[s], (x / kRing - 1) & 1, P.limit)) {
           fail();
           break;
         }
-        uint64_t* bar = &aux.q_full[s];
-        mbar_arrive_expect_tx(bar, 2 * bytes + kRows * (uint32_t)sizeof(float2));
+        mbar_arrive_expect_tx(&aux.full[s], bytes);
         for (int c = 0; c < NB; ++c)
-          tma_load_5d(smem + L::q + s * L::tile + c * kBlock, &tm_q, bar, c * 64, 0, qt * P.tokens, hk, b * P.qb);
-        for (int c = 0; c < NB; ++c)
-          tma_load_5d(smem + L::g + s * L::tile + c * kBlock, &tm_do, bar, c * 64, 0, qt * P.tokens, hk, b);
-        bulk_load(aux.stat[s], P.stat + ((long long)bh * P.qtiles + qt) * kRows, kRows * sizeof(float2), bar);
+          tma_load_5d(smem + L::ring + s * L::tile + c * kBlock, x & 1 ? &tm_do : &tm_q, &aux.full[s], c * 64, 0,
+                      qt * P.tokens, hk, x & 1 ? b : b * P.qb);
       }
       mbar_wait(&aux.kv_full, 0, kDrainPolls);
-      for (int x = max(0, i - kStages); x < i; ++x)
-        mbar_wait(&aux.q_full[x % kStages], (x / kStages) & 1, kDrainPolls);
+      for (int y = max(0, x - kRing); y < x; ++y) mbar_wait(&aux.full[y % kRing], (y / kRing) & 1, kDrainPolls);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
     if (n > 0) {
       const uint32_t idS = idesc_bf16(kRows, kRows, 0, 0), idO = idesc_bf16(kRows, D, 0, 1);
       const uint64_t dk = sdesc_sw128(smem_u32(smem + L::k), 16), dv = sdesc_sw128(smem_u32(smem + L::v), 16);
-      const uint64_t dq = sdesc_sw128(smem_u32(smem + L::q), 16), dg = sdesc_sw128(smem_u32(smem + L::g), 16);
-      const uint64_t dqn = sdesc_sw128(smem_u32(smem + L::q), kBlock);
-      const uint64_t dgn = sdesc_sw128(smem_u32(smem + L::g), kBlock);
+      // ring item x as a right operand: K-major, and MN-major
+      auto rowwise = [&](int x) { return sdesc_sw128(smem_u32(smem + L::ring + x % kRing * L::tile), 16); };
+      auto colwise = [&](int x) { return sdesc_sw128(smem_u32(smem + L::ring + x % kRing * L::tile), kBlock); };
       auto all = [&](uint64_t* bar, uint32_t ph) { return __all_sync(~0u, mbar_wait(bar, ph, P.limit)); };
       auto product = [&](uint32_t d, uint64_t a, uint64_t bb) {  // over the features, both K-major
 #pragma unroll
@@ -540,34 +558,43 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
         for (int ks = 0; ks < kRows / 16; ++ks)
           mma_bf16_ts_elect(d, a + (ks >> 1) * 32 + (ks & 1) * 8, bb + ks * (2048 >> 4), idO, more || ks > 0);
       };
-      bool ok = all(&aux.kv_full, 0) && all(&aux.q_full[0], 0);
+      auto landed = [&](int x) { return all(&aux.full[x % kRing], (x / kRing) & 1); };
+      bool ok = all(&aux.kv_full, 0) && landed(0);
       if (ok) {
         tc_fence_after_sync();
-        product(tm, dk, dq);
+        product(tm, dk, rowwise(0));
         mma_commit_elect(&aux.s_full);
-        product(tDP, dv, dg);
+        ok = landed(1);
+      }
+      if (ok) {
+        tc_fence_after_sync();
+        product(tDP, dv, rowwise(1));
         mma_commit_elect(&aux.dp_full);
       }
       for (int i = 0; ok && i < n; ++i) {
-        const uint32_t at = (i % kStages) * (L::tile >> 4), nx = ((i + 1) % kStages) * (L::tile >> 4);
+        const int q = 2 * i, g = 2 * i + 1;
         ok = all(&aux.p_full, i & 1);
         if (!ok) break;
         tc_fence_after_sync();
-        add(tDV, tm, dgn + at, i > 0);
+        add(tDV, tm, colwise(g), i > 0);
+        mma_commit_elect(&aux.empty[g % kRing]);
         if (i + 1 < n) {
-          ok = all(&aux.q_full[(i + 1) % kStages], ((i + 1) / kStages) & 1);
+          ok = landed(q + 2);
           if (!ok) break;
           tc_fence_after_sync();
-          product(tm, dk, dq + nx);
+          product(tm, dk, rowwise(q + 2));
           mma_commit_elect(&aux.s_full);
         }
         ok = all(&aux.ds_full, i & 1);
         if (!ok) break;
         tc_fence_after_sync();
-        add(tDK, tDP, dqn + at, i > 0);
-        mma_commit_elect(&aux.q_empty[i % kStages]);
+        add(tDK, tDP, colwise(q), i > 0);
+        mma_commit_elect(&aux.empty[q % kRing]);
         if (i + 1 < n) {
-          product(tDP, dv, dg + nx);
+          ok = landed(g + 2);
+          if (!ok) break;
+          tc_fence_after_sync();
+          product(tDP, dv, rowwise(g + 2));
           mma_commit_elect(&aux.dp_full);
         }
       }
@@ -580,30 +607,54 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
   } else {
     const int cg = warp >> 2;  // a key per lane; queries [32 cg, 32 cg + 32)
     const uint32_t trow = tm + ((uint32_t)((warp & 3) * 32) << 16);
-    const bool seen = word_of(keys, warp & 3) >> lane & 1;
+    const uint32_t seen = word_of(keys, warp & 3);
+    const uint32_t keep = seen >> lane & 1 ? ~0u : 0u;  // both halves of a packed pair
+    const uint64_t c2 = f2_pack(P.scale_log2, P.scale_log2);
+    // Warp 0 brings the next tile's -lse log2 e, warp 1 its -delta, each written while
+    // no one reads that place: nl under this tile's first half (every thread is past
+    // the last tile's), nd under its second.
+    const float* stat = P.stat + ((long long)bh * P.qtiles + i0) * (2 * kRows) + lane * 4;
+    if (n > 0) {
+      if (warp < 2)
+        *reinterpret_cast<float4*>((warp ? aux.nd : aux.nl)[0] + lane * 4) =
+            *reinterpret_cast<const float4*>(stat + warp * kRows);
+      named_barrier(1, kSoftmaxThreads);
+    }
     bool ok = true;
     for (int i = 0; i < n; ++i) {
+      float4 coming = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (warp < 2 && i + 1 < n)
+        coming = *reinterpret_cast<const float4*>(stat + (long long)(i + 1) * (2 * kRows) + warp * kRows);
       if (!__all_sync(~0u, *abort_flag == 0 && mbar_wait(&aux.s_full, i & 1, P.limit))) {
         ok = false;
         break;
       }
-      // (the product that filled S^T waited for this stage's rows and stats)
+      if (i > 0) mbar_wait(&aux.p_full, (i - 1) & 1, 2);  // complete: acquires what warp 0 wrote
       tc_fence_after_sync();
-      const int s = i % kStages;
-      const float4* st = reinterpret_cast<const float4*>(aux.stat[s] + kCols * cg);
-      float p[kCols], dp[kCols];
+      float x[kCols];
+      uint64_t p[kCols / 2];
       uint32_t pk[kCols / 2];
-      tmem_ld32(trow + kCols * cg, p);
+      tmem_ld32(trow + kCols * cg, x);
       tmem_wait_ld();
-      mbar_wait(&aux.q_full[s], (i / kStages) & 1, 2);  // the stats' bytes, landed already
+      const uint4* nl = reinterpret_cast<const uint4*>(aux.nl[i & 1] + kCols * cg);
 #pragma unroll
-      for (int c = 0; c < kCols / 2; ++c) {
-        const float4 x = st[c];
-        p[2 * c] = seen ? ex2_approx(fmaf(p[2 * c], P.scale_log2, -x.x)) : 0.f;
-        p[2 * c + 1] = seen ? ex2_approx(fmaf(p[2 * c + 1], P.scale_log2, -x.z)) : 0.f;
-        pk[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+      for (int c = 0; c < kCols / 4; ++c) {
+        const uint4 y = nl[c];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint64_t neg = f2_pack(__uint_as_float(h ? y.z : y.x), __uint_as_float(h ? y.w : y.y));
+          float a, e;
+          p[2 * c + h] = exp2_pair(f2_fma(f2_pack(x[4 * c + 2 * h], x[4 * c + 2 * h + 1]), c2, neg), 2 * c + h);
+          f2_unpack(p[2 * c + h], a, e);
+          pk[2 * c + h] = pack_bf16x2(a, e);
+        }
+      }
+      if (seen != ~0u) {  // a masked key's lane: 0 whatever its scores are
+#pragma unroll
+        for (int c = 0; c < kCols / 2; ++c) pk[c] &= keep;
       }
       tmem_st16u(trow + kCols * cg, pk);
+      if (warp == 0) *reinterpret_cast<float4*>(aux.nl[(i + 1) & 1] + lane * 4) = coming;
       tmem_wait_st();
       tc_fence_before_sync();
       mbar_arrive(&aux.p_full);
@@ -611,17 +662,28 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
         ok = false;
         break;
       }
+      if (i > 0) mbar_wait(&aux.ds_full, (i - 1) & 1, 2);  // ... and warp 1
       tc_fence_after_sync();
-      tmem_ld32(trow + tDP + kCols * cg, dp);
+      tmem_ld32(trow + tDP + kCols * cg, x);
       tmem_wait_ld();
+      const uint4* nd = reinterpret_cast<const uint4*>(aux.nd[i & 1] + kCols * cg);
 #pragma unroll
-      for (int c = 0; c < kCols / 2; ++c) {
-        const float4 x = st[c];
-        const float a = seen ? p[2 * c] * (dp[2 * c] - x.y) : 0.f;
-        const float e = seen ? p[2 * c + 1] * (dp[2 * c + 1] - x.w) : 0.f;
-        pk[c] = pack_bf16x2(a, e);
+      for (int c = 0; c < kCols / 4; ++c) {
+        const uint4 y = nd[c];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint64_t neg = f2_pack(__uint_as_float(h ? y.z : y.x), __uint_as_float(h ? y.w : y.y));
+          float a, e;
+          f2_unpack(f2_mul(p[2 * c + h], f2_add(f2_pack(x[4 * c + 2 * h], x[4 * c + 2 * h + 1]), neg)), a, e);
+          pk[2 * c + h] = pack_bf16x2(a, e);
+        }
+      }
+      if (seen != ~0u) {
+#pragma unroll
+        for (int c = 0; c < kCols / 2; ++c) pk[c] &= keep;
       }
       tmem_st16u(trow + tDP + kCols * cg, pk);
+      if (warp == 1) *reinterpret_cast<float4*>(aux.nd[(i + 1) & 1] + lane * 4) = coming;
       tmem_wait_st();
       tc_fence_before_sync();
       mbar_arrive(&aux.ds_full);
@@ -741,7 +803,7 @@ struct BwdScratch {
 BwdScratch bwd_scratch(const CrossCall& c, const BwdParams& P) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   BwdScratch s;
-  s.bits = up((size_t)c.B * c.Hk * P.qtiles * kRows * sizeof(float2));
+  s.bits = up((size_t)c.B * c.Hk * P.qtiles * 2 * kRows * sizeof(float));
   s.list = s.bits + (c.mask ? up((size_t)c.B * P.ntiles * 4 * sizeof(uint32_t)) : 0);
   s.part = s.list + (c.mask ? up((size_t)c.B * (P.ntiles + 1) * sizeof(int)) : 0);
   s.total = s.part + (P.nsplit > 1 ? (size_t)2 * P.nsplit * P.part_rows * c.D * sizeof(float) : 0);
@@ -782,7 +844,7 @@ cudaError_t launch_cross_backward(const CrossCall& c, void* ws) {
   P.dv = static_cast<__nv_bfloat16*>(c.dv);
   P.scale = c.scale;
   P.scale_log2 = c.scale * 1.4426950408889634f;
-  P.stat = static_cast<const float2*>(ws);
+  P.stat = static_cast<const float*>(ws);
   P.part = reinterpret_cast<float*>(base + at.part);
   P.limit = c.limit;
   P.err = c.err;
@@ -805,7 +867,7 @@ cudaError_t launch_cross_backward(const CrossCall& c, void* ws) {
     const unsigned blocks = (unsigned)((rows + kStatBlockRows - 1) / kStatBlockRows);
     gdn_cross_stat_kernel<<<blocks + (c.mask ? c.B : 0), kStatThreads, 0, c.stream>>>(
         static_cast<const __nv_bfloat16*>(c.out), static_cast<const __nv_bfloat16*>(c.d_out), c.lse,
-        static_cast<float2*>(ws), rows, blocks, c.mask, c.mask_bs, P);
+        static_cast<float*>(ws), rows, blocks, c.mask, c.mask_bs, P);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
