@@ -146,8 +146,8 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     for (int g = 0; g < NQ; ++g) {
       mbar_init(&aux.s_full[g], 1);
-      mbar_init(&aux.p_full[g][0], kRows);
-      mbar_init(&aux.p_full[g][1], kRows);
+      mbar_init(&aux.p_full[g][0], 4);  // warps of a half
+      mbar_init(&aux.p_full[g][1], 4);
       mbar_init(&aux.o_full[g], 1);
     }
     mbar_init(&aux.drain, 1);
@@ -405,7 +405,7 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(&aux.p_full[g][half]);
+      mbar_arrive_warp(&aux.p_full[g][half], lane);
       const uint64_t sa = f2_add(sum2[0], sum2[1]);
       float rs0, rs1;
       f2_unpack(sa, rs0, rs1);

@@ -157,8 +157,12 @@ gdn_cross_stat_kernel(const __nv_bfloat16* out, const __nv_bfloat16* d_out, cons
   }
 }
 
-// 2^x of a pair, x <= 0 up to rounding.
-__device__ __forceinline__ uint64_t exp2_pair(uint64_t x, int) {
+// 2^x of pair i of a thread's 16, x <= 0 up to rounding: one in four on the FMA pipe (to
+// 7.5e-5, far under the rounding of P and dS to bf16; 2^-125 for -inf, of rows
+// whose Q, dO or result are nothing), the others on the special-function unit, which
+// alone would take 1024 cycles for a tile, half of its products' time.
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t x, int i) {
+  if ((i & 3) == 3) return exp2_poly2(x);
   float a, e;
   f2_unpack(x, a, e);
   return f2_pack(ex2_approx(a), ex2_approx(e));
@@ -240,9 +244,9 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
     mbar_init(&aux.s_full[0], 1);
     mbar_init(&aux.s_full[1], 1);
     mbar_init(&aux.dp_full, 1);
-    mbar_init(&aux.dp_free, kSoftmaxThreads);
-    mbar_init(&aux.ds_full[0], kSoftmaxThreads);
-    mbar_init(&aux.ds_full[1], kSoftmaxThreads);
+    mbar_init(&aux.dp_free, kSoftmaxWarps);
+    mbar_init(&aux.ds_full[0], kSoftmaxWarps);
+    mbar_init(&aux.ds_full[1], kSoftmaxWarps);
     mbar_init(&aux.dq_full, 1);
     mbar_init(&aux.drain, 1);
     aux.abort = 0;
@@ -380,7 +384,7 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
       tmem_ld32(trow + tDP + kCols * cg, x);
       tmem_wait_ld();
       tc_fence_before_sync();
-      mbar_arrive(&aux.dp_free);
+      mbar_arrive_warp(&aux.dp_free, lane);
       uint32_t pk[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) {
@@ -409,7 +413,7 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
       }
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(&aux.ds_full[j & 1]);
+      mbar_arrive_warp(&aux.ds_full[j & 1], lane);
     }
     if (ok && !__all_sync(~0u, mbar_wait(&aux.dq_full, 0, P.limit))) ok = false;
     if (!ok && lane == 0) fail();
@@ -482,9 +486,9 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
       mbar_init(&aux.empty[s], 1);
     }
     mbar_init(&aux.s_full, 1);
-    mbar_init(&aux.p_full, kSoftmaxThreads);
+    mbar_init(&aux.p_full, kSoftmaxWarps);
     mbar_init(&aux.dp_full, 1);
-    mbar_init(&aux.ds_full, kSoftmaxThreads);
+    mbar_init(&aux.ds_full, kSoftmaxWarps);
     mbar_init(&aux.out_full, 1);
     mbar_init(&aux.drain, 1);
     aux.abort = 0;
@@ -657,7 +661,7 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
       if (warp == 0) *reinterpret_cast<float4*>(aux.nl[(i + 1) & 1] + lane * 4) = coming;
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(&aux.p_full);
+      mbar_arrive_warp(&aux.p_full, lane);
       if (!__all_sync(~0u, mbar_wait(&aux.dp_full, i & 1, P.limit))) {
         ok = false;
         break;
@@ -686,7 +690,7 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
       if (warp == 1) *reinterpret_cast<float4*>(aux.nd[(i + 1) & 1] + lane * 4) = coming;
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(&aux.ds_full);
+      mbar_arrive_warp(&aux.ds_full, lane);
     }
     if (ok && n > 0 && !__all_sync(~0u, mbar_wait(&aux.out_full, 0, P.limit))) ok = false;
     if (!ok && lane == 0) fail();
