@@ -1,0 +1,175 @@
+"""The softmax block's operators in a row, as a block calls them: the projection's
+queries and keys normalised and rotated (the keys straight into their cache slot),
+attention over the sink and the window, then the normalised queries over the
+encoder's normalised states, chunk after chunk; a training step back through the
+norm and the attention to the encoder; and both inside a CUDA graph.
+
+Every stage is held to its own oracle on the values it was given (what the stage
+before stored), with that stage's own bar: the norm and rotation half a step of bf16
+(2^-8) of each value and 2^-19 of its pair, the attention over the window 2e-2 of
+the head's largest value, the one over the encoder 2^-7 of the sum of p |v| (P and
+the result rounded to bf16) and 1e-3 for the scores' fp32 sums.
+"""
+import numpy as np
+import pytest
+import torch
+
+import gated_deltanet_linear_chunked_b200 as gdn
+from gated_deltanet_linear_chunked_b200 import _lib
+from oracle import cross_attn as ca
+from oracle import norm_rope as nr
+from oracle import sink_window_attn as swa
+
+from gdn_testlib import TOL, max_rel_per_head
+
+pytestmark = pytest.mark.gpu
+
+H = 2.0 ** -8
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+class Block:
+    def __init__(self, seed, Tc=330, heads=4, D=112, S=77, n_sink=1, window=2):
+        self.Tc, self.heads, self.D, self.n_sink, self.window = Tc, heads, D, n_sink, window
+        self.gen = torch.Generator(device="cuda").manual_seed(seed)
+        self.wq, self.wk, self.wx, self.wy = (1 + 0.2 * self.normal(D) for _ in range(4))
+        self.sections = (D // 2 - 2 * (D // 6), D // 6, D // 6)
+        self.freq, self.amp = gdn.rope_frequencies(D, sections=self.sections)
+        self.kc, self.vc = gdn.sink_window_cache(1, Tc, heads, D, n_sink, window)
+        kv = self.normal(1, S, 2, heads, D).bfloat16()     # the encoder side's projection
+        self.k_enc, self.v_enc = kv[:, :, 0], kv[:, :, 1]
+        self.mask = torch.arange(S, device="cuda")[None] < S - 13
+        self.kn_enc, _ = gdn.qk_norm_rope(self.k_enc, None, self.wy)
+
+    def normal(self, *shape):
+        return torch.randn(shape, generator=self.gen, device="cuda")
+
+    def positions(self, c):
+        t = torch.arange(self.Tc, device="cuda")
+        return torch.stack([3 * c + torch.div(t, 110, rounding_mode="floor"),
+                            torch.div(t, 11, rounding_mode="floor") % 10, t % 11], -1)
+
+    def turn(self):
+        return dict(sections=self.sections, amplitude=self.amp)
+
+    def chunk(self, c, qkv):
+        """The block's calls for chunk c; returns what each stage stored."""
+        h = self.heads
+        slot = gdn.sink_window_slot(c, self.n_sink, self.window)
+        q, _ = gdn.qk_norm_rope(qkv[:, :, :h], qkv[:, :, h:2 * h], self.wq, self.wk, self.positions(c), self.freq,
+                                k_out=self.kc[:, slot], **self.turn())
+        self.vc[:, slot].copy_(qkv[:, :, 2 * h:])
+        a = gdn.sink_window_attention(q, self.kc[:, slot], self.vc[:, slot], self.kc, self.vc, c, self.n_sink,
+                                      self.window)
+        x, _ = gdn.qk_norm_rope(a, None, self.wx)
+        return q, slot, a, x, gdn.cross_attention(x, self.kn_enc, self.v_enc, self.mask)
+
+
+def close_norm(got, ref, pair):
+    assert (np.abs(np64(got) - ref) <= 1.01 * H * np.abs(ref) + 2.0 ** -19 * pair).all()
+
+
+def test_stream_of_chunks():
+    b = Block(1)
+    ks, vs = [], []
+    for c in range(5):
+        qkv = b.normal(1, b.Tc, 3 * b.heads, b.D).bfloat16()
+        q, slot, a, x, out = b.chunk(c, qkv)
+        torch.cuda.synchronize()
+        assert gdn.device_error() == _lib.GDN_OK
+        ang = nr.angles(b.positions(c)[None].cpu().numpy(), b.freq.cpu().numpy(), b.sections)
+        h = b.heads
+        for got, src, w in ((q, qkv[:, :, :h], b.wq), (b.kc[:, slot], qkv[:, :, h:2 * h], b.wk)):
+            y = nr.norm(np64(src), np64(w), 1e-6)
+            pair = np.abs(y).max(-1, keepdims=True) * 2
+            close_norm(got, nr.turn(y, ang, "half", b.amp), pair)
+        ks.append(np64(b.kc[:, slot]))
+        vs.append(np64(qkv[:, :, 2 * h:]))
+        ref = swa.chunk_output(np64(q), np.concatenate(ks, 1), np.concatenate(vs, 1), c, b.Tc, b.n_sink, b.window)
+        assert max_rel_per_head(np64(a), ref, (0, 2)) <= TOL["bf16"], c
+        y = nr.norm(np64(a), np64(b.wx), 1e-6)
+        close_norm(x, y, np.abs(y).max(-1, keepdims=True))
+        args = (np64(x), np64(b.kn_enc))
+        m = b.mask.cpu().numpy()
+        ref, _ = ca.forward(*args, np64(b.v_enc), m)
+        size, _ = ca.forward(*args, np.abs(np64(b.v_enc)), m)
+        assert (np.abs(np64(out) - ref) <= H * np.abs(ref) + (H + 1e-3) * size).all(), c
+
+
+def test_captured_chunk_gives_the_same_bits():
+    """One graph holds a chunk's five calls; replayed with new projections in its
+    input it gives the eager calls' bits."""
+    eager, graphed = Block(2), Block(2)
+    inputs = [eager.normal(1, eager.Tc, 3 * eager.heads, eager.D).bfloat16() for _ in range(3)]
+    static = inputs[0].clone()
+    graphed.chunk(0, static)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = graphed.chunk(0, static)[-1]
+    for x in inputs:
+        want = eager.chunk(0, x)[-1]
+        static.copy_(x)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert torch.equal(eager.kc, graphed.kc) and torch.equal(eager.vc, graphed.vc)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_training_step(captured):
+    """Gradients of <out, g> through the attention to the encoder and the norms and
+    rotations before it, against fp64 autograd of the whole.  On the way to each
+    gradient at most ten values are rounded to bf16 (q, k, P and out going forward;
+    P, dS, delta through out, the inner gradient and the result going back, and the
+    scores' two operands again), each by at most h of its size: 10 h of the norm."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    n = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    B, T, S, Hk, G, D = 2, 150, 210, 2, 2, 64
+    q, k, v = n(B, T, Hk * G, D).bfloat16(), n(B, S, Hk, D).bfloat16(), n(B, S, Hk, D).bfloat16()
+    wq, wk = 1 + 0.2 * n(D), 1 + 0.2 * n(D)
+    g = n(B, T, Hk * G, D).bfloat16()
+    pos = torch.arange(T, device="cuda")
+    freq, amp = gdn.rope_frequencies(32, scaling="yarn", factor=2.0, original_length=64)
+    mask = torch.rand(B, S, generator=gen, device="cuda") < 0.8
+
+    def step():
+        qn, _ = gdn.qk_norm_rope(q, None, wq, None, pos, freq, amplitude=amp)
+        kn, _ = gdn.qk_norm_rope(k, None, wk)
+        out, lse = gdn.cross_attention(qn, kn, v, mask, return_lse=True)
+        d = gdn.cross_attention_backward(qn, kn, v, out, lse, g, mask)
+        dq = gdn.qk_norm_rope_backward(q, None, wq, None, d["dq"], None, pos, freq, amplitude=amp)
+        dk = gdn.qk_norm_rope_backward(k, None, wk, None, d["dk"], None)
+        return {"q": dq["dq"], "wq": dq["dq_weight"], "k": dk["dq"], "wk": dk["dq_weight"], "v": d["dv"]}
+
+    if captured:
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = step()
+        graph.replay()
+        torch.cuda.synchronize()
+    else:
+        got = step()
+    leaves = {"q": q, "k": k, "v": v, "wq": wq, "wk": wk}
+    x = {name: t.double().cpu().requires_grad_() for name, t in leaves.items()}
+
+    def norm(y, w):
+        return y * w / torch.sqrt((y * y).mean(-1, keepdim=True) + 1e-6)
+    y = norm(x["q"], x["wq"])
+    ang = (pos.double()[:, None] * freq).cpu()[None, :, None]
+    c, s = amp * ang.cos(), amp * ang.sin()
+    a, b = y[..., :16], y[..., 16:32]
+    y = torch.cat([a * c - b * s, a * s + b * c, y[..., 32:]], -1)
+    z = norm(x["k"], x["wk"]).repeat_interleave(G, 2)
+    scores = torch.einsum("bthd,bshd->bhts", y, z) * D ** -0.5
+    scores = scores.masked_fill(~mask.cpu()[:, None, None], -np.inf)
+    out = torch.einsum("bhts,bshd->bthd", scores.softmax(-1), x["v"].repeat_interleave(G, 2))
+    out.backward(g.double().cpu())
+    for name, t in x.items():
+        e = np.linalg.norm(np64(got[name]) - t.grad.numpy()) / np.linalg.norm(t.grad.numpy())
+        assert e <= 10 * H, (name, e)
