@@ -1513,22 +1513,6 @@ bool make_tile_map(CUtensorMap* m, const void* base, int nb, int T, int H, int D
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_heads_map(CUtensorMap* m, const void* base, int nb, int T, int Hk, int G, int D,
-                    long long batch_stride, long long token_stride, int box_tokens) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  // a stride that is never stepped by still has to be a valid one
-  const cuuint64_t ts = T > 1 ? (cuuint64_t)token_stride * 2 : (cuuint64_t)Hk * G * D * 2;
-  const cuuint64_t bs = nb > 1 ? (cuuint64_t)batch_stride * 2 : ts * (cuuint64_t)T;
-  const cuuint64_t dims[5] = {(cuuint64_t)D, (cuuint64_t)G, (cuuint64_t)T, (cuuint64_t)Hk, (cuuint64_t)nb};
-  const cuuint64_t strides[4] = {(cuuint64_t)D * 2, ts, (cuuint64_t)G * D * 2, bs};
-  const cuuint32_t box[5] = {64, (cuuint32_t)G, (cuuint32_t)box_tokens, 1, 1};
-  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 int num_sms() {
   constexpr int kMaxDev = 64;
   static int cached[kMaxDev] = {};

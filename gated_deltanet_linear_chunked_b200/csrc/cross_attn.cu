@@ -154,6 +154,7 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     aux.abort = 0;
     aux.count = kn;
     fence_mbar_init();
+    pdl_wait();  // inputs may come from the kernel in front
     // the queries are on their way while the CTA sets up and reads its mask
     const uint32_t qbytes = (uint32_t)P.tokens * P.G * 128;  // of one 64-feature block
     mbar_arrive_expect_tx(&aux.q_full, nq * nb * qbytes);
@@ -166,7 +167,8 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     tmem_alloc(&aux.tmem, kTileCols * NQ);
     tmem_relinquish();
   }
-  pdl_trigger();  // the join's blocks may take their places; they wait for this grid
+  pdl_wait();
+  pdl_trigger();  // the next kernel's blocks may take their places; they wait for this grid
   if (P.mask) {
     const uint8_t* mrow = P.mask + b * P.mask_bs;
     for (int w = warp; w < kn * 4; w += Roles<NQ>::softmax_warps) {
@@ -479,6 +481,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int per, long long rows) {
   const long long i = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  pdl_wait();
   if (i >= rows) return;
   const long long su = i / per;                       // per: rows of a unit, in whole tiles or one of few
   const int ur = (int)(i - su * per), r = ur % kRows;
@@ -488,7 +491,6 @@ gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int per, long long 
   const int hk = (int)(bh - b * P.Hk), t = tile * P.tokens + r / P.G, head = hk * P.G + r % P.G;
   if (r >= P.tokens * P.G || t >= P.Tq) return;       // no row
   const long long at = su * P.nsplit * per + ur;      // of split 0, then every `per`
-  pdl_wait();
   float top = -INFINITY;
   for (int s = 0; s < P.nsplit; ++s) top = fmaxf(top, P.part_lse[at + (long long)s * per]);
   const bool any = top > -INFINITY;
@@ -574,8 +576,7 @@ cudaError_t launch_nb(unsigned grid, cudaStream_t stream, const CUtensorMap& mq,
   const cudaError_t e = allow_smem(gdn_cross_kernel<NB, NQ>, bytes);
   if (e != cudaSuccess) return e;
   ProfileScope ps(stream, kKernCross);
-  gdn_cross_kernel<NB, NQ><<<grid, Roles<NQ>::threads, bytes, stream>>>(mq, mk, mv, P);
-  return cudaSuccess;
+  return launch_after(gdn_cross_kernel<NB, NQ>, grid, Roles<NQ>::threads, bytes, stream, mq, mk, mv, P);
 }
 
 cudaError_t launch_tiles(const CrossCall& c, CrossParams* P, int nq, unsigned grid) {
@@ -599,7 +600,6 @@ cudaError_t launch_tiles(const CrossCall& c, CrossParams* P, int nq, unsigned gr
     e = c.D > 64 ? launch_nb<2, 1>(grid, c.stream, mq, mk, mv, *P) : launch_nb<1, 1>(grid, c.stream, mq, mk, mv, *P);
   else
     e = c.D > 64 ? launch_nb<2, 2>(grid, c.stream, mq, mk, mv, *P) : launch_nb<1, 2>(grid, c.stream, mq, mk, mv, *P);
-  if (e == cudaSuccess) e = cudaGetLastError();
   if (e == cudaSuccess) count_launches(1);
   return e;
 }

@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(kStatThreads)
 gdn_cross_stat_kernel(const __nv_bfloat16* out, const __nv_bfloat16* d_out, const float* lse, float* stat,
                       long long rows, unsigned row_blocks, const uint8_t* mask, long long mask_bs,
                       const __grid_constant__ BwdParams P) {
+  pdl_wait();  // inputs may come from the kernel in front
   pdl_trigger();
   if (blockIdx.x >= row_blocks) {
     const int b = blockIdx.x - row_blocks;
@@ -866,14 +867,14 @@ cudaError_t launch_cross_backward(const CrossCall& c, void* ws) {
                       kRows))
     return cudaErrorInvalidValue;
   const long long rows = (long long)c.B * c.Hk * P.qtiles * kRows;
+  cudaError_t e;
   {
     ProfileScope ps(c.stream, kKernCrossStat);
     const unsigned blocks = (unsigned)((rows + kStatBlockRows - 1) / kStatBlockRows);
-    gdn_cross_stat_kernel<<<blocks + (c.mask ? c.B : 0), kStatThreads, 0, c.stream>>>(
-        static_cast<const __nv_bfloat16*>(c.out), static_cast<const __nv_bfloat16*>(c.d_out), c.lse,
-        static_cast<float*>(ws), rows, blocks, c.mask, c.mask_bs, P);
+    e = launch_after(gdn_cross_stat_kernel, blocks + (c.mask ? c.B : 0), kStatThreads, 0, c.stream,
+                     static_cast<const __nv_bfloat16*>(c.out), static_cast<const __nv_bfloat16*>(c.d_out),
+                     (const float*)c.lse, static_cast<float*>(ws), rows, blocks, c.mask, c.mask_bs, P);
   }
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   count_launches(1);
   e = c.D > 64 ? launch_nb<2>(c, P, mq, mg, mk, mv)

@@ -72,6 +72,7 @@ gdn_cross_few_kernel(const __grid_constant__ FewParams F) {
   const int b = bh / P.Hk, hk = bh - b * P.Hk;
   const int rows = P.tokens * P.G;  // of the 16
   const int Hq = P.Hk * P.G;
+  pdl_wait();  // inputs may come from the kernel in front
   pdl_trigger();
 
   // piece c of row r of a group: swizzled within aligned runs of eight pieces, or of
@@ -276,8 +277,7 @@ cudaError_t launch_nk(const FewParams& F, unsigned grid, cudaStream_t stream) {
   const cudaError_t e = allow_smem(gdn_cross_few_kernel<NK>, bytes);
   if (e != cudaSuccess) return e;
   ProfileScope ps(stream, kKernCrossFew);
-  gdn_cross_few_kernel<NK><<<grid, 32 * kWarps, bytes, stream>>>(F);
-  return cudaGetLastError();
+  return launch_after(gdn_cross_few_kernel<NK>, grid, 32 * kWarps, bytes, stream, F);
 }
 
 }  // namespace

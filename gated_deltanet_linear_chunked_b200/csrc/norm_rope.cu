@@ -264,6 +264,8 @@ gdn_norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
   const long long b = bu, t = tu;
   const T* x = static_cast<const T*>(S.x) + b * S.x_bs + t * S.x_ts;
   T* out = static_cast<T*>(S.out) + b * S.o_bs + t * S.o_ts;
+  pdl_wait();  // inputs may come from the kernel in front
+  pdl_trigger();
   // two heads' loads are always under way, the first before the angles
   uint4 ring[2][2];
   auto fetch = [&](uint4 (&to)[2], int h) {
@@ -332,6 +334,8 @@ gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
   const Side& S = P.side[pl.side];
   const int tk = pl.token, h0 = pl.h0;
   const Pieces pc = pieces_of<V, interleaved>(l, P.D, P.R);
+  pdl_wait();  // inputs may come from the kernel in front
+  pdl_trigger();
   uint64_t w[V], dw[V];
   take_weights<V>(S.w, pc, w);
 #pragma unroll
@@ -424,7 +428,6 @@ gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
       for (int x = lo; x < hi; ++x) sum += red[(k * per + x) * P.D + f];
     P.partial[((size_t)side * gridDim.x + blockIdx.x) * P.D + f] = sum;
   }
-  pdl_trigger();
 }
 
 // dw[side][f] = sum over the side's blocks of partial[block][f]: one block per
@@ -435,9 +438,9 @@ gdn_norm_rope_reduce_kernel(const float* partial, unsigned blocks, int D, float*
   pdl_wait();
   __shared__ float red[kRedRows][kRedCols + 1];
   const int col = threadIdx.x % kRedCols, row = threadIdx.x / kRedCols;
-  const int f = blockIdx.x * kRedCols + col;
-  float* dw = blockIdx.y ? dw1 : dw0;
-  const float* from = partial + (size_t)blockIdx.y * blocks * D + f;
+  const int per = D / kRedCols, side = blockIdx.x / per, f = (blockIdx.x - side * per) * kRedCols + col;
+  float* dw = side ? dw1 : dw0;
+  const float* from = partial + (size_t)side * blocks * D + f;
   float sum = 0.f;
   for (unsigned i = row; i < blocks; i += kRedRows) sum += from[(size_t)i * D];
   red[row][col] = sum;
@@ -494,21 +497,13 @@ cudaError_t launch_g(NormRopeParams& P, bool backward, cudaStream_t stream, unsi
   size_t smem = (size_t)P.tb * (P.R / 2) * sizeof(float2);
   if (backward) smem = std::max(smem, (size_t)groups * P.D * sizeof(float));
   *blocks = grid;
-  if (backward) {
-    ProfileScope ps(stream, kKernNormRopeBwd);
-    if (P.interleaved)
-      gdn_norm_rope_bwd_kernel<T, G, true><<<grid, kThreads, smem, stream>>>(P);
-    else
-      gdn_norm_rope_bwd_kernel<T, G, false><<<grid, kThreads, smem, stream>>>(P);
-  } else {
-    ProfileScope ps(stream, kKernNormRope);
-    if (P.interleaved)
-      gdn_norm_rope_kernel<T, G, true><<<grid, kThreads, smem, stream>>>(P);
-    else
-      gdn_norm_rope_kernel<T, G, false><<<grid, kThreads, smem, stream>>>(P);
-  }
-  count_launches(1);
-  return cudaGetLastError();
+  ProfileScope ps(stream, backward ? kKernNormRopeBwd : kKernNormRope);
+  void (*kernel)(const NormRopeParams) =
+      backward ? (P.interleaved ? gdn_norm_rope_bwd_kernel<T, G, true> : gdn_norm_rope_bwd_kernel<T, G, false>)
+               : (P.interleaved ? gdn_norm_rope_kernel<T, G, true> : gdn_norm_rope_kernel<T, G, false>);
+  const cudaError_t e = launch_after(kernel, grid, kThreads, smem, stream, P);
+  if (e == cudaSuccess) count_launches(1);
+  return e;
 }
 
 template <typename T>
@@ -736,18 +731,9 @@ gdn_status run(const Call& c) {
   cudaError_t e = c.dtype == GDN_BF16 ? launch_t<__nv_bfloat16>(P, true, stream, &blocks)
                                       : launch_t<float>(P, true, stream, &blocks);
   if (e == cudaSuccess && (c.dw[0] || c.dw[1])) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(c.D / kRedCols, 2);
-    cfg.blockDim = dim3(kRedCols * kRedRows);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
     ProfileScope ps(stream, kKernNormRopeReduce);
-    e = cudaLaunchKernelEx(&cfg, gdn_norm_rope_reduce_kernel, (const float*)P.partial, blocks, c.D,
-                           c.dw[0], c.dw[1]);
+    e = launch_after(gdn_norm_rope_reduce_kernel, 2 * (c.D / kRedCols), kRedCols * kRedRows, 0, stream,
+                     (const float*)P.partial, blocks, c.D, c.dw[0], c.dw[1]);
     if (e == cudaSuccess) count_launches(1);
   }
   const cudaError_t f = op_scratch_done(sc);
