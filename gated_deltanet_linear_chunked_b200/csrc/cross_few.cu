@@ -32,16 +32,6 @@ constexpr int kWarps = 4;
 constexpr int kKeys = 16;     // keys of a group
 constexpr int kDepth = 3;     // groups on their way per warp
 
-// 16 bytes to shared memory, zeros where `on` is false (then nothing is read).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 struct FewParams {
   CrossParams c;
   const __nv_bfloat16 *q, *k, *v;

@@ -192,7 +192,8 @@ template <typename K>
 cudaError_t allow_smem(K kernel, int bytes) {
   constexpr int kMaxDev = 64;
   static std::mutex mu;
-  static const void* seen[kMaxDev][4] = {};  // kernels of one type share this function
+  constexpr int kMost = 32;  // kernels of one type share this function
+  static const void* seen[kMaxDev][kMost] = {};
   int dev = 0;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -200,10 +201,10 @@ cudaError_t allow_smem(K kernel, int bytes) {
   const void* f = reinterpret_cast<const void*>(kernel);
   std::lock_guard<std::mutex> lock(mu);
   int i = 0;
-  while (i < 4 && seen[dev][i] && seen[dev][i] != f) ++i;
-  if (i < 4 && seen[dev][i]) return cudaSuccess;
+  while (i < kMost && seen[dev][i] && seen[dev][i] != f) ++i;
+  if (i < kMost && seen[dev][i]) return cudaSuccess;
   const cudaError_t s = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (s == cudaSuccess && i < 4) seen[dev][i] = f;
+  if (s == cudaSuccess && i < kMost) seen[dev][i] = f;
   return s;
 }
 

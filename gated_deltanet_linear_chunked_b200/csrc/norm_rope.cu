@@ -188,43 +188,89 @@ __device__ __forceinline__ Place place_of(const NormRopeParams& P, int grp) {
   return p;
 }
 
-// Fills tab[token][pair] for the tokens n0 .. n0 + tb - 1.
-__device__ __forceinline__ void fill_angles(const NormRopeParams& P, float2* tab, unsigned n0) {
+// The angles' table: for every token of a tile, lane l of a group and j < V / 2, the
+// cosines and sines of the lane's pairs V l + 2 j and V l + 2 j + 1 as
+// (cos, cos, sin, sin), at [token][j][l] so that a group's lanes read side by side.
+template <int V, int G>
+__device__ __forceinline__ void fill_angles(const NormRopeParams& P, float* tab, unsigned n0) {
   const int pairs = P.R / 2;
   for (int i = threadIdx.x; i < P.tb * pairs; i += kThreads) {
-    const int tk = i / pairs;
-    if (n0 + tk < P.tokens) tab[i] = angle(P, n0 + tk, i - tk * pairs);
+    const int tk = i / pairs, p = i - tk * pairs;
+    if (n0 + tk >= P.tokens) continue;
+    const float2 a = angle(P, n0 + tk, p);
+    float* to = tab + (((tk * (V / 2) + p % V / 2) * G + p / V) * 4 + p % 2);
+    to[0] = a.x;
+    to[2] = a.y;
   }
+}
+// Entry j of a lane: cosines and sines of two pairs (1 and 0 where nothing turns).
+__device__ __forceinline__ float4 angles_at(const float4* row, bool on, int j, int G) {
+  return on ? row[j * G] : make_float4(1.f, 1.f, 0.f, 0.f);
 }
 
 // A lane's factors c1, c2 (see turn) from its token's row of the table and the
 // weights of its features, wx of the feature itself and wp of its partner:
 // turned = wx x c1 + wp partner c2 with the weights folded in (pass ones to leave
 // them out).
-template <int V, bool interleaved>
-__device__ __forceinline__ void take_angles(const float2* row, const Pieces& pc, int l, const uint64_t (&w)[V],
+template <int V, int G, bool interleaved>
+__device__ __forceinline__ void take_angles(const float4* row, const Pieces& pc, const uint64_t (&w)[V],
                                             uint64_t (&c1)[V], uint64_t (&c2)[V]) {
   constexpr int N = V / 2;
   float wf[2 * V];
 #pragma unroll
   for (int j = 0; j < V; ++j) f2_unpack(w[j], wf[2 * j], wf[2 * j + 1]);
+  const bool on_a = pc.turns_a && pc.present, on_b = pc.turns_b && pc.present;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     if (interleaved) {  // pairs V l + j (piece a) and V l + N + j (piece b)
-      const float2 a = pc.turns_a && pc.present ? row[l * V + j] : make_float2(1.f, 0.f);
-      const float2 b = pc.turns_b && pc.present ? row[l * V + N + j] : make_float2(1.f, 0.f);
-      c1[j] = f2_pack(wf[2 * j] * a.x, wf[2 * j + 1] * a.x);
-      c2[j] = f2_pack(-wf[2 * j + 1] * a.y, wf[2 * j] * a.y);
-      c1[N + j] = f2_pack(wf[V + 2 * j] * b.x, wf[V + 2 * j + 1] * b.x);
-      c2[N + j] = f2_pack(-wf[V + 2 * j + 1] * b.y, wf[V + 2 * j] * b.y);
+      const float4 fa = angles_at(row, on_a, j / 2, G), fb = angles_at(row, on_b, (N + j) / 2, G);
+      const float ca = j % 2 ? fa.y : fa.x, sa = j % 2 ? fa.w : fa.z;
+      const float cb = j % 2 ? fb.y : fb.x, sb = j % 2 ? fb.w : fb.z;
+      c1[j] = f2_pack(wf[2 * j] * ca, wf[2 * j + 1] * ca);
+      c2[j] = f2_pack(-wf[2 * j + 1] * sa, wf[2 * j] * sa);
+      c1[N + j] = f2_pack(wf[V + 2 * j] * cb, wf[V + 2 * j + 1] * cb);
+      c2[N + j] = f2_pack(-wf[V + 2 * j + 1] * sb, wf[V + 2 * j] * sb);
     } else {  // pairs V l + 2 j and V l + 2 j + 1
-      const bool on = pc.turns_a && pc.present;
-      const float2 a = on ? row[l * V + 2 * j] : make_float2(1.f, 0.f);
-      const float2 b = on ? row[l * V + 2 * j + 1] : make_float2(1.f, 0.f);
-      c1[j] = f2_pack(wf[2 * j] * a.x, wf[2 * j + 1] * b.x);
-      c2[j] = f2_pack(-wf[V + 2 * j] * a.y, -wf[V + 2 * j + 1] * b.y);
-      c1[N + j] = f2_pack(wf[V + 2 * j] * a.x, wf[V + 2 * j + 1] * b.x);
-      c2[N + j] = f2_pack(wf[2 * j] * a.y, wf[2 * j + 1] * b.y);
+      const float4 f = angles_at(row, on_a, j, G);
+      c1[j] = f2_pack(wf[2 * j] * f.x, wf[2 * j + 1] * f.y);
+      c2[j] = f2_pack(-wf[V + 2 * j] * f.z, -wf[V + 2 * j + 1] * f.w);
+      c1[N + j] = f2_pack(wf[V + 2 * j] * f.x, wf[V + 2 * j + 1] * f.y);
+      c2[N + j] = f2_pack(wf[2 * j] * f.z, wf[2 * j + 1] * f.w);
+    }
+  }
+}
+
+// 16 bytes of shared memory that the compiler is not to keep in registers.
+__device__ __forceinline__ float4 reread(uint32_t addr) {
+  uint32_t r[4];
+  ld_shared_v4(addr, r);
+  return make_float4(__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[2]), __uint_as_float(r[3]));
+}
+
+// The turn of a gradient, its factors straight from the table, read anew for every
+// head: kept in registers they make the gradient kernel spill (the chunk's gradients
+// 23.8 us against 21.0; a third block per SM at 80 registers spills as well, 28.5).
+template <int V, int G, bool interleaved>
+__device__ __forceinline__ void turn_from(uint32_t row, uint64_t (&x)[V], const Pieces& pc) {
+  constexpr int N = V / 2;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    if (interleaved) {
+      if (j % 2) continue;
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        if (!(side ? pc.turns_b : pc.turns_a)) continue;
+        const float4 f = reread(row + ((side * N + j) / 2) * G * 16);
+        uint64_t* y = x + side * N + j;
+        y[0] = f2_fma(f2_swap(y[0]), f2_pack(-f.z, f.z), f2_mul(y[0], f2_pack(f.x, f.x)));
+        y[1] = f2_fma(f2_swap(y[1]), f2_pack(-f.w, f.w), f2_mul(y[1], f2_pack(f.y, f.y)));
+      }
+    } else if (pc.turns_a) {
+      const float4 f = reread(row + j * G * 16);
+      const uint64_t c = f2_pack(f.x, f.y), s = f2_pack(f.z, f.w), ns = f2_pack(-f.z, -f.w);
+      const uint64_t a = f2_fma(x[N + j], ns, f2_mul(x[j], c));
+      x[N + j] = f2_fma(x[j], s, f2_mul(x[N + j], c));
+      x[j] = a;
     }
   }
 }
@@ -252,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 3)
 gdn_norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
   using VT = Vec<T>;
   constexpr int V = VT::V, N = V / 2;
-  extern __shared__ float2 tab[];
+  extern __shared__ __align__(16) float tab[];
   const int l = threadIdx.x % G;
   const Place pl = place_of(P, threadIdx.x / G);
   const Side& S = P.side[pl.side];
@@ -282,10 +328,10 @@ gdn_norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
     uint64_t w[V];
     take_weights<V>(S.w, pc, w);
     if (P.R > 0) {
-      fill_angles(P, tab, n0);
+      fill_angles<V, G>(P, tab, n0);
       __syncthreads();
     }
-    take_angles<V, interleaved>(tab + min(tk, P.tb - 1) * (P.R / 2), pc, l, w, c1, c2);
+    take_angles<V, G, interleaved>(reinterpret_cast<const float4*>(tab) + min(tk, P.tb - 1) * (N * G) + l, pc, w, c1, c2);
   }
   const float inv_d = 1.f / P.D;
   auto work = [&](const uint4 (&from)[2], int h) {
@@ -328,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
   using VT = Vec<T>;
   constexpr int V = VT::V, N = V / 2;
-  extern __shared__ float2 tab[];
+  extern __shared__ __align__(16) float tab[];
   const int l = threadIdx.x % G, grp = threadIdx.x / G;
   const Place pl = place_of(P, grp);
   const Side& S = P.side[pl.side];
@@ -336,6 +382,7 @@ gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
   const Pieces pc = pieces_of<V, interleaved>(l, P.D, P.R);
   pdl_wait();  // inputs may come from the kernel in front
   pdl_trigger();
+  const uint32_t row = smem_u32(tab) + (min(tk, P.tb - 1) * (N * G) + l) * 16;
   uint64_t w[V], dw[V];
   take_weights<V>(S.w, pc, w);
 #pragma unroll
@@ -364,15 +411,8 @@ gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
     fetch(h0);
     if (P.R > 0) {
       __syncthreads();  // the table's readers of the tile before
-      fill_angles(P, tab, n0);
+      fill_angles<V, G>(P, tab, n0);
       __syncthreads();
-    }
-    uint64_t c1[V], c2[V];
-    {
-      uint64_t ones[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) ones[j] = f2_pack(1.f, 1.f);
-      take_angles<V, interleaved>(tab + min(tk, P.tb - 1) * (P.R / 2), pc, l, ones, c1, c2);
     }
     for (int i = 0, h = h0; i < P.heads; ++i, h += S.per) {
       uint64_t v[V], g[V];
@@ -381,12 +421,14 @@ gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
       VT::open(ring[2], g);
       VT::open(ring[3], g + N);
       fetch(h + S.per);
-      turn<V, interleaved>(g, c1, c2, pc);
+      if (pc.present) turn_from<V, G, interleaved>(row, g, pc);
       uint64_t s2[2] = {0, 0}, d2[2] = {0, 0};
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        s2[j & 1] = f2_fma(v[j], v[j], s2[j & 1]);
-        d2[j & 1] = f2_fma(f2_mul(g[j], w[j]), v[j], d2[j & 1]);
+      for (int j = 0; j < V; j += 2) {
+        s2[0] = f2_fma(v[j], v[j], s2[0]);
+        s2[1] = f2_fma(v[j + 1], v[j + 1], s2[1]);
+        d2[0] = f2_fma(f2_mul(g[j], w[j]), v[j], d2[0]);
+        d2[1] = f2_fma(f2_mul(g[j + 1], w[j + 1]), v[j + 1], d2[1]);
       }
       float sa, sb, da, db;
       f2_unpack(f2_add(s2[0], s2[1]), sa, sb);
@@ -396,10 +438,13 @@ gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
       const float m = -dot * r * inv_d;  // -mean(g w x^)
       const uint64_t r2 = f2_pack(r, r), m2 = f2_pack(m, m);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const uint64_t hat = f2_mul(v[j], r2);
-        dw[j] = f2_fma(g[j], hat, dw[j]);
-        g[j] = f2_mul(r2, f2_fma(hat, m2, f2_mul(g[j], w[j])));
+      for (int j = 0; j < V; j += 2) {
+#pragma unroll
+        for (int e = j; e < j + 2; ++e) {
+          const uint64_t hat = f2_mul(v[e], r2);
+          dw[e] = f2_fma(g[e], hat, dw[e]);
+          g[e] = f2_mul(r2, f2_fma(hat, m2, f2_mul(g[e], w[e])));
+        }
       }
       if (on && h < S.H) {
         *reinterpret_cast<uint4*>(out + (long long)h * P.D + pc.a * V) = VT::close(g);
@@ -491,10 +536,10 @@ bool share_groups(int groups, int slots, NormRopeParams* P) {
 template <typename T, int G>
 cudaError_t launch_g(NormRopeParams& P, bool backward, cudaStream_t stream, unsigned* blocks) {
   constexpr int groups = kThreads / G;
-  const int slots = (backward ? 2 : 3) * num_sms();
+  const int slots = (backward ? 2 : 3) * num_sms();  // blocks that run at a time
   if (!share_groups(groups, slots, &P)) return cudaErrorInvalidValue;
   const unsigned grid = backward ? std::min<unsigned>(P.tiles, slots) : P.tiles;
-  size_t smem = (size_t)P.tb * (P.R / 2) * sizeof(float2);
+  size_t smem = (size_t)P.tb * (Vec<T>::V / 2) * G * 16;
   if (backward) smem = std::max(smem, (size_t)groups * P.D * sizeof(float));
   *blocks = grid;
   ProfileScope ps(stream, backward ? kKernNormRopeBwd : kKernNormRope);
