@@ -169,7 +169,7 @@ gdn_status gdn_cross_attention(const gdn_rows* q, const gdn_rows* k, const gdn_r
   if (st != GDN_OK) return st;
   c.limit = current_wait_limit();
   const cudaError_t e = launch_cross(c, sc.p);
-  const cudaError_t f = op_scratch_done(sc);
+  const cudaError_t f = op_scratch_done(&sc);
   return finish(c.stream, e == cudaSuccess ? f : e, c.err);
 }
 
@@ -228,7 +228,7 @@ gdn_status gdn_cross_attention_backward(const gdn_rows* q, const gdn_rows* k, co
   if (st != GDN_OK) return st;
   c.limit = current_wait_limit();
   const cudaError_t e = launch_cross_backward(c, sc.p);
-  const cudaError_t f = op_scratch_done(sc);
+  const cudaError_t f = op_scratch_done(&sc);
   return finish(c.stream, e == cudaSuccess ? f : e, c.err);
 }
 

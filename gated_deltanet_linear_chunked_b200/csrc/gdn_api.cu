@@ -98,6 +98,10 @@ struct StreamCtx {
   size_t ws_bytes;
 };
 
+// Held over the launches of a call that passes scratch between them: two threads
+// that call on one stream share its scratch, so their launches must not interleave.
+std::mutex g_launch_mu;
+
 std::mutex g_ctx_mu;
 std::vector<StreamCtx*> g_ctx;
 struct Retired {
@@ -187,6 +191,7 @@ gdn_status scan(const void* q, const void* k, const void* v, const void* g,
   const size_t bytes =
       dtype == GDN_BF16 ? chunk_tc_workspace_bytes(B, T, H, Dk, Dv, bidir) : 0;
   void* ws = nullptr;
+  std::unique_lock<std::mutex> launching(g_launch_mu);
   st = stream_context(dev, a.stream, bytes, &a.err, &ws);
   if (st != GDN_OK) return st;
   if (!a.err && error_word(&a.err) != cudaSuccess) {
@@ -210,6 +215,7 @@ gdn_status scan(const void* q, const void* k, const void* v, const void* g,
       if (e == cudaSuccess) e = f;
     }
   }
+  launching.unlock();
   return finish(a.stream, e, a.err);
 }
 
@@ -331,6 +337,7 @@ void count_launches(unsigned n) { g_launches.fetch_add(n); }
 
 gdn_status op_scratch(int dev, cudaStream_t s, size_t bytes, unsigned int** err, OpScratch* sc) {
   sc->stream = s;
+  sc->launching = std::unique_lock<std::mutex>(g_launch_mu);
   sc->captured = bytes > 0 && capturing(s);
   gdn_status st = stream_context(dev, s, sc->captured ? 0 : bytes, err, &sc->p);
   if (st != GDN_OK) return st;
@@ -346,8 +353,10 @@ gdn_status op_scratch(int dev, cudaStream_t s, size_t bytes, unsigned int** err,
   return GDN_OK;
 }
 
-cudaError_t op_scratch_done(const OpScratch& sc) {
-  return sc.captured ? cudaFreeAsync(sc.p, sc.stream) : cudaSuccess;
+cudaError_t op_scratch_done(OpScratch* sc) {
+  const cudaError_t e = sc->captured ? cudaFreeAsync(sc->p, sc->stream) : cudaSuccess;
+  if (sc->launching.owns_lock()) sc->launching.unlock();
+  return e;
 }
 
 namespace {
@@ -407,6 +416,7 @@ gdn_status backward(const void* q, const void* k, const void* v, const float* g,
   }
   unsigned int* err = nullptr;
   void* ws = nullptr;
+  std::unique_lock<std::mutex> launching(g_launch_mu);
   const size_t bytes = bwd_workspace_bytes(B, T, H, Dk, Dv, dtype, bidir);
   st = stream_context(dev, s, bytes, &err, &ws);
   if (st != GDN_OK) return st;
@@ -432,6 +442,7 @@ gdn_status backward(const void* q, const void* k, const void* v, const float* g,
       if (e == cudaSuccess) e = f;
     }
   }
+  launching.unlock();
   return finish(s, e, err);
 }
 gdn_status sink_window(const void* q, const void* k, const void* v, void* k_cache,

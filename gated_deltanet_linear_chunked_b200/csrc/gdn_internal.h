@@ -249,14 +249,16 @@ cudaError_t launch_sink_window(const SwaCall& c);
 // a call that is being captured, an allocation of the graph's own (memory
 // nodes), so that two captured graphs never share it whatever streams they are
 // replayed on.  `err` gets the stream's error word, or the device-wide one.
-// GDN_OK or GDN_ERR_CUDA.
+// GDN_OK or GDN_ERR_CUDA.  No other call that uses scratch launches until
+// op_scratch_done (or the end of `sc`).
 struct OpScratch {
-  void* p;
-  cudaStream_t stream;
-  bool captured;
+  void* p = nullptr;
+  cudaStream_t stream = nullptr;
+  bool captured = false;
+  std::unique_lock<std::mutex> launching;
 };
 gdn_status op_scratch(int dev, cudaStream_t s, size_t bytes, unsigned int** err, OpScratch* sc);
-cudaError_t op_scratch_done(const OpScratch& sc);
+cudaError_t op_scratch_done(OpScratch* sc);
 
 // One cross-attention call, after validation.
 struct CrossCall {

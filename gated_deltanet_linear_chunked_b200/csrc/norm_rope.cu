@@ -781,7 +781,7 @@ gdn_status run(const Call& c) {
                      (const float*)P.partial, blocks, c.D, c.dw[0], c.dw[1]);
     if (e == cudaSuccess) count_launches(1);
   }
-  const cudaError_t f = op_scratch_done(sc);
+  const cudaError_t f = op_scratch_done(&sc);
   return finish(stream, e == cudaSuccess ? f : e, nullptr);
 }
 

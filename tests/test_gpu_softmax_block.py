@@ -173,3 +173,52 @@ def test_training_step(captured):
     for name, t in x.items():
         e = np.linalg.norm(np64(got[name]) - t.grad.numpy()) / np.linalg.norm(t.grad.numpy())
         assert e <= 10 * H, (name, e)
+
+
+def test_two_threads_on_one_stream():
+    """Two host threads call the C entries on one stream at once, which share its
+    scratch (partial sums, row statistics, shares): every call's results are those of
+    the same call alone."""
+    import struct
+    import threading
+    lib = _lib.load()
+    rows = lambda t: struct.pack("Pqq", t.data_ptr(), t.stride(0), t.stride(1))  # noqa: E731
+    stream = torch.cuda.current_stream().cuda_stream
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    n = lambda *s: torch.randn(s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    jobs = []
+    for Tq, S in ((1500, 140), (2100, 260)):
+        q, k, v, g = n(1, Tq, 4, 64), n(1, S, 2, 64), n(1, S, 2, 64), n(1, Tq, 4, 64)
+        mask = torch.rand(1, S, generator=gen, device="cuda") < 0.7
+        out, lse = gdn.cross_attention(q, k, v, mask, return_lse=True)
+        want = gdn.cross_attention_backward(q, k, v, out, lse, g, mask)
+        nwant = gdn.qk_norm_rope_backward(q, None, None, None, g, None)
+        got = [torch.empty_like(x) for x in (q, k, v)]
+        ngot = [torch.empty_like(q), torch.empty(64, device="cuda")]
+        jobs.append((q, k, v, g, mask, out, lse, want, nwant, got, ngot))
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(j):
+        q, k, v, g, mask, out, lse, _, _, (dq, dk, dv), (dx, dw) = jobs[j]
+        for _ in range(200):
+            st = lib.gdn_cross_attention_backward(
+                rows(q), rows(k), rows(v), mask.data_ptr(), mask.stride(0), out.data_ptr(), lse.data_ptr(),
+                g.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), 1, q.shape[1], k.shape[1], 4, 2, 64, 0.125,
+                _lib.GDN_BF16, stream)
+            st = st or lib.gdn_qk_norm_rope_backward(
+                rows(q), None, None, None, None, rows(g), None, rows(dx), None, dw.data_ptr(), None, 1, q.shape[1], 4,
+                0, 64, 1e-6, _lib.GDN_BF16, stream)
+            if st:
+                failed.append(st)
+    for _ in range(3):
+        threads = [threading.Thread(target=work, args=(j,)) for j in (0, 1)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        assert not failed
+        for *_, want, nwant, got, ngot in jobs:
+            assert all(torch.equal(a, b) for a, b in zip(got, (want["dq"], want["dk"], want["dv"])))
+            assert torch.equal(ngot[0], nwant["dq"]) and torch.equal(ngot[1], nwant["dq_weight"])
