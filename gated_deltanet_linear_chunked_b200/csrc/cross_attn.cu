@@ -531,7 +531,7 @@ int cross_shape(const CrossCall& c, CrossParams* P) {
     P->tokens = c.Tq;
     P->qtiles = P->groups = 1;
     P->nsplit = few_splits(c.B, c.Hk, c.S);
-    P->full = P->nsplit > 1 ? 0 : units;
+    P->full = P->nsplit > kFewCluster ? 0 : units;  // (a cluster leaves no parts)
     return kFewRows;
   }
   P->tokens = kRows / P->G;

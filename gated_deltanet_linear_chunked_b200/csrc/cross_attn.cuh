@@ -29,7 +29,9 @@ struct CrossParams {
   unsigned* err;
 };
 
-// The kernel for at most kFewRows rows: CTAs of a (b, key head), and the launch.
+// The kernel for at most kFewRows rows: CTAs of a (b, key head), and the launch.  Up
+// to kFewCluster CTAs join by themselves, more leave parts as split units do.
+constexpr int kFewCluster = 8;
 int few_splits(int B, int Hk, int S);
 cudaError_t launch_cross_few(const CrossCall& c, const CrossParams& P);
 

@@ -11,9 +11,8 @@
 // spend its time on 112 rows that are none.  Masked keys are not copied: their rows
 // arrive as zeros (so that 0 * NaN never arises), their scores become -inf, and
 // groups without any seen key are skipped.  The warps of a CTA join in shared
-// memory, CTAs of one (b, key head) through gdn_cross_join_kernel.
-// 8 queries of 16 heads over 4096 keys of 4 heads, 128 wide, an eighth masked: see
-// the figures in the launch rule.
+// memory, up to eight CTAs of one (b, key head) in each other's as a cluster, more
+// through gdn_cross_join_kernel.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -36,6 +35,7 @@ struct FewParams {
   CrossParams c;
   const __nv_bfloat16 *q, *k, *v;
   long long q_bs, q_ts, k_bs, k_ts, v_bs, v_ts;
+  int cluster;  // the CTAs of a (b, key head) are one cluster
 };
 
 // Shared memory of a warp: kDepth x (K, V) groups of 16 rows of D features, 16-byte
@@ -74,6 +74,50 @@ gdn_cross_few_kernel(const __grid_constant__ FewParams F) {
     return (uint32_t)(r * kPieces + cc) * 16;
   };
 
+  const int workers = P.nsplit * kWarps, me = split * kWarps + warp;
+  const int groups = (P.S + kKeys - 1) / kKeys;
+  const uint8_t* mrow = P.mask ? P.mask + b * P.mask_bs : nullptr;
+  const __nv_bfloat16* kbase = F.k + b * F.k_bs + hk * D;
+  const __nv_bfloat16* vbase = F.v + b * F.v_bs + hk * D;
+  const uint32_t base = smem_u32(smem) + warp * L::warp;
+
+  // which of the 16 keys of group i are seen: the lane's mask byte, and the vote
+  auto look = [&](int i) -> bool {
+    const long long key = (long long)i * kKeys + (lane & 15);
+    return i < groups && key < P.S && (!mrow || mrow[key] != 0);
+  };
+  auto vote = [&](bool on) -> uint32_t { return __ballot_sync(~0u, on) & 0xFFFFu; };
+  auto fetch = [&](int i, uint32_t seen, int slot) {
+    if (seen) {
+      const uint32_t dk = base + slot * 2 * L::group, dv = dk + L::group;
+#pragma unroll
+      for (int x = 0; x < kKeys * kPieces; x += 32) {
+        const int y = x + lane, r = y / kPieces, c = y - r * kPieces;
+        if (kKeys * kPieces % 32 == 0 || y < kKeys * kPieces) {
+          const bool on = seen >> r & 1;
+          const long long key = on ? (long long)i * kKeys + r : 0;
+          copy16(dk + piece(r, c), kbase + key * F.k_ts + c * 8, on);
+          copy16(dv + piece(r, c), vbase + key * F.v_ts + c * 8, on);
+        }
+      }
+    }
+    copy_commit();
+  };
+
+  // seen bits of the groups in flight, and of the one to be fetched next: all their
+  // bytes are asked for before the first is waited for
+  uint32_t seen[kDepth], coming;
+  {
+    bool on[kDepth];
+#pragma unroll
+    for (int s = 0; s < kDepth; ++s) on[s] = look(me + s * workers);
+#pragma unroll
+    for (int s = 0; s < kDepth; ++s) seen[s] = vote(on[s]);
+    coming = seen[kDepth - 1];
+  }
+#pragma unroll
+  for (int s = 0; s < kDepth - 1; ++s) fetch(me + s * workers, seen[s], s);
+
   // Q as left operands, row r = token * G + head, straight from memory
   uint32_t qa[NK][4];
   {
@@ -93,50 +137,10 @@ gdn_cross_few_kernel(const __grid_constant__ FewParams F) {
       }
   }
 
-  const int workers = P.nsplit * kWarps, me = split * kWarps + warp;
-  const int groups = (P.S + kKeys - 1) / kKeys;
-  const uint8_t* mrow = P.mask ? P.mask + b * P.mask_bs : nullptr;
-  const __nv_bfloat16* kbase = F.k + b * F.k_bs + hk * D;
-  const __nv_bfloat16* vbase = F.v + b * F.v_bs + hk * D;
-  const uint32_t base = smem_u32(smem) + warp * L::warp;
-
-  // which of the 16 keys of group i are seen
-  auto seen_of = [&](int i) -> uint32_t {
-    const long long key = (long long)i * kKeys + (lane & 15);
-    const bool on = i < groups && key < P.S && (!mrow || mrow[key] != 0);
-    return __ballot_sync(~0u, on) & 0xFFFFu;
-  };
-  auto fetch = [&](int i, uint32_t seen, int slot) {
-    if (seen) {
-      const uint32_t dk = base + slot * 2 * L::group, dv = dk + L::group;
-#pragma unroll
-      for (int x = 0; x < kKeys * kPieces; x += 32) {
-        const int y = x + lane, r = y / kPieces, c = y - r * kPieces;
-        if (kKeys * kPieces % 32 == 0 || y < kKeys * kPieces) {
-          const bool on = seen >> r & 1;
-          const long long key = on ? (long long)i * kKeys + r : 0;
-          copy16(dk + piece(r, c), kbase + key * F.k_ts + c * 8, on);
-          copy16(dv + piece(r, c), vbase + key * F.v_ts + c * 8, on);
-        }
-      }
-    }
-    copy_commit();
-  };
-
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   float o[2 * NK][4];
 #pragma unroll
   for (int i = 0; i < 2 * NK; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-
-  // seen bits of the groups in flight, and of the one to be fetched next
-  uint32_t seen[kDepth];
-#pragma unroll
-  for (int s = 0; s < kDepth - 1; ++s) {
-    seen[s] = seen_of(me + s * workers);
-    fetch(me + s * workers, seen[s], s);
-  }
-  seen[kDepth - 1] = 0;
-  uint32_t coming = seen_of(me + (kDepth - 1) * workers);
 
   int slot = 0;
   for (int i = me; i < groups; i += workers) {
@@ -145,9 +149,10 @@ gdn_cross_few_kernel(const __grid_constant__ FewParams F) {
     const uint32_t next = coming;
     __syncwarp();  // every lane is done with that slot
     fetch(i + (kDepth - 1) * workers, next, into);
-    coming = seen_of(i + kDepth * workers);
+    const bool later = look(i + kDepth * workers);
     copy_wait<kDepth - 1>();
     __syncwarp();
+    coming = vote(later);
     const uint32_t now = seen[0];
 #pragma unroll
     for (int s = 0; s + 1 < kDepth; ++s) seen[s] = seen[s + 1];
@@ -227,9 +232,17 @@ gdn_cross_few_kernel(const __grid_constant__ FewParams F) {
     }
   }
   __syncthreads();
-  for (int x = threadIdx.x; x < rows * (D / 4); x += 32 * kWarps) {
-    const int r = x / (D / 4), f = (x - r * (D / 4)) * 4;
-    float top = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  // this CTA's rows: normalised, and their lse
+  constexpr int kMine = (16 * D / 4 + 32 * kWarps - 1) / (32 * kWarps);  // pieces of a thread
+  float4 mine[kMine];
+  float mine_lse[kMine];
+#pragma unroll
+  for (int p = 0; p < kMine; ++p) {
+    const int x = threadIdx.x + p * 32 * kWarps, r = x / (D / 4), f = (x - r * (D / 4)) * 4;
+    mine[p] = make_float4(0.f, 0.f, 0.f, 0.f);
+    mine_lse[p] = -INFINITY;
+    if (r >= rows) continue;
+    float top = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * 16 + r].x);
 #pragma unroll
@@ -238,27 +251,69 @@ gdn_cross_few_kernel(const __grid_constant__ FewParams F) {
       const float a = v.x > -INFINITY ? exp2f(v.x - top) : 0.f;
       const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) + (w * 16 + r) * D + f);
       sum += a * v.y;
-      acc[0] += a * y.x;
-      acc[1] += a * y.y;
-      acc[2] += a * y.z;
-      acc[3] += a * y.w;
+      mine[p].x += a * y.x;
+      mine[p].y += a * y.y;
+      mine[p].z += a * y.z;
+      mine[p].w += a * y.w;
     }
     const bool any = top > -INFINITY;
     const float inv = any ? 1.f / sum : 0.f;
-    const float lse = any ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-    if (P.nsplit > 1) {
-      const long long at = (long long)blockIdx.x * kFewRows + r;
-      if (f == 0) P.part_lse[at] = lse;
-      *reinterpret_cast<float4*>(P.part_o + at * D + f) =
-          make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
-    } else {
-      const int dt = r * P.gmul >> 16, head = hk * P.G + r - dt * P.G;
-      const long long at = ((long long)b * P.Tq + dt) * Hq + head;
-      if (f == 0 && P.lse) P.lse[((long long)b * Hq + head) * P.Tq + dt] = lse;
-      *reinterpret_cast<uint2*>(P.out + at * D + f) =
-          make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-    }
+    mine[p] = make_float4(mine[p].x * inv, mine[p].y * inv, mine[p].z * inv, mine[p].w * inv);
+    mine_lse[p] = any ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
   }
+  auto put = [&](int r, int f, const float4& v, float lse) {
+    const int dt = r * P.gmul >> 16, head = hk * P.G + r - dt * P.G;
+    if (f == 0 && P.lse) P.lse[((long long)b * Hq + head) * P.Tq + dt] = lse;
+    *reinterpret_cast<uint2*>(P.out + (((long long)b * P.Tq + dt) * Hq + head) * D + f) =
+        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  };
+  if (!F.cluster) {
+#pragma unroll
+    for (int p = 0; p < kMine; ++p) {
+      const int x = threadIdx.x + p * 32 * kWarps, r = x / (D / 4), f = (x - r * (D / 4)) * 4;
+      if (r >= rows) continue;
+      if (P.nsplit == 1) {
+        put(r, f, mine[p], mine_lse[p]);
+      } else {
+        const long long at = (long long)blockIdx.x * kFewRows + r;
+        if (f == 0) P.part_lse[at] = mine_lse[p];
+        *reinterpret_cast<float4*>(P.part_o + at * D + f) = mine[p];
+      }
+    }
+    return;
+  }
+  // The CTAs of a cluster share the (b, key head): each leaves its rows in its own
+  // shared memory, then takes every nsplit-th row and joins it from all of them.
+  float* left = reinterpret_cast<float*>(smem);  // [16][D] | lse [16]
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < kMine; ++p) {
+    const int x = threadIdx.x + p * 32 * kWarps, r = x / (D / 4), f = (x - r * (D / 4)) * 4;
+    if (r >= rows) continue;
+    *reinterpret_cast<float4*>(left + r * D + f) = mine[p];
+    if (f == 0) left[16 * D + r] = mine_lse[p];
+  }
+  cluster_sync();
+  const uint32_t at = smem_u32(left);
+  for (int x = threadIdx.x; x < (rows - split + P.nsplit - 1) / P.nsplit * (D / 4); x += 32 * kWarps) {
+    const int r = split + x / (D / 4) * P.nsplit, f = x % (D / 4) * 4;
+    float top = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < P.nsplit; ++s) top = fmaxf(top, cluster_load(cluster_addr(at + (16 * D + r) * 4, s)));
+    const bool any = top > -INFINITY;
+    for (int s = 0; any && s < P.nsplit; ++s) {
+      const float w = expf(cluster_load(cluster_addr(at + (16 * D + r) * 4, s)) - top);
+      const float4 v = cluster_load4(cluster_addr(at + (r * D + f) * 4, s));
+      sum += w;
+      acc.x += w * v.x;
+      acc.y += w * v.y;
+      acc.z += w * v.z;
+      acc.w += w * v.w;
+    }
+    const float inv = any ? 1.f / sum : 0.f;
+    put(r, f, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), any ? top + logf(sum) : -INFINITY);
+  }
+  cluster_sync();  // no CTA's shared memory goes while another reads it
 }
 
 template <int NK>
@@ -267,21 +322,25 @@ cudaError_t launch_nk(const FewParams& F, unsigned grid, cudaStream_t stream) {
   const cudaError_t e = allow_smem(gdn_cross_few_kernel<NK>, bytes);
   if (e != cudaSuccess) return e;
   ProfileScope ps(stream, kKernCrossFew);
-  return launch_after(gdn_cross_few_kernel<NK>, grid, 32 * kWarps, bytes, stream, F);
+  return launch_after_in_clusters(gdn_cross_few_kernel<NK>, grid, 32 * kWarps, bytes, stream,
+                                  F.cluster ? (unsigned)F.c.nsplit : 1u, F);
 }
 
 }  // namespace
 
-// Two CTAs an SM, each warp at least two groups of keys.
+// Two CTAs an SM, each warp at least two groups of keys; where that is up to ten
+// CTAs, eight, which are a cluster and join without a second kernel.
 int few_splits(int B, int Hk, int S) {
   const long long units = (long long)B * Hk;
   const long long most = ((S + kKeys - 1) / kKeys) / (2 * kWarps);
-  return (int)std::max<long long>(1, std::min<long long>(2 * num_sms() / units, most));
+  const int n = (int)std::max<long long>(1, std::min<long long>(2 * num_sms() / units, most));
+  return n > kFewCluster && n <= kFewCluster + 2 ? kFewCluster : n;
 }
 
 cudaError_t launch_cross_few(const CrossCall& c, const CrossParams& P) {
   FewParams F;
   F.c = P;
+  F.cluster = P.nsplit > 1 && P.nsplit <= kFewCluster;
   F.q = static_cast<const __nv_bfloat16*>(c.q.data);
   F.k = static_cast<const __nv_bfloat16*>(c.k.data);
   F.v = static_cast<const __nv_bfloat16*>(c.v.data);

@@ -211,19 +211,26 @@ cudaError_t allow_smem(K kernel, int bytes) {
 // Launches a kernel whose blocks may take their places before the kernel in front
 // of it on the stream has ended (it calls pdl_wait before it touches its results).
 template <typename... Params, typename... Args>
-cudaError_t launch_after(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
-                         cudaStream_t stream, Args... args) {
+cudaError_t launch_after_in_clusters(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
+                                     cudaStream_t stream, unsigned cluster, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {cluster, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
+                         cudaStream_t stream, Args... args) {
+  return launch_after_in_clusters(kernel, grid, block, smem, stream, 1u, args...);
 }
 
 // Streaming multiprocessors of the current device (cached per device).

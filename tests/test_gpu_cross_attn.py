@@ -146,6 +146,9 @@ CASES = [
     (2, 5, 100, 1, 3, 32, "none"),
     (1, 4, 17, 2, 4, 96, "holes"),
     (9, 1, 700, 40, 1, 112, "tail"),
+    (5, 1, 4100, 8, 3, 64, "holes"),      # a cluster of CTAs a key head, more rows than CTAs or fewer
+    (8, 2, 4100, 4, 8, 128, "tail"),
+    (1, 1, 300, 30, 1, 80, "none"),
 ]
 
 
