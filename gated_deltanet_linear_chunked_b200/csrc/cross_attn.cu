@@ -65,16 +65,18 @@ using namespace sm100;
 
 constexpr int kRows = 128;             // rows of a query tile, keys of a key tile
 constexpr int kHalf = kRows / 2;       // keys of a softmax thread
+constexpr int kSingleTiles = 16;       // key tiles up to which a CTA takes one query tile
+constexpr int kMaskTiles = 1024;       // key tiles that a CTA can list under a mask
 template <int NQ>  // query tiles of a CTA
 struct Roles {
   static constexpr int softmax_warps = 8 * NQ;  // two groups of four warps per query tile
   static constexpr int producer = softmax_warps, mma = producer + 1;
   static constexpr int threads = 32 * (mma + 1);
   static constexpr int slots = 2 * NQ;          // ring of K and V tiles
+  static constexpr int mask_tiles = NQ == 1 ? kSingleTiles : kMaskTiles;
 };
 constexpr uint32_t kTileCols = 256;    // TMEM columns of a tile: S (and P) [0, 128) | O [128, 128 + D)
 constexpr uint32_t kBlock = kRows * 128;  // one 64-feature block of a 128-row tile, bytes
-constexpr int kMaskTiles = 128;        // key tiles of one CTA under a mask, at most
 constexpr float kRescaleLog2 = 8.f;
 constexpr long long kDrainPolls = 1LL << 40;  // drains are bounded by the 2 s timer
 
@@ -87,8 +89,8 @@ struct CrossAux {
   int abort;
   int count;                       // key tiles to walk
   float row[NQ][2][kRows];    // a row's two halves exchange maxima, later sums
-  uint32_t bits[kMaskTiles * 4];   // seen keys of each of the CTA's tiles (under a mask)
-  uint8_t list[kMaskTiles];        // tiles with any
+  uint32_t bits[Roles<NQ>::mask_tiles * 4];  // seen keys of each of the CTA's tiles (under a mask)
+  uint16_t list[Roles<NQ>::mask_tiles];      // tiles with any
 };
 
 // Shared memory: Q tiles, the ring, the barriers and mask.
@@ -189,7 +191,7 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const bool any = t < kn && (aux.bits[4 * t] | aux.bits[4 * t + 1] | aux.bits[4 * t + 2] |
                                     aux.bits[4 * t + 3]) != 0;
         const uint32_t bal = __ballot_sync(~0u, any);
-        if (any) aux.list[n + __popc(bal & ((1u << lane) - 1))] = (uint8_t)t;
+        if (any) aux.list[n + __popc(bal & ((1u << lane) - 1))] = (uint16_t)t;
         n += __popc(bal);
       }
       if (lane == 0) aux.count = n;
@@ -493,7 +495,6 @@ gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int per, long long 
   const long long at = su * P.nsplit * per + ur;      // of split 0, then every `per`
   float top = -INFINITY;
   for (int s = 0; s < P.nsplit; ++s) top = fmaxf(top, P.part_lse[at + (long long)s * per]);
-  const bool any = top > -INFINITY;
   float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
   const int f = lane * 4;
 #pragma unroll 4
@@ -501,14 +502,16 @@ gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int per, long long 
     const long long x = at + (long long)s * per;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (f < P.D) v = *reinterpret_cast<const float4*>(P.part_o + x * P.D + f);
-    const float w = any ? expf(P.part_lse[x] - top) : 0.f;
-    const bool on = w > 0.f;  // a split that saw nothing left no part
+    const float part = P.part_lse[x];
+    const bool on = part != -INFINITY;  // a split that saw nothing left no part; NaN is passed on
+    const float w = on ? expf(part - top) : 0.f;
     sum += w;
     o[0] += on ? w * v.x : 0.f;
     o[1] += on ? w * v.y : 0.f;
     o[2] += on ? w * v.z : 0.f;
     o[3] += on ? w * v.w : 0.f;
   }
+  const bool any = sum != 0.f;
   const float inv = any ? 1.f / sum : 0.f;
   const int Hq = P.Hk * P.G;
   if (f < P.D)
@@ -542,7 +545,7 @@ int cross_shape(const CrossCall& c, CrossParams* P) {
   // and values that are loaded.  2640 queries, 20 heads of 112 (pair / single, us):
   // 128 keys 15.1 / 12.3, 300 22.0 / 19.7, 1024 45.6 / 44.9, 2640 78.2 / 77.2,
   // 7920 181 / 188.
-  const int nq = P->ntiles <= 16 ? 1 : 2;
+  const int nq = P->ntiles <= kSingleTiles ? 1 : 2;
   P->groups = (P->qtiles + nq - 1) / nq;
   const long long units = (long long)c.B * c.Hk * P->groups;
   const long long slots = num_sms() * (3 - nq);  // CTAs that run at a time

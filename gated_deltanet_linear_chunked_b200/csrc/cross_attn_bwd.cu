@@ -149,7 +149,7 @@ gdn_cross_stat_kernel(const __nv_bfloat16* out, const __nv_bfloat16* d_out, cons
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(~0u, d, o);
     const long long row = first + i * (kStatThreads / 16);
-    const bool on = lg[i] > -INFINITY;
+    const bool on = lg[i] != -INFINITY;  // (a NaN row's gradients are NaN)
     if (l == 0 && row < rows) {
       float* to = stat + row / kRows * (2 * kRows) + row % kRows;
       to[0] = on ? lg[i] * -1.4426950408889634f : -INFINITY;
@@ -163,7 +163,7 @@ gdn_cross_stat_kernel(const __nv_bfloat16* out, const __nv_bfloat16* d_out, cons
 // whose Q, dO or result are nothing), the others on the special-function unit, which
 // alone would take 1024 cycles for a tile, half of its products' time.
 __device__ __forceinline__ uint64_t exp2_pair(uint64_t x, int i) {
-  if ((i & 3) == 3) return exp2_poly2(x);
+  if ((i & 3) == 3) return exp2_poly2_nan(x);
   float a, e;
   f2_unpack(x, a, e);
   return f2_pack(ex2_approx(a), ex2_approx(e));

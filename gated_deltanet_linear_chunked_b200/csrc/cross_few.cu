@@ -184,7 +184,8 @@ gdn_cross_few_kernel(const __grid_constant__ FewParams F) {
         float mx = fmaxf(fmaxf(s0[2 * h], s0[2 * h + 1]), fmaxf(s1[2 * h], s1[2 * h + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-        const float mn = fmaxf(m[h], mx);  // finite: the group has a seen key
+        const float mn = fmaxf(m[h], mx);  // finite (the group has a seen key) unless all scores were NaN:
+                                           // then p and the row's sum are
         const float alpha = exp2f(m[h] - mn);
         m[h] = mn;
         const float p0 = exp2f(s0[2 * h] - mn), p1 = exp2f(s0[2 * h + 1] - mn);
@@ -248,7 +249,7 @@ gdn_cross_few_kernel(const __grid_constant__ FewParams F) {
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float2 v = ml[w * 16 + r];
-      const float a = v.x > -INFINITY ? exp2f(v.x - top) : 0.f;
+      const float a = v.y != 0.f ? exp2f(v.x - top) : 0.f;  // (a NaN sum counts)
       const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(smem) + (w * 16 + r) * D + f);
       sum += a * v.y;
       mine[p].x += a * y.x;
@@ -256,7 +257,7 @@ gdn_cross_few_kernel(const __grid_constant__ FewParams F) {
       mine[p].z += a * y.z;
       mine[p].w += a * y.w;
     }
-    const bool any = top > -INFINITY;
+    const bool any = sum != 0.f;
     const float inv = any ? 1.f / sum : 0.f;
     mine[p] = make_float4(mine[p].x * inv, mine[p].y * inv, mine[p].z * inv, mine[p].w * inv);
     mine_lse[p] = any ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
@@ -300,9 +301,9 @@ gdn_cross_few_kernel(const __grid_constant__ FewParams F) {
     float top = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s = 0; s < P.nsplit; ++s) top = fmaxf(top, cluster_load(cluster_addr(at + (16 * D + r) * 4, s)));
-    const bool any = top > -INFINITY;
-    for (int s = 0; any && s < P.nsplit; ++s) {
-      const float w = expf(cluster_load(cluster_addr(at + (16 * D + r) * 4, s)) - top);
+    for (int s = 0; s < P.nsplit; ++s) {
+      const float x = cluster_load(cluster_addr(at + (16 * D + r) * 4, s));
+      const float w = x != -INFINITY ? expf(x - top) : 0.f;
       const float4 v = cluster_load4(cluster_addr(at + (r * D + f) * 4, s));
       sum += w;
       acc.x += w * v.x;
@@ -310,6 +311,7 @@ gdn_cross_few_kernel(const __grid_constant__ FewParams F) {
       acc.z += w * v.z;
       acc.w += w * v.w;
     }
+    const bool any = sum != 0.f;  // (NaN counts)
     const float inv = any ? 1.f / sum : 0.f;
     put(r, f, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), any ? top + logf(sum) : -INFINITY);
   }

@@ -248,6 +248,41 @@ def test_masked_places_hold_anything(Tq, G):
     assert (got[2]["dq"][-1] == 0).all()
 
 
+@pytest.mark.parametrize("Tq,S,G", [(1, 40, 4), (1, 1000, 4), (1, 5000, 4), (300, 300, 1), (300, 4000, 1)])
+def test_nan_is_not_hidden(Tq, S, G):
+    """A query row of NaN gives NaN for that row, whichever way its parts are joined,
+    and leaves the others' bits; a seen key of NaN reaches every row."""
+    c = Case(1, Tq, S, 2, G, 64, "none", 17)
+    out, lse, grads = both(c)
+    t, h = Tq // 2, G // 2
+    q = c.q.clone()
+    q[0, t, h] = float("nan")
+    o, l = gdn.cross_attention(q, c.k, c.v, return_lse=True)
+    g = gdn.cross_attention_backward(q, c.k, c.v, o, l, c.g)
+    other = torch.ones(Tq, 2 * G, dtype=torch.bool, device="cuda")
+    other[t, h] = False
+    assert o[0, t, h].isnan().all() and l[0, h, t].isnan()
+    assert torch.equal(o[0][other], out[0][other]) and torch.equal(l[0].T[other], lse[0].T[other])
+    assert g["dq"][0, t, h].isnan().all() and torch.equal(g["dq"][0][other], grads["dq"][0][other])
+    for n in ("dk", "dv"):
+        assert g[n][0, :, 0].isnan().all() and torch.equal(g[n][0, :, 1], grads[n][0, :, 1])
+    k = c.k.clone()
+    k[0, S // 2, 1] = float("nan")
+    o, l = gdn.cross_attention(c.q, k, c.v, return_lse=True)
+    g = gdn.cross_attention_backward(c.q, k, c.v, o, l, c.g)
+    assert o[0, :, G:].isnan().all() and l[0, G:].isnan().all() and torch.equal(o[0, :, :G], out[0, :, :G])
+    assert g["dq"][0, :, G:].isnan().all() and g["dk"][0, :, 1].isnan().all() and g["dv"][0, :, 1].isnan().all()
+    assert torch.equal(g["dk"][0, :, 0], grads["dk"][0, :, 0])
+
+
+@pytest.mark.parametrize("S", [131072, 140001])
+def test_long_mask(S):
+    """As many masked keys as one CTA lists, and more (each CTA then takes a part)."""
+    c = Case(2, 40, S, 1, 1, 16, "holes", S)
+    out, lse = gdn.cross_attention(c.q, c.k, c.v, c.mask, return_lse=True)
+    c.check(out, lse)
+
+
 def test_no_keys():
     q = torch.randn(2, 5, 4, 32, device="cuda").bfloat16()
     k = torch.empty(2, 0, 2, 32, device="cuda").bfloat16()
