@@ -20,7 +20,8 @@ __all__ = [*_API, "GDNError", "workloads"]
 def __getattr__(name):
     if name in _API:
         from . import api
-        return getattr(api, name)
+        globals()[name] = got = getattr(api, name)  # later calls find it here
+        return got
     if name == "GDNError":
         from ._lib import GDNError
         return GDNError
