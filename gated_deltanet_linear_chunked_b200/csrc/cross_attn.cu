@@ -39,7 +39,9 @@
 // scores were ready at the same time and their softmaxes ran together, the tensor
 // core waiting (7920 keys, 7 x 256 queries, 20 heads of 112: 186 us).
 // Masked keys: a CTA first reads its batch row's mask into one bit per key and
-// lists the key tiles that have any, so tiles without are never loaded; in tiles
+// lists the key tiles that have any, so tiles without are never loaded (but for the
+// first where there are few: it is on its way before the mask is known, which took
+// the chunk's 300 keys under a mask from 18.9 to 18.0 us); in tiles
 // with some, scores of masked keys become -inf whatever they were, and the masked
 // rows of V are cleared in shared memory, since 0 * NaN would reach the sum.
 // Few query tiles and many keys: the key tiles are split over CTAs, each leaves
@@ -73,11 +75,11 @@ struct Roles {
   static constexpr int producer = softmax_warps, mma = producer + 1;
   static constexpr int threads = 32 * (mma + 1);
   static constexpr int slots = 2 * NQ;          // ring of K and V tiles
-  static constexpr int mask_tiles = NQ == 1 ? kSingleTiles : kMaskTiles;
 };
 constexpr uint32_t kTileCols = 256;    // TMEM columns of a tile: S (and P) [0, 128) | O [128, 128 + D)
 constexpr uint32_t kBlock = kRows * 128;  // one 64-feature block of a 128-row tile, bytes
 constexpr float kRescaleLog2 = 8.f;
+constexpr float kLowest = -3e38f;      // the running maximum of no scores: from it, p of a masked key is 0
 constexpr long long kDrainPolls = 1LL << 40;  // drains are bounded by the 2 s timer
 
 template <int NQ>
@@ -89,8 +91,7 @@ struct CrossAux {
   int abort;
   int count;                       // key tiles to walk
   float row[NQ][2][kRows];    // a row's two halves exchange maxima, later sums
-  uint32_t bits[Roles<NQ>::mask_tiles * 4];  // seen keys of each of the CTA's tiles (under a mask)
-  uint16_t list[Roles<NQ>::mask_tiles];      // tiles with any
+  uint16_t list[NQ == 1 ? kSingleTiles : kMaskTiles];  // under a mask: the tiles with any seen key
 };
 
 // Shared memory: Q tiles, the ring, the barriers and mask.
@@ -100,7 +101,9 @@ struct CrossLayout {
   static constexpr uint32_t q = 0;
   static constexpr uint32_t ring = NQ * tile;
   static constexpr uint32_t aux = ring + Roles<NQ>::slots * tile;
-  static constexpr uint32_t total = aux + (uint32_t)sizeof(CrossAux<NQ>);
+  // under a mask: the seen keys of each of the CTA's tiles, one bit each
+  static constexpr uint32_t mask = aux + ((uint32_t)sizeof(CrossAux<NQ>) + 15) / 16 * 16;
+  static constexpr uint32_t mask_tile = 4 * sizeof(uint32_t);
 };
 
 // 32 scores of a row, those of masked keys -inf whatever they were.
@@ -122,8 +125,10 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   extern __shared__ __align__(1024) uint8_t smem[];
   const int D = P.D;
   constexpr int nb = NB, kSlots = Roles<NQ>::slots;
+  constexpr bool kEarly = NQ == 1;  // few tiles: the first is loaded before the mask is known
   using L = CrossLayout<NB, NQ>;
   CrossAux<NQ>& aux = *reinterpret_cast<CrossAux<NQ>*>(smem + L::aux);
+  uint32_t* const mask_bits = reinterpret_cast<uint32_t*>(smem + L::mask);
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;  // uniform
   // unit: (b * Hk + hk) * groups + group
   const bool whole = blockIdx.x < P.full;
@@ -136,6 +141,15 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const int k0 = split * P.per_split;                               // key tiles k0 .. k0 + kn - 1
   const int kn = whole ? P.ntiles : min(P.per_split, P.ntiles - k0);
   volatile int* abort_flag = &aux.abort;
+  // ring item i: K (even i) or V (odd i) of listed tile i / 2
+  auto slot_ptr = [&](int i) { return smem + L::ring + (i % kSlots) * L::tile; };
+  auto load_item = [&](int i, int tile) {
+    uint64_t* bar = &aux.full[i % kSlots];
+    mbar_arrive_expect_tx(bar, L::tile);
+    for (int c = 0; c < nb; ++c)
+      tma_load_5d(slot_ptr(i) + c * kBlock, i & 1 ? &tm_v : &tm_k, bar, c * 64, 0, tile * kRows, hk,
+                  b * (i & 1 ? P.vb : P.kb));
+  };
 
   if (warp == Roles<NQ>::producer && lane == 0) {
     prefetch_map(&tm_q);
@@ -164,6 +178,11 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       for (int c = 0; c < nb; ++c)
         tma_load_5d(smem + L::q + g * L::tile + c * kBlock, &tm_q, &aux.q_full, c * 64, 0,
                     (tile0 + g) * P.tokens, hk, b * P.qb);
+    // and so is the first key tile
+    if (kEarly && kn > 0) {
+      load_item(0, k0);
+      load_item(1, k0);
+    }
   }
   if (warp == Roles<NQ>::mma) {
     tmem_alloc(&aux.tmem, kTileCols * NQ);
@@ -177,7 +196,7 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       if (warp >= Roles<NQ>::softmax_warps) break;
       const long long key = (long long)(k0 * 4 + w) * 32 + lane;
       const uint32_t bits = __ballot_sync(~0u, key < P.S && mrow[key] != 0);
-      if (lane == 0) aux.bits[w] = bits;
+      if (lane == 0) mask_bits[w] = bits;
     }
   }
   tc_fence_before_sync();
@@ -186,15 +205,18 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   if (P.mask) {
     if (warp == 0) {
       int n = 0;
+      bool seen = false;
       for (int t0 = 0; t0 < kn; t0 += 32) {
         const int t = t0 + lane;
-        const bool any = t < kn && (aux.bits[4 * t] | aux.bits[4 * t + 1] | aux.bits[4 * t + 2] |
-                                    aux.bits[4 * t + 3]) != 0;
+        bool any = t < kn && (mask_bits[4 * t] | mask_bits[4 * t + 1] | mask_bits[4 * t + 2] |
+                              mask_bits[4 * t + 3]) != 0;
+        seen = __any_sync(~0u, any) || seen;
+        any = any || (kEarly && t == 0);  // it is there already
         const uint32_t bal = __ballot_sync(~0u, any);
         if (any) aux.list[n + __popc(bal & ((1u << lane) - 1))] = (uint16_t)t;
         n += __popc(bal);
       }
-      if (lane == 0) aux.count = n;
+      if (lane == 0) aux.count = seen ? n : 0;
     }
     __syncthreads();
   }
@@ -206,25 +228,18 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     *abort_flag = 1;
     atomicOr(P.err, kErrTimeout);
   };
-  // ring item i: K (even i) or V (odd i) of listed tile i / 2
-  auto slot_ptr = [&](int i) { return smem + L::ring + (i % kSlots) * L::tile; };
   auto wait_full = [&](int i) { return mbar_wait(&aux.full[i % kSlots], (i / kSlots) & 1, P.limit); };
 
   if (warp == Roles<NQ>::producer) {
     if (lane == 0) {
-      int issued = 0;
-      for (int i = 0; i < 2 * n; ++i) {
+      int issued = kEarly && kn > 0 ? 2 : 0;
+      for (int i = issued; i < 2 * n; ++i) {
         if (*abort_flag) break;
         if (i >= kSlots && !mbar_wait(&aux.empty[i % kSlots], (i / kSlots - 1) & 1, P.limit)) {
           fail();
           break;
         }
-        const int tile = k0 + (masked ? aux.list[i / 2] : i / 2);
-        uint64_t* bar = &aux.full[i % kSlots];
-        mbar_arrive_expect_tx(bar, L::tile);
-        for (int c = 0; c < nb; ++c)
-          tma_load_5d(slot_ptr(i) + c * kBlock, i & 1 ? &tm_v : &tm_k, bar, c * 64, 0, tile * kRows, hk,
-                      b * (i & 1 ? P.vb : P.kb));
+        load_item(i, k0 + (masked ? aux.list[i / 2] : i / 2));
         ++issued;
       }
       // every load has landed before shared memory goes
@@ -297,7 +312,7 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int t = tok0 + (r * P.gmul >> 16), head = hk * P.G + r - (r * P.gmul >> 16) * P.G;
     const bool row = r < P.tokens * P.G && t < P.Tq;
     __nv_bfloat16* const out0 = P.out + (((long long)b * P.Tq + tok0) * Hq + hk * P.G) * D;
-    float m_run = -INFINITY, l_run = 0.f;
+    float m_run = kLowest, l_run = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       bool got = __all_sync(~0u, *abort_flag == 0 && mbar_wait(&aux.s_full[g], j & 1, P.limit));
@@ -306,8 +321,8 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       uint32_t bits[2] = {~0u, ~0u};
       if (masked) {
         const int w = 4 * aux.list[j] + 2 * half;
-        bits[0] = aux.bits[w];
-        bits[1] = aux.bits[w + 1];
+        bits[0] = mask_bits[w];
+        bits[1] = mask_bits[w + 1];
       } else if (j == n - 1) {
         const int left = P.S - (k0 + j) * kRows - kHalf * half;
 #pragma unroll
@@ -334,20 +349,20 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         scores(tS + kHalf * half + 32 * c, bits[c], s);
         float acc[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = fmax3(s[e], s[e + 4], s[e + 8]);
+        for (int e = 0; e < 4; ++e) acc[e] = fmax3_nan(s[e], s[e + 4], s[e + 8]);
 #pragma unroll
         for (int i = 12; i + 8 <= 28; i += 8)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[e] = fmax3(acc[e], s[i + e], s[i + 4 + e]);
+          for (int e = 0; e < 4; ++e) acc[e] = fmax3_nan(acc[e], s[i + e], s[i + 4 + e]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = fmaxf(acc[e], s[28 + e]);
-        mx = fmaxf(mx, fmaxf(fmax3(acc[0], acc[1], acc[2]), acc[3]));
+        for (int e = 0; e < 4; ++e) acc[e] = fmax_nan(acc[e], s[28 + e]);
+        mx = fmax_nan(mx, fmax_nan(fmax3_nan(acc[0], acc[1], acc[2]), acc[3]));
       }
       mx *= P.scale_log2;
       // does any row of the tile need a larger maximum (or has a wait given up)?
       // One barrier with a vote; the rows' halves meet in shared memory only then.
       float alpha = 1.f;
-      const bool quiet = got && !(mx > m_run + kRescaleLog2);
+      const bool quiet = got && (mx <= m_run + kRescaleLog2 || !row);
       if (!named_barrier_and(1 + g, 2 * kRows, quiet)) {
         aux.row[g][half][r] = mx;
         if (!named_barrier_and(1 + g, 2 * kRows, got)) {
@@ -355,7 +370,10 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           ok = false;
           break;
         }
-        mx = fmaxf(mx, aux.row[g][half ^ 1][r]);
+        mx = fmax_nan(mx, aux.row[g][half ^ 1][r]);
+        // a score that is no number, or infinite, makes the row's sum and so its result
+        // none (exp2_poly2_fine, which takes some of the keys, loses it)
+        if (!(mx < INFINITY)) l_run = NAN;
         const bool grow = mx > m_run + kRescaleLog2;
         if (grow) {
           alpha = ex2_approx(m_run - mx);  // 0 on the first tile
@@ -494,7 +512,8 @@ gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int per, long long 
   if (r >= P.tokens * P.G || t >= P.Tq) return;       // no row
   const long long at = su * P.nsplit * per + ur;      // of split 0, then every `per`
   float top = -INFINITY;
-  for (int s = 0; s < P.nsplit; ++s) top = fmaxf(top, P.part_lse[at + (long long)s * per]);
+  for (int s = 0; s < P.nsplit; ++s) top = fmax_nan(top, P.part_lse[at + (long long)s * per]);
+  const bool any = top != -INFINITY;  // NaN is passed on
   float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
   const int f = lane * 4;
 #pragma unroll 4
@@ -502,16 +521,14 @@ gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int per, long long 
     const long long x = at + (long long)s * per;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (f < P.D) v = *reinterpret_cast<const float4*>(P.part_o + x * P.D + f);
-    const float part = P.part_lse[x];
-    const bool on = part != -INFINITY;  // a split that saw nothing left no part; NaN is passed on
-    const float w = on ? expf(part - top) : 0.f;
+    const float w = any ? expf(P.part_lse[x] - top) : 0.f;
+    const bool on = w > 0.f;  // a split that saw nothing left no part
     sum += w;
     o[0] += on ? w * v.x : 0.f;
     o[1] += on ? w * v.y : 0.f;
     o[2] += on ? w * v.z : 0.f;
     o[3] += on ? w * v.w : 0.f;
   }
-  const bool any = sum != 0.f;
   const float inv = any ? 1.f / sum : 0.f;
   const int Hq = P.Hk * P.G;
   if (f < P.D)
@@ -561,6 +578,7 @@ int cross_shape(const CrossCall& c, CrossParams* P) {
   }
   P->per_split = (int)std::max<long long>(1, (P->ntiles + n - 1) / n);
   P->nsplit = std::max(1, (P->ntiles + P->per_split - 1) / P->per_split);
+  P->most = P->full ? P->ntiles : P->per_split;
   return nq * kRows;
 }
 
@@ -575,8 +593,10 @@ cudaError_t launch_nb(unsigned grid, cudaStream_t stream, const CUtensorMap& mq,
   // more than a third (half) of an SM's shared memory: two CTAs (one) per SM, as
   // many as tensor memory has columns for
   constexpr int least = NQ == 1 ? 80 * 1024 : 116 * 1024;
-  constexpr int bytes = CrossLayout<NB, NQ>::total > least ? CrossLayout<NB, NQ>::total : least;
-  const cudaError_t e = allow_smem(gdn_cross_kernel<NB, NQ>, bytes);
+  using L = CrossLayout<NB, NQ>;
+  const int bytes = std::max<int>(least, L::mask + (P.mask ? P.most * L::mask_tile : 0));
+  constexpr int most = std::max<int>(least, L::mask + (NQ == 1 ? kSingleTiles : kMaskTiles) * L::mask_tile);
+  const cudaError_t e = allow_smem(gdn_cross_kernel<NB, NQ>, most);
   if (e != cudaSuccess) return e;
   ProfileScope ps(stream, kKernCross);
   return launch_after(gdn_cross_kernel<NB, NQ>, grid, Roles<NQ>::threads, bytes, stream, mq, mk, mv, P);

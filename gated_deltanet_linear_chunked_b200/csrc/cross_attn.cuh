@@ -17,6 +17,7 @@ struct CrossParams {
   int ntiles;            // key tiles
   unsigned full;         // units that one CTA each takes whole; those behind them ...
   int nsplit, per_split; // ... are split along the keys: CTAs of a unit, tiles of each
+  int most;              // key tiles of a CTA, at most
   int qb, kb, vb;        // batch coordinate factors: 0 for a broadcast batch
   const uint8_t* mask;
   long long mask_bs;

@@ -163,7 +163,7 @@ gdn_cross_stat_kernel(const __nv_bfloat16* out, const __nv_bfloat16* d_out, cons
 // whose Q, dO or result are nothing), the others on the special-function unit, which
 // alone would take 1024 cycles for a tile, half of its products' time.
 __device__ __forceinline__ uint64_t exp2_pair(uint64_t x, int i) {
-  if ((i & 3) == 3) return exp2_poly2_nan(x);
+  if ((i & 3) == 3) return exp2_poly2<true>(x);
   float a, e;
   f2_unpack(x, a, e);
   return f2_pack(ex2_approx(a), ex2_approx(e));

@@ -300,10 +300,10 @@ gdn_cross_few_kernel(const __grid_constant__ FewParams F) {
     const int r = split + x / (D / 4) * P.nsplit, f = x % (D / 4) * 4;
     float top = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < P.nsplit; ++s) top = fmaxf(top, cluster_load(cluster_addr(at + (16 * D + r) * 4, s)));
-    for (int s = 0; s < P.nsplit; ++s) {
-      const float x = cluster_load(cluster_addr(at + (16 * D + r) * 4, s));
-      const float w = x != -INFINITY ? expf(x - top) : 0.f;
+    for (int s = 0; s < P.nsplit; ++s) top = fmax_nan(top, cluster_load(cluster_addr(at + (16 * D + r) * 4, s)));
+    const bool any = top != -INFINITY;  // NaN is passed on
+    for (int s = 0; any && s < P.nsplit; ++s) {
+      const float w = expf(cluster_load(cluster_addr(at + (16 * D + r) * 4, s)) - top);
       const float4 v = cluster_load4(cluster_addr(at + (r * D + f) * 4, s));
       sum += w;
       acc.x += w * v.x;
@@ -311,7 +311,6 @@ gdn_cross_few_kernel(const __grid_constant__ FewParams F) {
       acc.z += w * v.z;
       acc.w += w * v.w;
     }
-    const bool any = sum != 0.f;  // (NaN counts)
     const float inv = any ? 1.f / sum : 0.f;
     put(r, f, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), any ? top + logf(sum) : -INFINITY);
   }

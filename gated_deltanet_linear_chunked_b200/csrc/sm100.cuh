@@ -477,6 +477,18 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return r;
 }
 
+// The same, NaN if any of them is.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // 2^x on the special-function unit (the PTX ISA's ex2.approx: flush-to-zero,
 // 2^-inf = 0).
 __device__ __forceinline__ float ex2_approx(float x) {
@@ -517,11 +529,14 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
 // fitted here to 2^f on [-1/2, 1/2] by weighted least squares in relative
 // error (Lawson's iteration); its largest relative error is 7.5e-5, far under
 // the bf16 rounding of P.  2^n enters by adding n to the exponent field.
-// Inputs are clamped at -125 (2^-125 stands for 0, as ex2 gives for -inf).
+// Inputs are clamped at -125 (2^-125 stands for 0, as ex2 gives for -inf).  NaN gives
+// 2^-125, or, if kNan, 3.4e38, infinity in bf16 (n of NaN being -1).
+template <bool kNan = false>
 __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x) {
   float x0, x1;
   f2_unpack(x, x0, x1);
-  const uint64_t xc = f2_pack(fmaxf(x0, -125.f), fmaxf(x1, -125.f));
+  const uint64_t xc = kNan ? f2_pack(fmax_nan(x0, -125.f), fmax_nan(x1, -125.f))
+                           : f2_pack(fmaxf(x0, -125.f), fmaxf(x1, -125.f));
   const uint64_t magic = f2_pack(12582912.f, 12582912.f);
   const uint64_t t = f2_add(xc, magic);                        // n in the low bits
   const uint64_t n = f2_add(t, f2_pack(-12582912.f, -12582912.f));
@@ -537,40 +552,13 @@ __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x) {
                  __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23)));
 }
 
-// The larger of each of a pair and b; NaN stays NaN.
-__device__ __forceinline__ uint64_t f2_max_nan(uint64_t a, float b) {
-  float x, y;
-  f2_unpack(a, x, y);
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(b));
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(y) : "f"(b));
-  return f2_pack(x, y);
-}
-// p times 2^n, n in the low bits of t.  Added to the exponent n would make a number
-// of NaN; the product keeps it.
-__device__ __forceinline__ uint64_t f2_scale2(uint64_t p, uint64_t t) {
-  float t0, t1;
-  f2_unpack(t, t0, t1);
-  return f2_mul(p, f2_pack(__uint_as_float((__float_as_uint(t0) << 23) + 0x3F800000u),
-                           __uint_as_float((__float_as_uint(t1) << 23) + 0x3F800000u)));
-}
-
-// exp2_poly2 that passes NaN on.
-__device__ __forceinline__ uint64_t exp2_poly2_nan(uint64_t x) {
-  const uint64_t xc = f2_max_nan(x, -125.f);
-  const uint64_t t = f2_add(xc, f2_pack(12582912.f, 12582912.f));
-  const uint64_t n = f2_add(t, f2_pack(-12582912.f, -12582912.f));
-  const uint64_t f = f2_fma(n, f2_pack(-1.f, -1.f), xc);
-  uint64_t p = f2_fma(f2_pack(0.0551716648f, 0.0551716648f), f, f2_pack(0.2426111251f, 0.2426111251f));
-  p = f2_fma(p, f, f2_pack(0.6932609677f, 0.6932609677f));
-  p = f2_fma(p, f, f2_pack(0.9999280572f, 0.9999280572f));
-  return f2_scale2(p, t);
-}
-
 // The same with a polynomial of degree 5, fitted the same way: largest relative
 // error 7.5e-8, 2.0e-7 as evaluated in fp32.  For sums of exponentials that leave
 // as fp32 (a log-sum-exp), which the shorter one would limit to 1e-5.
 __device__ __forceinline__ uint64_t exp2_poly2_fine(uint64_t x) {
-  const uint64_t xc = f2_max_nan(x, -125.f);
+  float x0, x1;
+  f2_unpack(x, x0, x1);
+  const uint64_t xc = f2_pack(fmaxf(x0, -125.f), fmaxf(x1, -125.f));
   const uint64_t t = f2_add(xc, f2_pack(12582912.f, 12582912.f));  // n in the low bits
   const uint64_t n = f2_add(t, f2_pack(-12582912.f, -12582912.f));
   const uint64_t f = f2_fma(n, f2_pack(-1.f, -1.f), xc);           // x - n
@@ -579,7 +567,11 @@ __device__ __forceinline__ uint64_t exp2_poly2_fine(uint64_t x) {
   p = f2_fma(p, f, f2_pack(0.2402212024f, 0.2402212024f));
   p = f2_fma(p, f, f2_pack(0.693146944f, 0.693146944f));
   p = f2_fma(p, f, f2_pack(1.000000119f, 1.000000119f));
-  return f2_scale2(p, t);
+  float p0, p1, t0, t1;
+  f2_unpack(p, p0, p1);
+  f2_unpack(t, t0, t1);
+  return f2_pack(__uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23)),
+                 __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23)));
 }
 
 // 32 rows of a warp to global memory: lane l holds N 16-byte pieces of row l, and
