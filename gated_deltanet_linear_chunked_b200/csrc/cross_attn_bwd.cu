@@ -257,6 +257,8 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
     tmem_alloc(&aux.tmem, 512);
     tmem_relinquish();
   }
+  pdl_wait();  // the row statistics and mask lists
+  pdl_trigger();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -499,13 +501,15 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
     tmem_alloc(&aux.tmem, 512);
     tmem_relinquish();
   }
-  const uint4 keys = seen_keys(P, b, kt);
   // rows of Q and dO past the packed ones are never loaded, and a product runs
   // over them: they have to be numbers
   for (int i = P.tokens * P.G * 8 + tid; i < kRows * 8; i += kThreads)
     for (int c = 0; c < kRing * NB; ++c)
       *reinterpret_cast<uint4*>(smem + L::ring + c * kBlock + i * 16) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
+  pdl_wait();  // the row statistics and mask bits
+  pdl_trigger();
+  const uint4 keys = seen_keys(P, b, kt);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -736,8 +740,6 @@ gdn_cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     prefetch_map(&tm_k);
     prefetch_map(&tm_v);
   }
-  pdl_wait();  // the row statistics and mask lists
-  pdl_trigger();
   if (blockIdx.x < P.dkv_blocks)
     dkv_tile<NB>(smem, blockIdx.x, tm_q, tm_do, tm_k, tm_v, P);
   else
