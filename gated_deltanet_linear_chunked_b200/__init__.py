@@ -1,7 +1,8 @@
 """B200-native chunked Gated DeltaNet (GDN) scan, and the sink + sliding-window
-softmax attention of the same hybrid DiT's softmax blocks.
+softmax attention of the same hybrid DiT's softmax blocks, with the operators
+around it: rotary positions, q/k norms, the attention to an encoder's states.
 
-The scan runs in ``libgdn.so`` (hand-written CUDA for sm_100a, C ABI in
+All of it runs in ``libgdn.so`` (hand-written CUDA for sm_100a, C ABI in
 ``include/gdn.h``); this package is its thin torch binding plus the seeded
 workload generators.  Importing the package does not load CUDA; the library
 is loaded on the first call.

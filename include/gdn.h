@@ -407,7 +407,8 @@ GDN_API gdn_status gdn_qk_norm_rope_backward(const gdn_rows* q, const gdn_rows* 
  * (or S = 0) has out = 0 and lse = -infinity.  Values in masked rows of k and v
  * (NaN and infinities among them) do not reach any result.
  *
- *   q [B, Tq, Hq, D], k, v [B, S, Hk, D]   bf16 views as for gdn_qk_norm_rope
+ *   q [B, Tq, Hq, D], k, v [B, S, Hk, D]   bf16 views as for gdn_qk_norm_rope,
+ *                          strides at most 2^36, token strides not 0
  *                          (batch stride 0: one batch row's states for all)
  *   key_mask               [B, S] bytes, nonzero: the key is seen; NULL: all are;
  *                          mask_batch_stride bytes between rows (0: one row for all)
