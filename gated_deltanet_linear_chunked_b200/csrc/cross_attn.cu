@@ -46,6 +46,10 @@
 // rows of V are cleared in shared memory, since 0 * NaN would reach the sum.
 // Few query tiles and many keys: the key tiles are split over CTAs, each leaves
 // its normalised fp32 part and its lse, and gdn_cross_join_kernel joins them.
+// 2640 queries over 7920 keys, 20 heads of 112: 183 us, 1025 TFLOP/s, tensor core 53%
+// and special-function unit 46% busy; what is left is the hand-offs between them, and
+// when repeated the power limit.  Over 300 keys 19.7 us, the chain of a CTA's three
+// tiles, twice.
 // Every wait is bounded; one that gives up sets the error word and the CTA drains
 // its copies and MMAs before it frees TMEM.
 #include <cuda.h>
@@ -495,7 +499,8 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 }
 
 // Joins the splits: out = sum_i w_i o_i with w_i = e^(lse_i - lse).  A warp per
-// row of the split units, four features a lane.
+// row of the split units, four features a lane.  A stream over the parts: those of
+// the case above, 72 units in two, 17 MB written and read, about 11 us.
 constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads)
 gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int per, long long rows) {

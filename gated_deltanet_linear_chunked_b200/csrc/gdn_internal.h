@@ -182,8 +182,7 @@ bool make_tile_map(CUtensorMap* m, const void* base, int nb, int T, int H, int D
 // A [nb, T, Hk * G, D] bf16 view (strides in elements) as 5-D (D, G, T, Hk, nb):
 // one box is 64 features of the G heads that share a key head, box_tokens
 // tokens of them, and lands in shared memory as rows token * G + head of 128
-// bytes with the 128-byte swizzle.  Features past D and tokens past T read as 0
-// and are not stored.
+// bytes with the 128-byte swizzle.  Features past D and tokens past T read as 0.
 bool make_heads_map(CUtensorMap* m, const void* base, int nb, int T, int Hk, int G, int D,
                     long long batch_stride, long long token_stride, int box_tokens);
 

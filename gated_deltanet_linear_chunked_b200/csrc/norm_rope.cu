@@ -21,6 +21,11 @@
 // and keeps them for its heads, two of which are always on their way from memory.
 // Angles are formed in 64 bits and reduced to a fraction of a turn there: a
 // position of 10^6 has an angle whose 32-bit rounding is already 0.06.
+// Bound by memory: 65536 tokens, 16 + 4 heads of 128 in fp32 219 us (6.1 TB/s), 2640
+// tokens, 20 + 20 heads of 112 in bf16 10.0 us (4.7 TB/s, two waves of blocks).  The
+// gradients, which read twice as much and hold the weights' sums in registers, are
+// bound by latency at 16 warps an SM: the same 18.5 us (3.8 TB/s), 4 x 4096 tokens,
+// 16 + 4 heads of 128 in bf16 61 us (4.1 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -368,7 +373,8 @@ gdn_norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
 // The gradients.  Blocks are persistent: each walks its side's token tiles with
 // a stride of the side's blocks, so that the weight's gradient leaves as one
 // partial row per block, which gdn_norm_rope_reduce_kernel adds up in a fixed
-// order (no atomics: the same call gives the same bits).
+// order (no atomics: the same call gives the same bits).  Two heads on their way
+// instead of one took longer (the chunk's gradients 23.1 us for 21.1 in rotation).
 template <typename T, int G, bool interleaved>
 __global__ void __launch_bounds__(kThreads, 2)
 gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
@@ -476,7 +482,8 @@ gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
 }
 
 // dw[side][f] = sum over the side's blocks of partial[block][f]: one block per
-// (side, 16 features), 16 lanes across features and 32 rows at a time.
+// (side, 16 features), 16 lanes across features and 32 rows at a time.  About 2 us,
+// most of them its launch.
 constexpr int kRedCols = 16, kRedRows = 32;
 __global__ void __launch_bounds__(kRedCols * kRedRows)
 gdn_norm_rope_reduce_kernel(const float* partial, unsigned blocks, int D, float* dw0, float* dw1) {
