@@ -502,48 +502,85 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   }
 }
 
-// Joins the splits: out = sum_i w_i o_i with w_i = e^(lse_i - lse).  A warp per
-// row of the split units, four features a lane.  A stream over the parts: those of
-// the case above, 72 units in two, 17 MB written and read, about 11 us.
-constexpr int kJoinThreads = 256;
+// Joins the splits: out = sum_i w_i o_i with w_i = e^(lse_i - lse).  Four features a
+// lane; a warp takes two rows of the split units, or, where there are many splits (few
+// query rows over many keys), eight warps take one and add up in their order.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinSplits = 8;  // above, eight warps to a row
+template <int W>  // warps of a row
 __global__ void __launch_bounds__(kJoinThreads)
-gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int per, long long rows) {
-  const long long i = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+gdn_cross_join_kernel(const __grid_constant__ CrossParams P, int per, unsigned rows) {
+  constexpr int R = W == 1 ? 2 : 1;                   // rows of a warp
+  __shared__ float4 sums[W > 1 ? W : 1][33];          // a warp's o of 4 x 32 features, and its weights' sum
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = W > 1 ? warp % W : 0, f = lane * 4;
+  bool on[R];
+  long long at[R], to[R], to_lse[R];
   pdl_wait();
-  if (i >= rows) return;
-  const long long su = i / per;                       // per: rows of a unit, in whole tiles or one of few
-  const int ur = (int)(i - su * per), r = ur % kRows;
-  const long long u = P.full + su, bh = u / P.groups;
-  const int tile = ((int)(u - bh * P.groups) * per + ur) / kRows;
-  const long long b = bh / P.Hk;
-  const int hk = (int)(bh - b * P.Hk), t = tile * P.tokens + r / P.G, head = hk * P.G + r % P.G;
-  if (r >= P.tokens * P.G || t >= P.Tq) return;       // no row
-  const long long at = su * P.nsplit * per + ur;      // of split 0, then every `per`
-  float top = -INFINITY;
-  for (int s = 0; s < P.nsplit; ++s) top = fmax_nan(top, P.part_lse[at + (long long)s * per]);
-  const bool any = top != -INFINITY;  // NaN is passed on
-  float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  const int f = lane * 4;
-#pragma unroll 4
-  for (int s = 0; s < P.nsplit; ++s) {
-    const long long x = at + (long long)s * per;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (f < P.D) v = *reinterpret_cast<const float4*>(P.part_o + x * P.D + f);
-    const float w = any ? expf(P.part_lse[x] - top) : 0.f;
-    const bool on = w > 0.f;  // a split that saw nothing left no part
-    sum += w;
-    o[0] += on ? w * v.x : 0.f;
-    o[1] += on ? w * v.y : 0.f;
-    o[2] += on ? w * v.z : 0.f;
-    o[3] += on ? w * v.w : 0.f;
+#pragma unroll
+  for (int e = 0; e < R; ++e) {
+    const unsigned i = (blockIdx.x * (kJoinWarps / W) + warp / W) * R + e;
+    const unsigned su = i / per, ur = i - su * per, r = ur % kRows;  // per: rows of a unit, in whole tiles or one of few
+    const unsigned u = P.full + su, bh = u / P.groups;
+    const int tile = ((u - bh * P.groups) * per + ur) / kRows;
+    const int b = bh / P.Hk, hk = bh - b * P.Hk, dt = r * P.gmul >> 16;
+    const int t = tile * P.tokens + dt, head = hk * P.G + r - dt * P.G, Hq = P.Hk * P.G;
+    on[e] = i < rows && r < P.tokens * P.G && t < P.Tq;  // a row
+    at[e] = (long long)su * P.nsplit * per + ur;         // of split 0, then every `per`
+    to[e] = (((long long)b * P.Tq + t) * Hq + head) * P.D + f;
+    to_lse[e] = ((long long)b * Hq + head) * P.Tq + t;
   }
-  const float inv = any ? 1.f / sum : 0.f;
-  const int Hq = P.Hk * P.G;
-  if (f < P.D)
-    *reinterpret_cast<uint2*>(P.out + ((b * P.Tq + t) * Hq + head) * P.D + f) =
-        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-  if (lane == 0 && P.lse) P.lse[(b * Hq + head) * P.Tq + t] = any ? top + logf(sum) : -INFINITY;
+  float top[R], sum[R], o[R][4];
+#pragma unroll
+  for (int e = 0; e < R; ++e) {
+    top[e] = -INFINITY;
+    for (int s = lane; on[e] && s < P.nsplit; s += 32) top[e] = fmax_nan(top[e], P.part_lse[at[e] + (long long)s * per]);
+    sum[e] = o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.f;
+  }
+#pragma unroll
+  for (int e = 0; e < R; ++e)
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top[e] = fmax_nan(top[e], __shfl_xor_sync(~0u, top[e], x));
+#pragma unroll 4
+  for (int s = first; s < P.nsplit; s += W) {
+#pragma unroll
+    for (int e = 0; e < R; ++e) {
+      const long long x = at[e] + (long long)s * per;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (on[e] && f < P.D) v = *reinterpret_cast<const float4*>(P.part_o + x * P.D + f);
+      const float w = top[e] != -INFINITY ? expf(P.part_lse[x] - top[e]) : 0.f;  // NaN is passed on
+      const bool some = w > 0.f;  // a split that saw nothing left no part
+      sum[e] += w;
+      o[e][0] += some ? w * v.x : 0.f;
+      o[e][1] += some ? w * v.y : 0.f;
+      o[e][2] += some ? w * v.z : 0.f;
+      o[e][3] += some ? w * v.w : 0.f;
+    }
+  }
+  if (W > 1) {
+    sums[first][lane] = make_float4(o[0][0], o[0][1], o[0][2], o[0][3]);
+    if (lane == 0) sums[first][32].x = sum[0];
+    __syncthreads();
+    if (first) return;
+#pragma unroll
+    for (int x = 1; x < W; ++x) {
+      const float4 v = sums[x][lane];
+      sum[0] += sums[x][32].x;
+      o[0][0] += v.x;
+      o[0][1] += v.y;
+      o[0][2] += v.z;
+      o[0][3] += v.w;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < R; ++e) {
+    if (!on[e]) continue;
+    const bool any = top[e] != -INFINITY;
+    const float inv = any ? 1.f / sum[e] : 0.f;
+    if (f < P.D)
+      *reinterpret_cast<uint2*>(P.out + to[e]) =
+          make_uint2(pack_bf16x2(o[e][0] * inv, o[e][1] * inv), pack_bf16x2(o[e][2] * inv, o[e][3] * inv));
+    if (lane == 0 && P.lse) P.lse[to_lse[e]] = any ? top[e] + logf(sum[e]) : -INFINITY;
+  }
 }
 
 // The shape of a call: units, splits along the keys.  Returns the rows of a unit:
@@ -661,9 +698,11 @@ cudaError_t launch_cross(const CrossCall& c, void* ws) {
   if (e != cudaSuccess) return e;
   if (parts > 0) {
     ProfileScope ps(c.stream, kKernCrossJoin);
-    const long long rows = parts / P.nsplit * per;
-    const unsigned blocks = (unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
-    e = launch_after(gdn_cross_join_kernel, blocks, kJoinThreads, 0, c.stream, P, per, rows);
+    const unsigned rows = (unsigned)(parts / P.nsplit * per);  // (their parts fit the device's memory)
+    const bool many = P.nsplit > kJoinSplits;
+    const unsigned each = many ? 1 : 2 * kJoinWarps;  // rows of a block
+    e = launch_after(many ? gdn_cross_join_kernel<kJoinWarps> : gdn_cross_join_kernel<1>, (rows + each - 1) / each,
+                     kJoinThreads, 0, c.stream, P, per, rows);
     if (e == cudaSuccess) count_launches(1);
   }
   return e;
