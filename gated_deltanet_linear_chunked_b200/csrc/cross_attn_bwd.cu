@@ -13,12 +13,13 @@
 //   gdn_cross_stat_kernel  -lse log2 e and -delta of every packed row; -inf and 0
 //                  for the rows that are none (past the tokens, or with no key),
 //                  for which 2^(s - inf) = 0.
-//   gdn_cross_bwd_kernel   dQ: a CTA per query tile walks the key tiles.
+//   gdn_cross_bwd_kernel   dQ: a CTA per query tile (and share of the key tiles, where
+//                  there are few query tiles) walks the key tiles.
 //                  dK, dV: a CTA per key tile and share of the query tiles; the
 //                  products are transposed, S^T = K Q^T and dP^T = V dO^T, so that
 //                  a TMEM lane is a key, P^T and dS^T are left operands out of
 //                  TMEM, and dK and dV add up there.
-//   gdn_cross_dkv_join_kernel  adds the shares up where there are several.
+//   gdn_cross_grad_join_kernel  adds the shares up where there are several.
 // No maximum is searched and no row's threads meet: lse is known.  16 warps take
 // a 128 x 128 tile, 32 columns a thread; one warp copies, one issues products.
 // 2 x 4095 queries of 16 heads over 2641 keys of 4, 128 wide, a fifth masked: 400 us,
@@ -57,6 +58,7 @@ struct BwdParams {
   int tokens, qtiles, ntiles;   // tokens and tiles of queries, tiles of keys
   int gmul;                     // r / G = r * gmul >> 16 for rows r < 128
   int nsplit, per_split;        // dkv: shares of the query tiles, tiles of each
+  int qsplit, per_qsplit;       // dq: shares of the (listed) key tiles, tiles of each
   unsigned dkv_blocks;          // ntiles * nsplit of every (b, key head)
   int qb, kb, vb;
   const uint32_t* bits;         // under a mask: seen keys, [B][ntiles][4], one bit each
@@ -66,6 +68,8 @@ struct BwdParams {
   const float* stat;            // [B * Hk][qtiles][2][128]: -lse log2 e, -delta
   float* part;                  // nsplit > 1: [nsplit][2 (dk, dv)][B * Hk][ntiles][128][D]
   long long part_rows;          // B * Hk * ntiles * 128
+  float* qpart;                 // qsplit > 1: [qsplit][B * Hk][qtiles][128][D]
+  long long qpart_rows;         // B * Hk * qtiles * 128
   long long limit;
   unsigned* err;
 };
@@ -226,14 +230,16 @@ struct DqLayout {
   static constexpr uint32_t total = aux + (uint32_t)sizeof(DqAux);
 };
 
-template <int NB>
+template <int NB, bool kShares>  // whether the key tiles are shared out
 __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUtensorMap& tm_q,
                                         const CUtensorMap& tm_do, const CUtensorMap& tm_k,
                                         const CUtensorMap& tm_v, const BwdParams& P) {
   using L = DqLayout<NB>;
   DqAux& aux = *reinterpret_cast<DqAux*>(smem + L::aux);
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
-  const int qt = block % P.qtiles, bh = block / P.qtiles;
+  // unit: ((b * Hk + hk) * qtiles + tile) * qsplit + split
+  const int split = kShares ? block % P.qsplit : 0, u = kShares ? block / P.qsplit : block;
+  const int qt = u % P.qtiles, bh = u / P.qtiles;
   const int b = bh / P.Hk, hk = bh - b * P.Hk;
   const int D = P.D;
   volatile int* abort_flag = &aux.abort;
@@ -270,8 +276,9 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
   constexpr uint32_t tm = 0;  // all 512 columns: the allocation starts at the first
   constexpr uint32_t tDP = tm + 256, tDQ = tm + 384;
   const int* list = P.bits ? P.list + (long long)b * (P.ntiles + 1) : nullptr;
+  const int j0 = split * P.per_qsplit, all_tiles = list ? list[P.ntiles] : P.ntiles;
   // (a reduction's result is uniform: the issuing warp's loop stays in uniform registers)
-  const int n = __reduce_max_sync(~0u, list ? list[P.ntiles] : P.ntiles);
+  const int n = __reduce_max_sync(~0u, kShares ? max(0, min(all_tiles - j0, P.per_qsplit)) : all_tiles);
   auto fail = [&]() {
     *abort_flag = 1;
     atomicOr(P.err, kErrTimeout);
@@ -288,7 +295,7 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
       int j = 0;
       for (; j < n; ++j) {
         if (*abort_flag) break;
-        const int ks = j % kKs, vs = j % kVs, t = list ? list[j] : j;
+        const int ks = j % kKs, vs = j % kVs, t = list ? list[j0 + j] : j0 + j;
         if ((j >= kKs && !mbar_wait(&aux.k_empty[ks], (j / kKs - 1) & 1, P.limit)) ||
             (j >= kVs && !mbar_wait(&aux.v_empty[vs], (j / kVs - 1) & 1, P.limit))) {
           fail();
@@ -370,7 +377,7 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
     const uint64_t nl = f2_pack(st[0], st[0]), nd = f2_pack(st[kRows], st[kRows]);
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      const uint4 keys = seen_keys(P, b, list ? list[j] : j);
+      const uint4 keys = seen_keys(P, b, list ? list[j0 + j] : j0 + j);
       if (!__all_sync(~0u, *abort_flag == 0 && mbar_wait(&aux.s_full[j & 1], (j >> 1) & 1, P.limit))) {
         ok = false;
         break;
@@ -431,15 +438,16 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
       // every product has completed: Q's (and dO's) buffer takes the rows, 2 KB a warp
       const int Hq = P.Hk * P.G, tok0 = qt * P.tokens, c0 = kCols * cg, r0 = (warp & 3) * 32;
       __nv_bfloat16* to = P.dq + (((long long)b * P.Tq + tok0) * Hq + hk * P.G) * D + c0;
+      float* part = kShares ? P.qpart + (split * P.qpart_rows + ((long long)bh * P.qtiles + qt) * kRows) * D + c0 : nullptr;
       if (c0 < D)
         put_columns(
             trow + tDQ + c0, min(kCols, D - c0), n > 0, P.scale, smem + L::q + warp * 2048, lane,
-            true,
+            !kShares,
             [&](int i) -> void* {
               const int q = r0 + i, dt = q * P.gmul >> 16, dh = q - dt * P.G;  // row = token * G + head
               return dt < P.tokens && tok0 + dt < P.Tq ? to + ((long long)dt * Hq + dh) * D : nullptr;
             },
-            [](int) -> float* { return nullptr; });
+            [&](int i) { return part + (long long)(r0 + i) * D; });
     }
   }
   tc_fence_before_sync();
@@ -733,7 +741,7 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
 
 // One grid for both: the dK, dV tiles first, which are longer, then the dQ tiles,
 // so that neither's last wave leaves SMs idle.
-template <int NB>
+template <int NB, bool kShares>
 __global__ void __launch_bounds__(kThreads, 1)
 gdn_cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -748,34 +756,47 @@ gdn_cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
   if (blockIdx.x < P.dkv_blocks)
     dkv_tile<NB>(smem, blockIdx.x, tm_q, tm_do, tm_k, tm_v, P);
   else
-    dq_tile<NB>(smem, blockIdx.x - P.dkv_blocks, tm_q, tm_do, tm_k, tm_v, P);
+    dq_tile<NB, kShares>(smem, blockIdx.x - P.dkv_blocks, tm_q, tm_do, tm_k, tm_v, P);
 }
 
-// dK, dV = the sum of the shares, in their order.  A thread per four features.
+// dK, dV and dQ = the sums of their shares, in their order.  A thread per four
+// features: kv of dK in the first kv_blocks, as many of dV, then q of dQ.  Every
+// number of rows or features is below 2^32, as their fp32 shares fit the memory.
 __global__ void __launch_bounds__(256)
-gdn_cross_dkv_join_kernel(const float* part, long long part_rows, int nsplit, int S, int Hk, int ntiles, int D,
-                          long long total, __nv_bfloat16* dk, __nv_bfloat16* dv) {
+gdn_cross_grad_join_kernel(const __grid_constant__ BwdParams P, unsigned kv, unsigned kv_blocks, unsigned q) {
   pdl_wait();
-  const long long j = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (j >= 2 * total) return;
-  const int which = j >= total;
-  const long long i = which ? j - total : j;
-  const int q = D / 4;
-  const long long row = i / q;  // ((b * S) + s) * Hk + hk
-  const int f = (int)(i - row * q) * 4, hk = (int)(row % Hk), s = (int)(row / Hk % S);
-  const long long b = row / Hk / S;
-  const long long prow = (b * Hk + hk) * ntiles * kRows + s;
+  const int which = blockIdx.x >= 2 * kv_blocks ? 2 : blockIdx.x >= kv_blocks;
+  const unsigned i = (blockIdx.x - which * kv_blocks) * 256 + threadIdx.x;
+  if (i >= (which < 2 ? kv : q)) return;
+  const unsigned d4 = P.D / 4, row = i / d4;
+  const int f = (int)(i - row * d4) * 4;
+  const float* from;
+  long long step;
+  int n;
+  if (which < 2) {  // row ((b * S) + s) * Hk + hk
+    const unsigned bs = row / P.Hk, hk = row - bs * P.Hk, b = bs / P.S, t = bs - b * P.S;
+    from = P.part + (which * P.part_rows + (long long)(b * P.Hk + hk) * P.ntiles * kRows + t) * P.D + f;
+    step = 2 * P.part_rows * P.D;
+    n = P.nsplit;
+  } else {  // row ((b * Tq) + t) * Hq + head
+    const unsigned Hq = P.Hk * P.G, bt = row / Hq, head = row - bt * Hq, b = bt / P.Tq, t = bt - b * P.Tq;
+    const unsigned hk = head / P.G, qt = t / P.tokens, r = (t - qt * P.tokens) * P.G + head - hk * P.G;
+    from = P.qpart + (((long long)(b * P.Hk + hk) * P.qtiles + qt) * kRows + r) * P.D + f;
+    step = P.qpart_rows * P.D;
+    n = P.qsplit;
+  }
   float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-  for (int x = 0; x < nsplit; ++x) {
-    const float4 v = *reinterpret_cast<const float4*>(part + ((2 * x + which) * part_rows + prow) * D + f);
+  for (int x = 0; x < n; ++x) {
+    const float4 v = *reinterpret_cast<const float4*>(from + x * step);
     o[0] += v.x;
     o[1] += v.y;
     o[2] += v.z;
     o[3] += v.w;
   }
-  __nv_bfloat16* to = which ? dv : dk;
-  *reinterpret_cast<uint2*>(to + row * D + f) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+  __nv_bfloat16* to = which == 2 ? P.dq : which ? P.dv : P.dk;
+  *reinterpret_cast<uint2*>(to + (long long)row * P.D + f) =
+      make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
 }
 
 void bwd_shape(const CrossCall& c, BwdParams* P) {
@@ -806,11 +827,31 @@ void bwd_shape(const CrossCall& c, BwdParams* P) {
   P->per_split = (P->qtiles + P->nsplit - 1) / P->nsplit;
   P->nsplit = (P->qtiles + P->per_split - 1) / P->per_split;
   P->dkv_blocks = (unsigned)(units * P->nsplit);
+  // Shares of the key tiles: few query tiles over many keys would leave the other SMs
+  // idle at the end (a token of 16 heads over 8192 keys 69.4 us whole, 14.2 shared out,
+  // 2 x 64 queries of 8 heads 120 and 94).  A dK, dV step takes 1.4 times a dQ step;
+  // the grid takes its work over all SMs or its longest CTA, whichever is longer.
+  const long long qunits = (long long)c.B * c.Hk * P->qtiles;
+  P->qpart_rows = qunits * kRows;
+  const double dkv = 1.4 * (P->per_split + 3);
+  best = 1e300;
+  P->qsplit = 1;
+  for (int s = 1; s <= 16 && (s == 1 || s <= P->ntiles / 4); ++s) {
+    const double dq = (P->ntiles + s - 1) / s + 3 + (s > 1 ? 2 : 0);
+    const double cost = std::max({(P->dkv_blocks * dkv + qunits * s * dq) / sms, dq, dkv}) +
+                        (s > 1 && P->nsplit == 1 ? 3 : 0);  // a join's launch
+    if (cost < best) {
+      best = cost;
+      P->qsplit = s;
+    }
+  }
+  P->per_qsplit = (P->ntiles + P->qsplit - 1) / P->qsplit;
+  P->qsplit = (P->ntiles + P->per_qsplit - 1) / P->per_qsplit;
 }
 
 // Scratch: the row stats, under a mask its bits and lists, then the shares' parts.
 struct BwdScratch {
-  size_t bits, list, part, total;
+  size_t bits, list, part, qpart, total;
 };
 BwdScratch bwd_scratch(const CrossCall& c, const BwdParams& P) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
@@ -818,7 +859,8 @@ BwdScratch bwd_scratch(const CrossCall& c, const BwdParams& P) {
   s.bits = up((size_t)c.B * c.Hk * P.qtiles * 2 * kRows * sizeof(float));
   s.list = s.bits + (c.mask ? up((size_t)c.B * P.ntiles * 4 * sizeof(uint32_t)) : 0);
   s.part = s.list + (c.mask ? up((size_t)c.B * (P.ntiles + 1) * sizeof(int)) : 0);
-  s.total = s.part + (P.nsplit > 1 ? (size_t)2 * P.nsplit * P.part_rows * c.D * sizeof(float) : 0);
+  s.qpart = s.part + (P.nsplit > 1 ? (size_t)2 * P.nsplit * P.part_rows * c.D * sizeof(float) : 0);
+  s.total = s.qpart + (P.qsplit > 1 ? (size_t)P.qsplit * P.qpart_rows * c.D * sizeof(float) : 0);
   return s;
 }
 
@@ -827,11 +869,12 @@ cudaError_t launch_nb(const CrossCall& c, const BwdParams& P, const CUtensorMap&
                       const CUtensorMap& mk, const CUtensorMap& mv) {
   // more than half an SM's shared memory: one CTA (all of TMEM) per SM
   constexpr int bytes = std::max({(int)DqLayout<NB>::total, (int)DkvLayout<NB>::total, 116 * 1024});
-  cudaError_t e = allow_smem(gdn_cross_bwd_kernel<NB>, bytes);
+  const auto kernel = P.qsplit > 1 ? gdn_cross_bwd_kernel<NB, true> : gdn_cross_bwd_kernel<NB, false>;
+  cudaError_t e = allow_smem(kernel, bytes);
   if (e != cudaSuccess) return e;
   ProfileScope ps(c.stream, kKernCrossBwd);
-  e = launch_after(gdn_cross_bwd_kernel<NB>, P.dkv_blocks + (unsigned)(c.B * c.Hk * P.qtiles), kThreads, bytes,
-                   c.stream, mq, mg, mk, mv, P);
+  e = launch_after(kernel, P.dkv_blocks + (unsigned)(c.B * c.Hk * P.qtiles * P.qsplit), kThreads, bytes, c.stream,
+                   mq, mg, mk, mv, P);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
@@ -858,6 +901,7 @@ cudaError_t launch_cross_backward(const CrossCall& c, void* ws) {
   P.scale_log2 = c.scale * 1.4426950408889634f;
   P.stat = static_cast<const float*>(ws);
   P.part = reinterpret_cast<float*>(base + at.part);
+  P.qpart = reinterpret_cast<float*>(base + at.qpart);
   P.limit = c.limit;
   P.err = c.err;
   P.qb = c.q.batch_stride != 0;
@@ -886,12 +930,13 @@ cudaError_t launch_cross_backward(const CrossCall& c, void* ws) {
   count_launches(1);
   e = c.D > 64 ? launch_nb<2>(c, P, mq, mg, mk, mv)
                : launch_nb<1>(c, P, mq, mg, mk, mv);
-  if (e != cudaSuccess || P.nsplit == 1) return e;
-  ProfileScope ps(c.stream, kKernCrossDkvJoin);
-  const long long total = (long long)c.B * c.S * c.Hk * (c.D / 4);
-  e = launch_after(gdn_cross_dkv_join_kernel, (unsigned)((2 * total + 255) / 256), 256, 0, c.stream,
-                   (const float*)P.part, P.part_rows, P.nsplit, c.S, c.Hk, P.ntiles, c.D, total,
-                   static_cast<__nv_bfloat16*>(c.dk), static_cast<__nv_bfloat16*>(c.dv));
+  if (e != cudaSuccess || (P.nsplit == 1 && P.qsplit == 1)) return e;
+  ProfileScope ps(c.stream, kKernCrossGradJoin);
+  const unsigned kv = P.nsplit > 1 ? (unsigned)((long long)c.B * c.S * c.Hk * (c.D / 4)) : 0;
+  const unsigned q = P.qsplit > 1 ? (unsigned)((long long)c.B * c.Tq * c.Hq * (c.D / 4)) : 0;
+  const unsigned kv_blocks = (unsigned)(((long long)kv + 255) / 256);
+  e = launch_after(gdn_cross_grad_join_kernel, 2 * kv_blocks + (unsigned)(((long long)q + 255) / 256), 256, 0,
+                   c.stream, P, kv, kv_blocks, q);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }

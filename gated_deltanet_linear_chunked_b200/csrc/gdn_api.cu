@@ -793,7 +793,7 @@ const char* gdn_kernel_name(int id) {
     case gdn::kKernCross: return "gdn_cross_kernel";
     case gdn::kKernCrossJoin: return "gdn_cross_join_kernel";
     case gdn::kKernCrossBwd: return "gdn_cross_bwd_kernel";
-    case gdn::kKernCrossDkvJoin: return "gdn_cross_dkv_join_kernel";
+    case gdn::kKernCrossGradJoin: return "gdn_cross_grad_join_kernel";
     case gdn::kKernCrossStat: return "gdn_cross_stat_kernel";
     case gdn::kKernCrossFew: return "gdn_cross_few_kernel";
   }

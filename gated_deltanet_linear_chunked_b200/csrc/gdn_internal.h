@@ -72,7 +72,7 @@ enum KernelId : int {
   kKernCross = 14,
   kKernCrossJoin = 15,
   kKernCrossBwd = 16,
-  kKernCrossDkvJoin = 17,
+  kKernCrossGradJoin = 17,
   kKernCrossStat = 18,
   kKernCrossFew = 19,
   kNumKernelIds = 20,

@@ -124,5 +124,5 @@ def test_kernel_names():
     lib = _lib.load()
     names = [ctypes.string_at(lib.gdn_kernel_name(i)).decode() for i in range(14, 20)]
     assert names == ["gdn_cross_kernel", "gdn_cross_join_kernel", "gdn_cross_bwd_kernel",
-                     "gdn_cross_dkv_join_kernel", "gdn_cross_stat_kernel", "gdn_cross_few_kernel"]
+                     "gdn_cross_grad_join_kernel", "gdn_cross_stat_kernel", "gdn_cross_few_kernel"]
     assert lib.gdn_kernel_name(20) == b"unknown"

@@ -177,6 +177,8 @@ def both(c, mask="own", **kw):
     (1, 2000, 130, 1, 2, 64, "none"),      # many query tiles to few key tiles: shares of them
     (1, 128, 1, 1, 1, 32, "none"),
     (2, 40, 3000, 1, 3, 48, "far"),
+    (2, 20, 2500, 2, 2, 64, "holes"),      # few query tiles to many key tiles: shares of those
+    (1, 1, 9000, 1, 16, 32, "tail"),
 ])
 def test_gradients(B, Tq, S, Hk, G, D, mask):
     c = Case(B, Tq, S, Hk, G, D, mask, 3 * Tq + S + D)
