@@ -20,6 +20,10 @@
 //                  a TMEM lane is a key, P^T and dS^T are left operands out of
 //                  TMEM, and dK and dV add up there.
 //   gdn_cross_grad_join_kernel  adds the shares up where there are several.
+// dS enters the products as bf16, and where there is one key tile as the sum of two
+// bf16: its rounding is as large as the result's own, and with few keys the rounding
+// of out in delta comes to it (18 keys: error of dq 1.5 times that of one rounding, 1.1
+// with two terms; the products it costs are not what bounds calls that small).
 // No maximum is searched and no row's threads meet: lse is known.  16 warps take
 // a 128 x 128 tile, 32 columns a thread; one warp copies, one issues products.
 // 2 x 4095 queries of 16 heads over 2641 keys of 4, 128 wide, a fifth masked: 400 us,
@@ -178,6 +182,11 @@ __device__ __forceinline__ uint64_t exp2_pair(uint64_t x, int i) {
   return f2_pack(ex2_approx(a), ex2_approx(e));
 }
 
+// What rounding a and b to the packed pair left, as a packed pair.
+__device__ __forceinline__ uint32_t rest_of(float a, float b, uint32_t pair) {
+  return pack_bf16x2(a - __uint_as_float(pair << 16), b - __uint_as_float(pair & 0xFFFF0000u));
+}
+
 // Columns [c0, c0 + n) (n 16 or 32) of a warp's 32 rows out of TMEM, times `mul`
 // (zeros if there is nothing), as bf16 to dst(row) or as fp32 to part(row).
 template <typename Dst, typename Part>
@@ -230,11 +239,15 @@ struct DqLayout {
   static constexpr uint32_t total = aux + (uint32_t)sizeof(DqAux);
 };
 
-template <int NB, bool kShares>  // whether the key tiles are shared out
+// How a call's key tiles are taken: all by a CTA of dQ, or shared out, or there is one
+// and dS has two terms.
+enum Mode { kWhole, kShared, kOne };
+template <int NB, Mode kMode>
 __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUtensorMap& tm_q,
                                         const CUtensorMap& tm_do, const CUtensorMap& tm_k,
                                         const CUtensorMap& tm_v, const BwdParams& P) {
   using L = DqLayout<NB>;
+  constexpr bool kShares = kMode == kShared;
   DqAux& aux = *reinterpret_cast<DqAux*>(smem + L::aux);
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
   // unit: ((b * Hk + hk) * qtiles + tile) * qsplit + split
@@ -362,6 +375,12 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
       for (int ks = 0; ks < kRows / 16; ++ks)
         mma_bf16_ts_elect(tDQ, tm + (j & 1) * 128 + (ks >> 1) * 32 + (ks & 1) * 8,
                           dkn + ((s * L::tile + ks * 2048) >> 4), idQ, j > 0 || ks > 0);
+      if (kMode == kOne) {
+#pragma unroll
+        for (int ks = 0; ks < kRows / 16; ++ks)
+          mma_bf16_ts_elect(tDQ, tm + (j & 1) * 128 + (ks >> 1) * 32 + (ks & 1) * 8 + kCols / 2,
+                            dkn + ((s * L::tile + ks * 2048) >> 4), idQ, true);
+      }
       mma_commit_elect(&aux.k_empty[s]);
     }
     if (!ok && lane == 0) fail();
@@ -413,6 +432,16 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
           pk[i] &= (seen >> (2 * i) & 1 ? 0xFFFFu : 0u) | (seen >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
       }
       tmem_st16u(ts, pk);
+      if (kMode == kOne) {  // what the rounding left, beside it
+#pragma unroll
+        for (int i = 0; i < kCols / 2; ++i) {
+          float a, e;
+          f2_unpack(f2_mul(p[i], f2_add(f2_pack(x[2 * i], x[2 * i + 1]), nd)), a, e);
+          pk[i] = rest_of(a, e, pk[i]);
+          pk[i] &= (seen >> (2 * i) & 1 ? 0xFFFFu : 0u) | (seen >> (2 * i + 1) & 1 ? 0xFFFF0000u : 0u);
+        }
+        tmem_st16u(ts + kCols / 2, pk);
+      }
       if (P.bits && (keys.x & keys.y & keys.z & keys.w) != ~0u) {
         // clear the masked rows of K (its product with Q is done): 0 * NaN would reach dQ
         const int key = tid >> 2, part = tid & 3;  // four threads a row
@@ -481,7 +510,7 @@ struct DkvLayout {
   static constexpr uint32_t total = aux + (uint32_t)sizeof(DkvAux);
 };
 
-template <int NB>
+template <int NB, Mode kMode>
 __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CUtensorMap& tm_q,
                                          const CUtensorMap& tm_do, const CUtensorMap& tm_k,
                                          const CUtensorMap& tm_v, const BwdParams& P) {
@@ -611,6 +640,7 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
         if (!ok) break;
         tc_fence_after_sync();
         add(tDK, tDP, colwise(q), i > 0);
+        if (kMode == kOne) add(tDK, tDP + kCols / 2, colwise(q), true);
         mma_commit_elect(&aux.empty[q % kRing]);
         if (i + 1 < n) {
           ok = landed(g + 2);
@@ -705,6 +735,20 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
         for (int c = 0; c < kCols / 2; ++c) pk[c] &= keep;
       }
       tmem_st16u(trow + tDP + kCols * cg, pk);
+      if (kMode == kOne) {
+#pragma unroll
+        for (int c = 0; c < kCols / 4; ++c) {
+          const uint4 y = nd[c];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint64_t neg = f2_pack(__uint_as_float(h ? y.z : y.x), __uint_as_float(h ? y.w : y.y));
+            float a, e;
+            f2_unpack(f2_mul(p[2 * c + h], f2_add(f2_pack(x[4 * c + 2 * h], x[4 * c + 2 * h + 1]), neg)), a, e);
+            pk[2 * c + h] = rest_of(a, e, pk[2 * c + h]) & keep;
+          }
+        }
+        tmem_st16u(trow + tDP + kCols * cg + kCols / 2, pk);
+      }
       if (warp == 1) *reinterpret_cast<float4*>(aux.nd[(i + 1) & 1] + lane * 4) = coming;
       tmem_wait_st();
       tc_fence_before_sync();
@@ -741,7 +785,7 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
 
 // One grid for both: the dK, dV tiles first, which are longer, then the dQ tiles,
 // so that neither's last wave leaves SMs idle.
-template <int NB, bool kShares>
+template <int NB, Mode kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 gdn_cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -754,9 +798,9 @@ gdn_cross_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     prefetch_map(&tm_v);
   }
   if (blockIdx.x < P.dkv_blocks)
-    dkv_tile<NB>(smem, blockIdx.x, tm_q, tm_do, tm_k, tm_v, P);
+    dkv_tile<NB, kMode>(smem, blockIdx.x, tm_q, tm_do, tm_k, tm_v, P);
   else
-    dq_tile<NB, kShares>(smem, blockIdx.x - P.dkv_blocks, tm_q, tm_do, tm_k, tm_v, P);
+    dq_tile<NB, kMode>(smem, blockIdx.x - P.dkv_blocks, tm_q, tm_do, tm_k, tm_v, P);
 }
 
 // dK, dV and dQ = the sums of their shares, in their order.  A thread per four
@@ -869,7 +913,9 @@ cudaError_t launch_nb(const CrossCall& c, const BwdParams& P, const CUtensorMap&
                       const CUtensorMap& mk, const CUtensorMap& mv) {
   // more than half an SM's shared memory: one CTA (all of TMEM) per SM
   constexpr int bytes = std::max({(int)DqLayout<NB>::total, (int)DkvLayout<NB>::total, 116 * 1024});
-  const auto kernel = P.qsplit > 1 ? gdn_cross_bwd_kernel<NB, true> : gdn_cross_bwd_kernel<NB, false>;
+  const auto kernel = P.qsplit > 1    ? gdn_cross_bwd_kernel<NB, kShared>
+                      : P.ntiles == 1 ? gdn_cross_bwd_kernel<NB, kOne>
+                                      : gdn_cross_bwd_kernel<NB, kWhole>;
   cudaError_t e = allow_smem(kernel, bytes);
   if (e != cudaSuccess) return e;
   ProfileScope ps(c.stream, kKernCrossBwd);
