@@ -117,12 +117,21 @@ __device__ __forceinline__ uint32_t word_of(const uint4& w, int c) {
 // Sixteen lanes per packed row, 8 features a lane; four rows of a group are loaded
 // before any is summed.  Under a mask, the last B blocks turn the rows of the mask
 // into bits and lists instead.
+// With at most kFewKeys keys (template argument) delta is formed from them instead,
+// sum_j P_j dO.v_j: dO.out holds the rounding of out, which weighs the more the fewer
+// keys there are (2 keys: error of dq 2.1 times that of one rounding, against 1.1).
+struct FewKeys {
+  const __nv_bfloat16 *q, *k, *v;
+  long long q_bs, q_ts, k_bs, k_ts, v_bs, v_ts;
+};
+constexpr int kFewKeys = 8;
 constexpr int kStatRows = 4;
 constexpr int kStatBlockRows = kStatThreads / 16 * kStatRows;
+template <bool kFew>
 __global__ void __launch_bounds__(kStatThreads)
 gdn_cross_stat_kernel(const __nv_bfloat16* out, const __nv_bfloat16* d_out, const float* lse, float* stat,
                       long long rows, unsigned row_blocks, const uint8_t* mask, long long mask_bs,
-                      const __grid_constant__ BwdParams P) {
+                      const __grid_constant__ BwdParams P, const __grid_constant__ FewKeys F) {
   pdl_wait();  // inputs may come from the kernel in front
   pdl_trigger();
   if (blockIdx.x >= row_blocks) {
@@ -133,12 +142,14 @@ gdn_cross_stat_kernel(const __nv_bfloat16* out, const __nv_bfloat16* d_out, cons
   }
   const int l = threadIdx.x & 15, Hq = P.Hk * P.G;
   const long long first = (long long)blockIdx.x * kStatBlockRows + threadIdx.x / 16;
-  uint4 x[kStatRows], y[kStatRows];
+  uint4 x[kStatRows], y[kStatRows];  // out (kFew: the query) and dO
   float lg[kStatRows];
+  int at_b[kStatRows], at_hk[kStatRows];
 #pragma unroll
   for (int i = 0; i < kStatRows; ++i) {
     x[i] = y[i] = make_uint4(0, 0, 0, 0);
     lg[i] = -INFINITY;
+    at_b[i] = at_hk[i] = -1;
     const long long row = first + i * (kStatThreads / 16);
     const int r = (int)(row % kRows), dt = r * P.gmul >> 16;
     const unsigned tile = (unsigned)(row / kRows), bh = tile / P.qtiles, qt = tile - bh * P.qtiles;
@@ -146,8 +157,10 @@ gdn_cross_stat_kernel(const __nv_bfloat16* out, const __nv_bfloat16* d_out, cons
     const int t = qt * P.tokens + dt, head = hk * P.G + r - dt * P.G;
     if (row >= rows || r >= P.tokens * P.G || t >= P.Tq) continue;
     const long long at = (((long long)b * P.Tq + t) * Hq + head) * P.D + l * 8;
+    at_b[i] = b;
+    at_hk[i] = hk;
     if (l * 8 < P.D) {
-      x[i] = *reinterpret_cast<const uint4*>(out + at);
+      x[i] = *reinterpret_cast<const uint4*>(kFew ? F.q + b * F.q_bs + t * F.q_ts + head * P.D + l * 8 : out + at);
       y[i] = *reinterpret_cast<const uint4*>(d_out + at);
     }
     lg[i] = lse[((long long)b * Hq + head) * P.Tq + t];
@@ -157,10 +170,35 @@ gdn_cross_stat_kernel(const __nv_bfloat16* out, const __nv_bfloat16* d_out, cons
     float u[8], v[8], d = 0.f;
     unpack8_bf16(x[i], u);
     unpack8_bf16(y[i], v);
+    if (kFew) {
+      for (int s = 0; s < P.S; ++s) {
+        const bool on = at_b[i] >= 0 && (!mask || mask[at_b[i] * mask_bs + s] != 0);
+        uint4 ku = make_uint4(0, 0, 0, 0), vu = ku;
+        if (on && l * 8 < P.D) {
+          ku = *reinterpret_cast<const uint4*>(F.k + at_b[i] * F.k_bs + s * F.k_ts + at_hk[i] * P.D + l * 8);
+          vu = *reinterpret_cast<const uint4*>(F.v + at_b[i] * F.v_bs + s * F.v_ts + at_hk[i] * P.D + l * 8);
+        }
+        float kf[8], vf[8], qk = 0.f, dp = 0.f;
+        unpack8_bf16(ku, kf);
+        unpack8_bf16(vu, vf);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) d = fmaf(u[e], v[e], d);
+        for (int e = 0; e < 8; ++e) {
+          qk = fmaf(u[e], kf[e], qk);
+          dp = fmaf(v[e], vf[e], dp);
+        }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(~0u, d, o);
+        for (int o = 8; o > 0; o >>= 1) {
+          qk += __shfl_xor_sync(~0u, qk, o);
+          dp += __shfl_xor_sync(~0u, dp, o);
+        }
+        if (on) d = fmaf(exp2f(fmaf(qk, P.scale_log2, lg[i] * -1.4426950408889634f)), dp, d);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d = fmaf(u[e], v[e], d);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(~0u, d, o);
+    }
     const long long row = first + i * (kStatThreads / 16);
     const bool on = lg[i] != -INFINITY;  // (a NaN row's gradients are NaN)
     if (l == 0 && row < rows) {
@@ -968,9 +1006,13 @@ cudaError_t launch_cross_backward(const CrossCall& c, void* ws) {
   {
     ProfileScope ps(c.stream, kKernCrossStat);
     const unsigned blocks = (unsigned)((rows + kStatBlockRows - 1) / kStatBlockRows);
-    e = launch_after(gdn_cross_stat_kernel, blocks + (c.mask ? c.B : 0), kStatThreads, 0, c.stream,
+    const FewKeys few = {static_cast<const __nv_bfloat16*>(c.q.data), static_cast<const __nv_bfloat16*>(c.k.data),
+                         static_cast<const __nv_bfloat16*>(c.v.data), c.q.batch_stride, c.q.token_stride,
+                         c.k.batch_stride, c.k.token_stride, c.v.batch_stride, c.v.token_stride};
+    e = launch_after(c.S <= kFewKeys ? gdn_cross_stat_kernel<true> : gdn_cross_stat_kernel<false>,
+                     blocks + (c.mask ? c.B : 0), kStatThreads, 0, c.stream,
                      static_cast<const __nv_bfloat16*>(c.out), static_cast<const __nv_bfloat16*>(c.d_out),
-                     (const float*)c.lse, static_cast<float*>(ws), rows, blocks, c.mask, c.mask_bs, P);
+                     (const float*)c.lse, static_cast<float*>(ws), rows, blocks, c.mask, c.mask_bs, P, few);
   }
   if (e != cudaSuccess) return e;
   count_launches(1);

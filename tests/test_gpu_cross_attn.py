@@ -192,6 +192,42 @@ def test_gradients(B, Tq, S, Hk, G, D, mask):
         assert (grads["dk"][~c.mask] == 0).all() and (grads["dv"][~c.mask] == 0).all()
 
 
+@pytest.mark.parametrize("Tq,S,G,D,mask", [(50, 2, 1, 64, "none"), (33, 5, 3, 80, "holes"), (1, 8, 4, 128, "none"),
+                                           (70, 60, 2, 32, "tail")])
+def test_gradients_of_few_keys(Tq, S, G, D, mask):
+    """With few keys neither dS's rounding nor that of out is in dq and dk, only their
+    own.  dS = P (dP - delta), delta = A = sum P dP: P is off by e_P = 7.5e-5 (the
+    polynomial) + d + the error of lse (8e-5 + d), so P dP and P delta by P |dP| e_P and
+    P sum(P |dP|) 2 e_P, dS's two terms by 2^-16, and out, from 9 keys on, by its
+    rounding in delta: sum |dO| (H |out| + (H + 8e-5 + 2 d) sum P |v|)."""
+    c = Case(2, Tq, S, 2, G, D, mask, 5 * S + Tq)
+    _, _, grads = both(c)
+    q, k, v, g = (c.np[n] for n in ("q", "k", "v", "g"))
+    ref = dict(zip(("dq", "dk", "dv"), ca.backward(q, k, v, g, c.npmask)))
+    out, lse = ca.forward(q, k, v, c.npmask)
+    size, _ = ca.forward(q, k, np.abs(v), c.npmask)
+    d, scale = c.score_error(), D ** -0.5
+    tol = {n: np.zeros_like(x) for n, x in ref.items()}
+    for b in range(2):
+        keep = np.arange(S) if c.npmask is None else np.flatnonzero(c.npmask[b])
+        for h in range(2 * G if len(keep) else 0):
+            kh, vh = k[b, keep, h // G], v[b, keep, h // G]
+            p = np.exp(scale * (q[b, :, h] @ kh.T) - lse[b, h][:, None])
+            dp = np.abs(g[b, :, h] @ vh.T)
+            e_p = 1.6e-4 + 2 * d[b, h][:, None]
+            a = np.sum(p * dp, -1, keepdims=True)
+            e = p * ((dp + 2 * a) * e_p + (dp + a) * 2.0 ** -16 + 4 * U * (D + 4) * (np.abs(g[b, :, h]) @ np.abs(vh).T))
+            if S > 8:
+                rounded = H * np.abs(out[b, :, h]) + (H + 8e-5 + 2 * d[b, h][:, None]) * size[b, :, h]
+                e += p * np.sum(np.abs(g[b, :, h]) * rounded, -1, keepdims=True)
+            tol["dq"][b, :, h] = scale * e @ np.abs(kh)
+            tol["dk"][b, keep, h // G] += scale * e.T @ np.abs(q[b, :, h])
+    for n in ("dq", "dk"):
+        err = np.abs(np64(grads[n]) - ref[n])
+        t = H * np.abs(ref[n]) + (1 + H) * tol[n]
+        assert (err <= t).all(), (n, float((err / (t + 1e-300)).max()))
+
+
 def test_gradients_along_a_direction():
     """<gradient, step> against central differences of the fp64 oracle's loss along a
     random step: the differences are exact to 1e-6, the gradients to 2 h of their
