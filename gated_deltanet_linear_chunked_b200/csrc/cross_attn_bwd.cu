@@ -20,10 +20,11 @@
 //                  a TMEM lane is a key, P^T and dS^T are left operands out of
 //                  TMEM, and dK and dV add up there.
 //   gdn_cross_grad_join_kernel  adds the shares up where there are several.
-// dS enters the products as bf16, and where there is one key tile as the sum of two
-// bf16: its rounding is as large as the result's own, and with few keys the rounding
-// of out in delta comes to it (18 keys: error of dq 1.5 times that of one rounding, 1.1
-// with two terms; the products it costs are not what bounds calls that small).
+// P and dS enter the products as bf16, and where there is one key tile as the sum of
+// two bf16: their rounding is as large as the result's own, and with few keys the
+// rounding of out in delta comes to it (22 keys: error of dq 1.5 times that of one
+// rounding, of dv 1.4; 1.1 and 1.0 with two terms; the products they cost are not what
+// bounds calls that small: 333 queries of 77 keys 19.1 -> 21 us).
 // No maximum is searched and no row's threads meet: lse is known.  16 warps take
 // a 128 x 128 tile, 32 columns a thread; one warp copies, one issues products.
 // 2 x 4095 queries of 16 heads over 2641 keys of 4, 128 wide, a fifth masked: 400 us,
@@ -666,6 +667,7 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
         if (!ok) break;
         tc_fence_after_sync();
         add(tDV, tm, colwise(g), i > 0);
+        if (kMode == kOne) add(tDV, tm + kCols / 2, colwise(g), true);
         mma_commit_elect(&aux.empty[g % kRing]);
         if (i + 1 < n) {
           ok = landed(q + 2);
@@ -744,6 +746,15 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
         for (int c = 0; c < kCols / 2; ++c) pk[c] &= keep;
       }
       tmem_st16u(trow + kCols * cg, pk);
+      if (kMode == kOne) {
+#pragma unroll
+        for (int c = 0; c < kCols / 2; ++c) {
+          float a, e;
+          f2_unpack(p[c], a, e);
+          pk[c] = rest_of(a, e, pk[c]) & keep;
+        }
+        tmem_st16u(trow + kCols * cg + kCols / 2, pk);
+      }
       if (warp == 0) *reinterpret_cast<float4*>(aux.nl[(i + 1) & 1] + lane * 4) = coming;
       tmem_wait_st();
       tc_fence_before_sync();
