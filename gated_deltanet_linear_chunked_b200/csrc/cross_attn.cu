@@ -46,7 +46,7 @@
 // rows of V are cleared in shared memory, since 0 * NaN would reach the sum.
 // Few query tiles and many keys: the key tiles are split over CTAs, each leaves
 // its normalised fp32 part and its lse, and gdn_cross_join_kernel joins them.
-// 2640 queries over 7920 keys, 20 heads of 112: 183 us, 1025 TFLOP/s, tensor core 53%
+// 2640 queries over 7920 keys, 20 heads of 112: 180 us, 1040 TFLOP/s, tensor core 53%
 // and special-function unit 46% busy; what is left is the hand-offs between them, and
 // when repeated the power limit.  Over 300 keys 19.7 us, the chain of a CTA's three
 // tiles, twice.

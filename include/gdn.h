@@ -433,7 +433,8 @@ GDN_API gdn_status gdn_cross_attention(const gdn_rows* q, const gdn_rows* k, con
  * and the gradient d_out of out (contiguous, as out): dq [B, Tq, Hq, D], dk, dv
  * [B, S, Hk, D], contiguous bf16, every element written; those of masked keys and
  * of rows that see none are 0.  Products of bf16 operands (P and dS rounded to
- * bf16) with fp32 sums, taken in a fixed order: the same call gives the same bits.
+ * bf16, with at most 128 keys each the sum of two bf16) with fp32 sums, taken in a
+ * fixed order: the same call gives the same bits.
  * For states that the batch shares (batch stride 0) dk and dv hold each batch
  * row's share.  dq, dk, dv overlap nothing.  Requirements, errors and scratch as
  * for gdn_cross_attention.
