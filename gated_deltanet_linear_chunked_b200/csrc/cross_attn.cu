@@ -441,7 +441,10 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       f2_unpack(sa, rs0, rs1);
       l_run = l_run * alpha + (rs0 + rs1);
     }
-    if (ok && n > 0 && !__all_sync(~0u, mbar_wait(&aux.o_full[g], 0, P.limit))) {
+    // the last product, or, with no key tile and so no product that has waited for
+    // them, the queries: their copy is started before the mask is known and lands
+    // where the rows are staged below
+    if (ok && !__all_sync(~0u, mbar_wait(n > 0 ? &aux.o_full[g] : &aux.q_full, 0, P.limit))) {
       fail();
       ok = false;
     }
@@ -455,7 +458,8 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       if (row && half == 0 && P.lse && whole) P.lse[((long long)b * Hq + head) * P.Tq + t] = lse;
       const long long part = ((long long)x * NQ + g) * kRows;  // x: split unit * nsplit + split
       if (half == 0 && !whole) P.part_lse[part + r] = lse;
-      // every S MMA has completed: the tile's Q buffer takes its rows, 4 KB a warp
+      // every S MMA has completed, or none was issued and Q has landed: the tile's Q
+      // buffer takes its rows, 4 KB a warp
       uint8_t* stage = smem + L::q + g * L::tile + (warp & 7) * (L::tile / 8);
       const int r0 = (warp & 3) * 32;
       for (int c0 = oc0; c0 < oc1; c0 += 32) {

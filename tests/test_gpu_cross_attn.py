@@ -339,6 +339,27 @@ def test_no_keys():
     assert gdn.cross_attention(q[:0], k[:0], k[:0]).shape == (0, 5, 4, 32)
 
 
+@pytest.mark.parametrize("Tq,S,G", [(300, 0, 1), (1500, 0, 3), (300, 300, 1), (1500, 77, 3), (300, 2500, 1), (70, 4000, 5)])
+def test_batch_rows_without_keys_in_tiles(Tq, S, G):
+    """More than 16 query rows a key head and nothing to attend to, in CTAs of one query
+    tile and of two and along split keys: zeros and -inf in every row, whenever the
+    queries arrive; a row of the batch that sees keys keeps its bits."""
+    c = Case(24, Tq, S, 2, G, 112, "none", 41)
+    if S:
+        c.mask = torch.zeros(24, S, dtype=torch.bool, device="cuda")
+        c.mask[5] = True
+        c.npmask = c.mask.cpu().numpy()
+    first = None
+    for _ in range(30):
+        out = torch.full_like(c.q, 7.0)
+        out, lse = gdn.cross_attention(c.q, c.k, c.v, c.mask, out=out, return_lse=True)
+        if first is None:
+            c.check(out, lse)
+            first = out, lse
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert gdn.device_error() == _lib.GDN_OK
+
+
 def test_views_and_broadcast():
     """Queries inside a wider projection, states shared by the batch, scale given."""
     wide = torch.randn(3, 70, 9, 48, device="cuda").bfloat16()
