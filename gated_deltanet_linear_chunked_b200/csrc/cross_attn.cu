@@ -193,7 +193,6 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     tmem_relinquish();
   }
   pdl_wait();
-  pdl_trigger();  // the next kernel's blocks may take their places; they wait for this grid
   if (P.mask) {
     const uint8_t* mrow = P.mask + b * P.mask_bs;
     for (int w = warp; w < kn * 4; w += Roles<NQ>::softmax_warps) {
@@ -206,6 +205,10 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  // The next kernel's blocks may take their places; they wait for this grid.  Not before
+  // this CTA has its tensor memory: a block of theirs on this SM could take the columns
+  // first, and would give them back only after this grid.
+  pdl_trigger();
   if (P.mask) {
     if (warp == 0) {
       int n = 0;

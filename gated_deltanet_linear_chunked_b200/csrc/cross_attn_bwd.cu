@@ -321,10 +321,10 @@ __device__ __forceinline__ void dq_tile(uint8_t* smem, unsigned block, const CUt
     tmem_relinquish();
   }
   pdl_wait();  // the row statistics and mask lists
-  pdl_trigger();
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  pdl_trigger();  // with tensor memory in hand: the next kernel's blocks may want it too
   constexpr uint32_t tm = 0;  // all 512 columns: the allocation starts at the first
   constexpr uint32_t tDP = tm + 256, tDQ = tm + 384;
   const int* list = P.bits ? P.list + (long long)b * (P.ntiles + 1) : nullptr;
@@ -589,11 +589,11 @@ __device__ __forceinline__ void dkv_tile(uint8_t* smem, unsigned block, const CU
       *reinterpret_cast<uint4*>(smem + L::ring + c * kBlock + i * 16) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   pdl_wait();  // the row statistics and mask bits
-  pdl_trigger();
   const uint4 keys = seen_keys(P, b, kt);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  pdl_trigger();  // as in dq_tile
   constexpr uint32_t tm = 0;
   constexpr uint32_t tDP = tm + 128, tDV = tm + 256, tDK = tm + 384;
   const bool any = (keys.x | keys.y | keys.z | keys.w) != 0;
