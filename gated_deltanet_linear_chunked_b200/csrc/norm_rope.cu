@@ -427,7 +427,11 @@ gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
       VT::open(ring[2], g);
       VT::open(ring[3], g + N);
       fetch(h + S.per);
-      if (pc.present) turn_from<V, G, interleaved>(row, g, pc);
+      // A place without a row (a token or head past the end) holds zeros, and adds zeros
+      // to dw: its part of the table was never written, and r of its sum of squares may
+      // be infinite.
+      const bool mine = on && h < S.H;
+      if (mine) turn_from<V, G, interleaved>(row, g, pc);
       uint64_t s2[2] = {0, 0}, d2[2] = {0, 0};
 #pragma unroll
       for (int j = 0; j < V; j += 2) {
@@ -440,7 +444,7 @@ gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
       f2_unpack(f2_add(s2[0], s2[1]), sa, sb);
       f2_unpack(f2_add(d2[0], d2[1]), da, db);
       const float ss = group_sum<G>(sa + sb), dot = group_sum<G>(da + db);
-      const float r = rsqrtf(ss * inv_d + P.eps);
+      const float r = mine ? rsqrtf(ss * inv_d + P.eps) : 0.f;
       const float m = -dot * r * inv_d;  // -mean(g w x^)
       const uint64_t r2 = f2_pack(r, r), m2 = f2_pack(m, m);
 #pragma unroll
@@ -452,7 +456,7 @@ gdn_norm_rope_bwd_kernel(const __grid_constant__ NormRopeParams P) {
           g[e] = f2_mul(r2, f2_fma(hat, m2, f2_mul(g[e], w[e])));
         }
       }
-      if (on && h < S.H) {
+      if (mine) {
         *reinterpret_cast<uint4*>(out + (long long)h * P.D + pc.a * V) = VT::close(g);
         *reinterpret_cast<uint4*>(out + (long long)h * P.D + pc.b * V) = VT::close(g + N);
       }

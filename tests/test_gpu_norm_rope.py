@@ -122,6 +122,42 @@ def test_forward_and_gradients(B, T, Hq, Hk, D, R, dtype, layout, sections, pack
     assert torch.equal(c.q, q0) and torch.equal(c.k, k0)        # inputs untouched
 
 
+def backward(c, **kw):
+    return gdn.qk_norm_rope_backward(c.q, c.k, c.wq, c.wk, c.gq, c.gk, c.pos, c.freq, **c.turn, **kw)
+
+
+@pytest.mark.parametrize("B,T,Hq,Hk,D,R,dtype,packed", [
+    (1, 33, 5, 2, 64, 32, "f32", False),
+    (1, 1, 1, 1, 16, 16, "bf16", False),
+    (2, 301, 16, 4, 128, 64, "bf16", False),   # heads that the groups do not share evenly
+    (1, 700, 20, 20, 112, 112, "bf16", True),  # a last tile with places for tokens that are none
+    (3, 130, 7, 3, 48, 48, "f32", True),
+])
+def test_weight_gradients_without_eps(B, T, Hq, Hk, D, R, dtype, packed):
+    """eps = 0: finite wherever no row is all zeros; places of a block that have no row
+    (past the last token or head) add nothing."""
+    c = Case(B, T, Hq, Hk, D, R, dtype, "half", (R // 2,), 3 * T + D, packed=packed)
+    g = backward(c, eps=0.0)
+    c.check_backward(g["dq"], g["dq_weight"], c.q, c.wq, c.gq, eps=0.0)
+    c.check_backward(g["dk"], g["dk_weight"], c.k, c.wk, c.gk, eps=0.0)
+
+
+@pytest.mark.parametrize("T,Hq,Hk,D", [(700, 20, 20, 112), (1000, 16, 4, 64), (300, 2, 2, 64), (5, 3, 1, 16)])
+def test_weight_gradients_do_not_hold_what_another_call_left(T, Hq, Hk, D):
+    """A rotation by NaN angles before it, which leaves them in the shared memory of
+    every SM, changes no bit: the places of the last tile that have no token read none."""
+    c = Case(1, T, Hq, Hk, D, D, "bf16", "half", (D // 2,), 5 * T + D)
+    want = backward(c)
+    c.check_backward(want["dq"], want["dq_weight"], c.q, c.wq, c.gq)
+    x = torch.ones(1, 1 << 18, 1, 16, dtype=torch.bfloat16, device="cuda")
+    at = torch.zeros(1 << 18, dtype=torch.int64, device="cuda")
+    freq = torch.full((8,), float("nan"), dtype=torch.float64, device="cuda")
+    for _ in range(5):
+        assert gdn.rope(x, None, at, freq)[0].isnan().all()
+        got = backward(c)
+        assert all(torch.equal(got[n], want[n]) for n in want)
+
+
 def test_rope_backward_is_the_transposed_turn():
     """<rope(x), y> = <x, rope_backward(y)>: both are sums of fp32-exact turns rounded once."""
     c = Case(2, 37, 3, 2, 64, 32, "f32", "half", (16,), 6)
