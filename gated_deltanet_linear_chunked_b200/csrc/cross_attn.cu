@@ -83,7 +83,6 @@ struct Roles {
 constexpr uint32_t kTileCols = 256;    // TMEM columns of a tile: S (and P) [0, 128) | O [128, 128 + D)
 constexpr uint32_t kBlock = kRows * 128;  // one 64-feature block of a 128-row tile, bytes
 constexpr float kRescaleLog2 = 8.f;
-constexpr float kLowest = -3e38f;      // the running maximum of no scores: from it, p of a masked key is 0
 constexpr long long kDrainPolls = 1LL << 40;  // drains are bounded by the 2 s timer
 
 template <int NQ>
@@ -456,8 +455,11 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (ok) {
       tc_fence_after_sync();
       l_run += aux.row[g][half ^ 1][r];
-      const float lse = n > 0 ? (m_run + log2f(l_run)) * 0.6931471805599453f : -INFINITY;
-      const float inv = n > 0 ? 1.f / l_run : 0.f;
+      // no key is seen, or every score is -inf (the sum is then what the polynomial gives
+      // for 0, 2^-125 each) and none is NaN
+      const bool any = n > 0 && !(m_run == kLowest && l_run < 1.f);
+      const float lse = any ? (m_run + log2f(l_run)) * 0.6931471805599453f : -INFINITY;
+      const float inv = any ? 1.f / l_run : 0.f;
       if (row && half == 0 && P.lse && whole) P.lse[((long long)b * Hq + head) * P.Tq + t] = lse;
       const long long part = ((long long)x * NQ + g) * kRows;  // x: split unit * nsplit + split
       if (half == 0 && !whole) P.part_lse[part + r] = lse;
@@ -476,7 +478,7 @@ gdn_cross_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           tmem_wait_ld();
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = n > 0 ? o[e] * inv : 0.f;
+        for (int e = 0; e < 32; ++e) o[e] = any ? o[e] * inv : 0.f;
         if (whole) {
           const uint4 v[4] = {pack8_bf16(o), pack8_bf16(o + 8), pack8_bf16(o + 16), pack8_bf16(o + 24)};
           store_rows<4>(stage, lane, v, cols / 8, [&](int i) -> void* {

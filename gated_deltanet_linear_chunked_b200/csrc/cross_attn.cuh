@@ -7,6 +7,7 @@
 
 namespace gdn {
 
+constexpr float kLowest = -3e38f;  // the running maximum of no scores: from it, p of a score of -inf is 0
 constexpr int kFewRows = 16;  // query rows of a (b, key head) that cross_few.cu takes
 
 struct CrossParams {

@@ -139,7 +139,7 @@ gdn_cross_few_kernel(const __grid_constant__ FewParams F) {
       }
   }
 
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float m[2] = {kLowest, kLowest}, l[2] = {0.f, 0.f};
   float o[2 * NK][4];
 #pragma unroll
   for (int i = 0; i < 2 * NK; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -186,8 +186,8 @@ gdn_cross_few_kernel(const __grid_constant__ FewParams F) {
         float mx = fmaxf(fmaxf(s0[2 * h], s0[2 * h + 1]), fmaxf(s1[2 * h], s1[2 * h + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-        const float mn = fmaxf(m[h], mx);  // finite (the group has a seen key) unless all scores were NaN:
-                                           // then p and the row's sum are
+        const float mn = fmaxf(m[h], mx);  // finite: p of a score of -inf is 0; NaN is ignored here, but not
+                                           // in p and the row's sum
         const float alpha = exp2f(m[h] - mn);
         m[h] = mn;
         const float p0 = exp2f(s0[2 * h] - mn), p1 = exp2f(s0[2 * h + 1] - mn);
@@ -259,7 +259,7 @@ gdn_cross_few_kernel(const __grid_constant__ FewParams F) {
       mine[p].z += a * y.z;
       mine[p].w += a * y.w;
     }
-    const bool any = sum != 0.f;
+    const bool any = sum != 0.f;  // else no key is seen, or every score is -inf
     const float inv = any ? 1.f / sum : 0.f;
     mine[p] = make_float4(mine[p].x * inv, mine[p].y * inv, mine[p].z * inv, mine[p].w * inv);
     mine_lse[p] = any ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;

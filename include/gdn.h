@@ -404,8 +404,9 @@ GDN_API gdn_status gdn_qk_norm_rope_backward(const gdn_rows* q, const gdn_rows* 
  *     out = sum e^(s - lse) v
  *
  * fp32 scores, softmax and sums, bf16 P and out.  A batch row that keeps no key
- * (or S = 0) has out = 0 and lse = -infinity.  Values in masked rows of k and v
- * (NaN and infinities among them) do not reach any result.
+ * (or S = 0) has out = 0 and lse = -infinity, and so has a query row all of whose
+ * scores are -infinity.  Scores are held up to |s| = 10^9.  Values in masked rows of
+ * k and v (NaN and infinities among them) do not reach any result.
  *
  *   q [B, Tq, Hq, D], k, v [B, S, Hk, D]   bf16 views as for gdn_qk_norm_rope,
  *                          strides at most 2^36, token strides not 0
@@ -435,6 +436,7 @@ GDN_API gdn_status gdn_cross_attention(const gdn_rows* q, const gdn_rows* k, con
  * of rows that see none are 0.  Products of bf16 operands (P and dS rounded to
  * bf16, with at most 128 keys each the sum of two bf16) with fp32 sums, taken in a
  * fixed order: the same call gives the same bits.
+ * P is formed anew from lse, whose rounding to fp32 is then in it: |lse| 2^-23.
  * For states that the batch shares (batch stride 0) dk and dv hold each batch
  * row's share.  dq, dk, dv overlap nothing.  Requirements, errors and scratch as
  * for gdn_cross_attention.

@@ -316,6 +316,41 @@ def test_nan_is_not_hidden(Tq, S, G):
     assert torch.equal(g["dk"][0, :, 0], grads["dk"][0, :, 0])
 
 
+@pytest.mark.parametrize("Tq,S,G", [(1, 40, 4), (1, 1000, 4), (1, 5000, 4), (300, 300, 1), (300, 4000, 1),
+                                    (40, 5000, 3), (2000, 2500, 1)])
+def test_scores_of_minus_infinity(Tq, S, G):
+    """Seen keys whose score is -inf have no weight, wherever they lie and however many
+    query rows there are; a row that has no other scores gives 0 and -inf, as one that
+    keeps no key."""
+    c = Case(2, Tq, S, 2, G, 64, "none", 51)
+    c.q = c.q.clone()
+    c.q[..., 0] = 1.0
+    c.np["q"] = np64(c.q)
+    gone = torch.arange(S, device="cuda") % 3 == 1
+    gone[:S // 2] = True
+    k = c.k.clone()
+    k[:, gone, :, 0] = -float("inf")
+    c.npmask = (~gone)[None].expand(2, -1).cpu().numpy()
+    c.check(*gdn.cross_attention(c.q, k, c.v, return_lse=True))
+    k[1, ..., 0] = -float("inf")
+    c.npmask = c.npmask.copy()
+    c.npmask[1] = False
+    c.check(*gdn.cross_attention(c.q, k, c.v, return_lse=True))
+
+
+@pytest.mark.parametrize("Tq,S", [(1, 40), (1, 5000), (300, 300), (300, 2500)])
+def test_scores_of_a_thousand_million(Tq, S):
+    """Scores of +-2^30, exact in fp32: the one key that matches is all of the result."""
+    c = Case(1, Tq, S, 1, 1, 16, "none", 52)
+    q, k = torch.zeros_like(c.q), torch.zeros(1, S, 1, 16, dtype=torch.bfloat16, device="cuda")
+    q[..., 0], k[..., 0] = 2.0 ** 15, -2.0 ** 15
+    k[:, S // 2 + 9, :, 0] = 2.0 ** 15
+    out, lse = gdn.cross_attention(q, k, c.v, scale=1.0, return_lse=True)
+    v = np64(c.v)[:, S // 2 + 9]
+    assert (np.abs(np64(out) - v[:, None]) <= 2 * H * np.abs(v[:, None])).all()
+    assert (np.abs(np64(lse) - 2.0 ** 30) <= 8 * U * 2.0 ** 30).all()
+
+
 @pytest.mark.parametrize("S", [131072, 140001])
 def test_long_mask(S):
     """As many masked keys as one CTA lists, and more (each CTA then takes a part)."""
