@@ -122,9 +122,11 @@ def bind():
             try:
                 _build.build_bind()
             except Exception as e:
-                if not os.path.exists(_build.BIND_PATH):
-                    raise RuntimeError(
-                        f"_gdn_torch.so is missing and could not be built (g++ is required): {e}") from e
+                # a stale one is not loaded: calls laid out for another torch or another
+                # gdn.h would go astray
+                what = "stale" if os.path.exists(_build.BIND_PATH) else "missing"
+                raise RuntimeError(
+                    f"_gdn_torch.so is {what} and could not be built (g++ is required): {e}") from e
         loader = importlib.machinery.ExtensionFileLoader("_gdn_torch", _build.BIND_PATH)
         spec = importlib.util.spec_from_file_location("_gdn_torch", _build.BIND_PATH, loader=loader)
         module = importlib.util.module_from_spec(spec)

@@ -15,6 +15,7 @@ not link libgdn.so (the loader hands it the entry points' addresses).
 from __future__ import annotations
 
 import glob
+import hashlib
 import os
 import subprocess
 import sys
@@ -66,15 +67,39 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB_PATH
 
 
+def _bind_tag() -> str:
+    """What the binding's compiled code depends on besides its own sources: torch's C++
+    layout and internal entries, and the interpreter's ABI."""
+    import sysconfig
+
+    import torch
+    return "torch %s, git %s, cxx11 abi %d, python %s" % (
+        torch.__version__, torch.version.git_version, int(torch.compiled_with_cxx11_abi()),
+        sysconfig.get_config_var("SOABI"))
+
+
+def _bind_stamp(path: str) -> str:
+    """The tag and the digest of the binding at `path`, as kept beside it."""
+    with open(path, "rb") as f:
+        return "%s\n%s\n" % (_bind_tag(), hashlib.sha256(f.read()).hexdigest())
+
+
 def bind_is_stale() -> bool:
+    """Missing, older than its sources, or built against another torch or Python."""
     if not os.path.exists(BIND_PATH):
         return True
     t = os.path.getmtime(BIND_PATH)
-    return any(os.path.getmtime(p) > t for p in (BIND_SRC, os.path.join(INCLUDE, "gdn.h")))
+    if any(os.path.getmtime(p) > t for p in (BIND_SRC, os.path.join(INCLUDE, "gdn.h"))):
+        return True
+    try:
+        with open(BIND_PATH + ".stamp") as f:
+            return f.read() != _bind_stamp(BIND_PATH)
+    except OSError:
+        return True
 
 
 def build_bind(force: bool = False, verbose: bool = False) -> str:
-    """Compile _gdn_torch.so if it is missing or older than its source."""
+    """Compile _gdn_torch.so if it is missing or stale."""
     if not force and not bind_is_stale():
         return BIND_PATH
     import sysconfig
@@ -93,7 +118,11 @@ def build_bind(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True, cwd=PKG)
-    os.replace(tmp, BIND_PATH)
+    stamp = _bind_stamp(tmp)
+    with open(tmp + ".stamp", "w") as f:
+        f.write(stamp)
+    os.replace(tmp, BIND_PATH)  # until the stamp follows, the binding counts as stale
+    os.replace(tmp + ".stamp", BIND_PATH + ".stamp")
     return BIND_PATH
 
 

@@ -81,3 +81,55 @@ def test_missing_library_raises_instead_of_falling_back(monkeypatch, tmp_path):
     monkeypatch.setattr(_build, "build", no_nvcc)
     with pytest.raises(RuntimeError, match="libgdn.so is missing"):
         _lib.load()
+
+
+# ------------------------------------- the compiled binding and what it was built against
+@pytest.fixture
+def built(monkeypatch, tmp_path):
+    """A binding that counts as fresh: any bytes, with the stamp that belongs to them."""
+    path = tmp_path / "_gdn_torch.so"
+    path.write_bytes(b"compiled")
+    (tmp_path / "_gdn_torch.so.stamp").write_text(_build._bind_stamp(str(path)))
+    monkeypatch.setattr(_build, "BIND_PATH", str(path))
+    assert not _build.bind_is_stale()
+    return path
+
+
+def test_binding_of_another_torch_or_python_is_stale(built, monkeypatch):
+    import sysconfig
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "0.0.1")
+        assert _build.bind_is_stale()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "compiled_with_cxx11_abi", lambda: not torch._C._GLIBCXX_USE_CXX11_ABI)
+        assert _build.bind_is_stale()
+    with monkeypatch.context() as m:
+        m.setattr(sysconfig, "get_config_var", lambda name: "cpython-30-other")
+        assert _build.bind_is_stale()
+    assert not _build.bind_is_stale()
+
+
+def test_binding_without_its_own_stamp_is_stale(built):
+    built.write_bytes(b"compiled elsewhere")
+    assert _build.bind_is_stale()
+    built.write_bytes(b"compiled")
+    assert not _build.bind_is_stale()
+    (built.parent / "_gdn_torch.so.stamp").unlink()
+    assert _build.bind_is_stale()
+
+
+def test_stale_binding_is_not_loaded(built, monkeypatch):
+    """A binding that is known to be stale and cannot be rebuilt raises; it is not used."""
+    (built.parent / "_gdn_torch.so.stamp").write_text("torch 0.0.1\n")
+    monkeypatch.setattr(_lib, "_bind", None)
+
+    def no_compiler(*a, **k):
+        raise OSError("g++ not found")
+    monkeypatch.setattr(_build, "build_bind", no_compiler)
+    with pytest.raises(RuntimeError, match="_gdn_torch.so is stale"):
+        _lib.bind()
+
+
+def test_built_binding_has_its_stamp():
+    _lib.bind()
+    assert not _build.bind_is_stale()
