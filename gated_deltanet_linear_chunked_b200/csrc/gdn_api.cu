@@ -6,29 +6,16 @@
 // caller's stream and returns without synchronising.  Nothing here throws,
 // aborts or prints.
 //
-// Per-stream context.  The chunked path needs scratch between its kernels,
-// and every bounded wait needs a word to report an expiry in.  Both are kept
-// per (device, stream): the first call on a stream allocates them
-// (cudaMalloc), later calls reuse them, and a larger problem replaces the
-// scratch with a larger one.  Calls on one stream are ordered, so they can
-// share the scratch; calls on different streams never share anything.  A
-// replaced scratch buffer is not freed (a captured CUDA graph may still name
-// it) until gdn_workspace_release.  A call made while its stream is being
-// captured, on a stream with no context yet or with too small a scratch,
-// cannot allocate outside the graph: it falls back to a stream-ordered
-// allocation (captured as graph memory nodes) and to the device-wide error
-// word.
+// Scratch and the error words of bounded waits are kept per (device, stream):
+// stream_context.cu.
 #include <cuda_runtime.h>
 
 #include <atomic>
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
-#include <functional>
 #include <mutex>
 #include <new>
-#include <thread>
-#include <vector>
 
 #include "gdn_internal.h"
 
@@ -88,94 +75,6 @@ gdn_status take_error(unsigned int* err) {
   return GDN_ERR_TIMEOUT;
 }
 
-// ------------------------------------------------------ per-stream contexts
-struct StreamCtx {
-  int dev;
-  cudaStream_t stream;
-  size_t thread;        // owning host thread for the per-thread default stream, else 0
-  unsigned int* err;    // error word of this stream's calls
-  void* ws;             // chunked-path scratch
-  size_t ws_bytes;
-};
-
-// Held over the launches of a call that passes scratch between them: two threads
-// that call on one stream share its scratch, so their launches must not interleave.
-std::mutex g_launch_mu;
-
-std::mutex g_ctx_mu;
-std::vector<StreamCtx*> g_ctx;
-struct Retired {
-  int dev;
-  void* p;
-};
-std::vector<Retired> g_retired;  // scratch buffers replaced by larger ones
-
-size_t thread_key(cudaStream_t s) {
-  if (s != cudaStreamPerThread) return 0;
-  return std::hash<std::thread::id>()(std::this_thread::get_id()) | 1u;
-}
-
-bool capturing(cudaStream_t s) {
-  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-  const cudaError_t e = cudaStreamIsCapturing(s, &cs);
-  if (e != cudaSuccess) {  // e.g. the legacy stream while another stream captures
-    cudaGetLastError();
-    return true;
-  }
-  return cs != cudaStreamCaptureStatusNone;
-}
-
-// The error word and scratch of (dev, s), the context created or its scratch
-// grown to at least `bytes` as needed.  Both are copied out under the lock.
-// Sets them to nullptr (and returns GDN_OK) when the stream is being captured
-// and its context cannot serve the call as it is.
-gdn_status stream_context(int dev, cudaStream_t s, size_t bytes, unsigned int** err,
-                          void** ws) {
-  *err = nullptr;
-  *ws = nullptr;
-  const size_t tk = thread_key(s);
-  std::lock_guard<std::mutex> lock(g_ctx_mu);
-  StreamCtx* c = nullptr;
-  for (StreamCtx* x : g_ctx)
-    if (x->dev == dev && x->stream == s && x->thread == tk) c = x;
-  if (!(c && c->ws_bytes >= bytes)) {
-    if (capturing(s)) return GDN_OK;
-    if (!c) {
-      void* p = nullptr;
-      if (cudaMalloc(&p, 256) != cudaSuccess) {
-        cudaGetLastError();
-        return GDN_ERR_CUDA;
-      }
-      if (cudaMemsetAsync(p, 0, 256, s) != cudaSuccess) {
-        cudaGetLastError();
-        cudaFree(p);
-        return GDN_ERR_CUDA;
-      }
-      c = new (std::nothrow) StreamCtx{dev, s, tk, static_cast<unsigned int*>(p), nullptr, 0};
-      if (!c) {
-        cudaFree(p);
-        return GDN_ERR_CUDA;
-      }
-      g_ctx.push_back(c);
-    }
-    if (bytes > c->ws_bytes) {
-      const size_t grain = size_t(2) << 20;
-      const size_t nb = (bytes + grain - 1) / grain * grain;
-      void* p = nullptr;
-      if (cudaMalloc(&p, nb) != cudaSuccess) {
-        cudaGetLastError();
-        return GDN_ERR_CUDA;
-      }
-      if (c->ws) g_retired.push_back({dev, c->ws});
-      c->ws = p;
-      c->ws_bytes = nb;
-    }
-  }
-  *err = c->err;
-  *ws = c->ws;
-  return GDN_OK;
-}
-
 gdn_status scan(const void* q, const void* k, const void* v, const void* g,
                 const void* beta, const float* state_in, float* state_out,
                 void* out, int B, int T, int H, int Dk, int Dv, gdn_dtype dtype,
@@ -191,13 +90,9 @@ gdn_status scan(const void* q, const void* k, const void* v, const void* g,
   const size_t bytes =
       dtype == GDN_BF16 ? chunk_tc_workspace_bytes(B, T, H, Dk, Dv, bidir) : 0;
   void* ws = nullptr;
-  std::unique_lock<std::mutex> launching(g_launch_mu);
-  st = stream_context(dev, a.stream, bytes, &a.err, &ws);
+  std::unique_lock<std::mutex> launching;
+  st = scan_scratch(dev, a.stream, bytes, &a.err, &ws, &launching);
   if (st != GDN_OK) return st;
-  if (!a.err && error_word(&a.err) != cudaSuccess) {
-    cudaGetLastError();
-    return GDN_ERR_CUDA;
-  }
   a.wait_limit = g_wait_limit.load();
 
   cudaError_t e;
@@ -335,30 +230,6 @@ gdn_status finish(cudaStream_t s, cudaError_t launch_err, unsigned int* err) {
 
 void count_launches(unsigned n) { g_launches.fetch_add(n); }
 
-gdn_status op_scratch(int dev, cudaStream_t s, size_t bytes, unsigned int** err, OpScratch* sc) {
-  sc->stream = s;
-  sc->launching = std::unique_lock<std::mutex>(g_launch_mu);
-  sc->captured = bytes > 0 && capturing(s);
-  gdn_status st = stream_context(dev, s, sc->captured ? 0 : bytes, err, &sc->p);
-  if (st != GDN_OK) return st;
-  if (!*err && error_word(err) != cudaSuccess) {
-    cudaGetLastError();
-    return GDN_ERR_CUDA;
-  }
-  if (!sc->captured) return GDN_OK;
-  if (cudaMallocAsync(&sc->p, bytes, s) != cudaSuccess) {
-    cudaGetLastError();
-    return GDN_ERR_CUDA;
-  }
-  return GDN_OK;
-}
-
-cudaError_t op_scratch_done(OpScratch* sc) {
-  const cudaError_t e = sc->captured ? cudaFreeAsync(sc->p, sc->stream) : cudaSuccess;
-  if (sc->launching.owns_lock()) sc->launching.unlock();
-  return e;
-}
-
 namespace {
 gdn_status backward(const void* q, const void* k, const void* v, const float* g,
                     const float* beta, const float* state_in, const void* d_out,
@@ -416,14 +287,10 @@ gdn_status backward(const void* q, const void* k, const void* v, const float* g,
   }
   unsigned int* err = nullptr;
   void* ws = nullptr;
-  std::unique_lock<std::mutex> launching(g_launch_mu);
+  std::unique_lock<std::mutex> launching;
   const size_t bytes = bwd_workspace_bytes(B, T, H, Dk, Dv, dtype, bidir);
-  st = stream_context(dev, s, bytes, &err, &ws);
+  st = scan_scratch(dev, s, bytes, &err, &ws, &launching);
   if (st != GDN_OK) return st;
-  if (!err && error_word(&err) != cudaSuccess) {
-    cudaGetLastError();
-    return GDN_ERR_CUDA;
-  }
   BwdCall c;
   c.q = q; c.k = k; c.v = v; c.g = g; c.beta = beta; c.state_in = state_in;
   c.d_out = d_out; c.d_state_out = d_state_out;
@@ -492,13 +359,8 @@ gdn_status sink_window(const void* q, const void* k, const void* v, void* k_cach
   c.q = q; c.k = k; c.v = v; c.k_cache = k_cache; c.v_cache = v_cache; c.out = out;
   c.B = B; c.Tc = Tc; c.H = H; c.D = D; c.n_sink = n_sink; c.window = window; c.chunk = chunk;
   c.stream = static_cast<cudaStream_t>(stream);
-  void* ws = nullptr;
-  gdn_status st = stream_context(dev, c.stream, 0, &c.err, &ws);
+  const gdn_status st = stream_error_word(dev, c.stream, &c.err);
   if (st != GDN_OK) return st;
-  if (!c.err && error_word(&c.err) != cudaSuccess) {
-    cudaGetLastError();
-    return GDN_ERR_CUDA;
-  }
   c.limit = g_wait_limit.load();
   return finish(c.stream, launch_sink_window(c), c.err);
 }
@@ -635,13 +497,7 @@ gdn_status gdn_device_error(void* stream) {
     cudaGetLastError();
     return GDN_ERR_CUDA;
   }
-  unsigned int* own = nullptr;
-  {
-    const size_t tk = gdn::thread_key(s);
-    std::lock_guard<std::mutex> lock(gdn::g_ctx_mu);
-    for (const gdn::StreamCtx* c : gdn::g_ctx)
-      if (c->dev == dev && c->stream == s && c->thread == tk) own = c->err;
-  }
+  unsigned int* own = gdn::own_error_word(dev, s);
   unsigned int* shared = nullptr;
   if (gdn::error_word(&shared) != cudaSuccess) {
     cudaGetLastError();
@@ -663,30 +519,7 @@ gdn_status gdn_workspace_release(void) {
     cudaGetLastError();
     return GDN_ERR_CUDA;
   }
-  std::lock_guard<std::mutex> lock(gdn::g_ctx_mu);
-  gdn_status st = GDN_OK;
-  std::vector<gdn::StreamCtx*> keep;
-  for (gdn::StreamCtx* c : gdn::g_ctx) {
-    if (c->dev != dev) {
-      keep.push_back(c);
-      continue;
-    }
-    if (c->ws && cudaFree(c->ws) != cudaSuccess) st = GDN_ERR_CUDA;
-    if (c->err && cudaFree(c->err) != cudaSuccess) st = GDN_ERR_CUDA;
-    delete c;
-  }
-  gdn::g_ctx.swap(keep);
-  std::vector<gdn::Retired> left;
-  for (const gdn::Retired& r : gdn::g_retired) {
-    if (r.dev != dev) {
-      left.push_back(r);
-      continue;
-    }
-    if (cudaFree(r.p) != cudaSuccess) st = GDN_ERR_CUDA;
-  }
-  gdn::g_retired.swap(left);
-  if (st != GDN_OK) cudaGetLastError();
-  return st;
+  return gdn::release_contexts(dev);
 }
 
 int gdn_set_time_segments(int segments) {

@@ -1,0 +1,216 @@
+// stream_context.cu -- what the library keeps per (device, stream): an error word
+// and the scratch that calls pass between their kernels.  Host code only.
+//
+// The first call on a stream allocates its error word and scratch, later calls
+// reuse them, and a larger problem replaces the scratch with a larger one.  Calls on
+// one stream are ordered, so they can share the scratch; calls on different streams
+// never share anything.
+//
+// Two scratches, by who may still name one that a larger call replaces:
+//   * the scan's and its gradients'.  A call that is being captured uses it where it
+//     is large enough, so a replaced one may live on in a graph and is kept until
+//     gdn_workspace_release.  One model has one shape of them.
+//   * the operators'.  Their captured calls take an allocation of the graph's own, so
+//     a replaced one is named by work already on the stream and by nothing else: it is
+//     freed in stream order.  Their sizes follow prompts and batches; kept, every
+//     length of a run would leave its buffer behind.
+//
+// A call made while its stream is being captured, on a stream with no context yet or
+// with too small a scratch, cannot allocate outside the graph: it gets none here and
+// allocates stream-ordered (captured as graph memory nodes), and reports to the
+// device-wide error word.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <functional>
+#include <mutex>
+#include <new>
+#include <thread>
+#include <vector>
+
+#include "gdn_internal.h"
+
+namespace gdn {
+namespace {
+
+struct Buffer {
+  void* p = nullptr;
+  size_t bytes = 0;
+};
+
+struct StreamCtx {
+  int dev;
+  cudaStream_t stream;
+  size_t thread;  // owning host thread for the per-thread default stream, else 0
+  unsigned int* err = nullptr;  // error word of this stream's calls
+  Buffer scan, op;
+};
+
+// Held over the launches of a call that passes scratch between them: two threads
+// that call on one stream share its scratch, so their launches must not interleave.
+std::mutex g_launch_mu;
+
+std::mutex g_ctx_mu;
+std::vector<StreamCtx*> g_ctx;
+struct Retired {
+  int dev;
+  void* p;
+};
+std::vector<Retired> g_retired;  // the scan's scratch buffers replaced by larger ones
+
+size_t thread_key(cudaStream_t s) {
+  if (s != cudaStreamPerThread) return 0;
+  return std::hash<std::thread::id>()(std::this_thread::get_id()) | 1u;
+}
+
+bool capturing(cudaStream_t s) {
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamIsCapturing(s, &cs);
+  if (e != cudaSuccess) {  // e.g. the legacy stream while another stream captures
+    cudaGetLastError();
+    return true;
+  }
+  return cs != cudaStreamCaptureStatusNone;
+}
+
+StreamCtx* find(int dev, cudaStream_t s) {
+  const size_t tk = thread_key(s);
+  for (StreamCtx* x : g_ctx)
+    if (x->dev == dev && x->stream == s && x->thread == tk) return x;
+  return nullptr;
+}
+
+gdn_status failed() {
+  cudaGetLastError();
+  return GDN_ERR_CUDA;
+}
+
+// A buffer of at least `bytes` in place of a smaller one.
+gdn_status grow_scan(StreamCtx* c, size_t bytes) {
+  const size_t grain = size_t(2) << 20;
+  const size_t n = (bytes + grain - 1) / grain * grain;
+  void* p = nullptr;
+  if (cudaMalloc(&p, n) != cudaSuccess) return failed();
+  if (c->scan.p) g_retired.push_back({c->dev, c->scan.p});
+  c->scan = {p, n};
+  return GDN_OK;
+}
+gdn_status grow_op(StreamCtx* c, size_t bytes) {
+  // a quarter more than asked for, so that lengths that creep up do not allocate
+  // every time
+  const size_t grain = size_t(2) << 20;
+  const size_t n = (bytes + bytes / 4 + grain - 1) / grain * grain;
+  if (c->op.p && cudaFreeAsync(c->op.p, c->stream) != cudaSuccess) return failed();
+  c->op = {};
+  void* p = nullptr;
+  if (cudaMallocAsync(&p, n, c->stream) != cudaSuccess) return failed();
+  c->op = {p, n};
+  return GDN_OK;
+}
+
+// The error word and one scratch of (dev, s), the context created or the scratch grown
+// to at least `bytes` as needed.  Both are copied out under the lock.  Sets them to
+// nullptr (and returns GDN_OK) when the stream is being captured and its context
+// cannot serve the call as it is.
+gdn_status stream_context(int dev, cudaStream_t s, size_t bytes, Buffer StreamCtx::*which,
+                          unsigned int** err, void** ws) {
+  *err = nullptr;
+  *ws = nullptr;
+  std::lock_guard<std::mutex> lock(g_ctx_mu);
+  StreamCtx* c = find(dev, s);
+  if (!(c && (c->*which).bytes >= bytes)) {
+    if (capturing(s)) return GDN_OK;
+    if (!c) {
+      void* p = nullptr;
+      if (cudaMalloc(&p, 256) != cudaSuccess) return failed();
+      if (cudaMemsetAsync(p, 0, 256, s) != cudaSuccess) {
+        cudaFree(p);
+        return failed();
+      }
+      c = new (std::nothrow) StreamCtx{dev, s, thread_key(s), static_cast<unsigned int*>(p)};
+      if (!c) {
+        cudaFree(p);
+        return GDN_ERR_CUDA;
+      }
+      g_ctx.push_back(c);
+    }
+    if (bytes > (c->*which).bytes) {
+      const gdn_status st = which == &StreamCtx::op ? grow_op(c, bytes) : grow_scan(c, bytes);
+      if (st != GDN_OK) return st;
+    }
+  }
+  *err = c->err;
+  *ws = (c->*which).p;
+  return GDN_OK;
+}
+
+// The device-wide error word where the stream has none.
+gdn_status some_error_word(unsigned int** err) {
+  return *err || current_error_word(err) == cudaSuccess ? GDN_OK : failed();
+}
+
+}  // namespace
+
+gdn_status scan_scratch(int dev, cudaStream_t s, size_t bytes, unsigned int** err, void** ws,
+                        std::unique_lock<std::mutex>* launching) {
+  *launching = std::unique_lock<std::mutex>(g_launch_mu);
+  const gdn_status st = stream_context(dev, s, bytes, &StreamCtx::scan, err, ws);
+  return st != GDN_OK ? st : some_error_word(err);
+}
+
+gdn_status stream_error_word(int dev, cudaStream_t s, unsigned int** err) {
+  void* ws = nullptr;
+  const gdn_status st = stream_context(dev, s, 0, &StreamCtx::scan, err, &ws);
+  return st != GDN_OK ? st : some_error_word(err);
+}
+
+gdn_status op_scratch(int dev, cudaStream_t s, size_t bytes, unsigned int** err, OpScratch* sc) {
+  sc->stream = s;
+  sc->launching = std::unique_lock<std::mutex>(g_launch_mu);
+  sc->captured = bytes > 0 && capturing(s);
+  gdn_status st = stream_context(dev, s, sc->captured ? 0 : bytes, &StreamCtx::op, err, &sc->p);
+  if (st == GDN_OK) st = some_error_word(err);
+  if (st != GDN_OK || !sc->captured) return st;
+  return cudaMallocAsync(&sc->p, bytes, s) == cudaSuccess ? GDN_OK : failed();
+}
+
+cudaError_t op_scratch_done(OpScratch* sc) {
+  const cudaError_t e = sc->captured ? cudaFreeAsync(sc->p, sc->stream) : cudaSuccess;
+  if (sc->launching.owns_lock()) sc->launching.unlock();
+  return e;
+}
+
+unsigned int* own_error_word(int dev, cudaStream_t s) {
+  std::lock_guard<std::mutex> lock(g_ctx_mu);
+  const StreamCtx* c = find(dev, s);
+  return c ? c->err : nullptr;
+}
+
+gdn_status release_contexts(int dev) {
+  std::lock_guard<std::mutex> lock(g_ctx_mu);
+  gdn_status st = GDN_OK;
+  std::vector<StreamCtx*> keep;
+  for (StreamCtx* c : g_ctx) {
+    if (c->dev != dev) {
+      keep.push_back(c);
+      continue;
+    }
+    for (void* p : {c->scan.p, c->op.p, static_cast<void*>(c->err)})
+      if (p && cudaFree(p) != cudaSuccess) st = GDN_ERR_CUDA;
+    delete c;
+  }
+  g_ctx.swap(keep);
+  std::vector<Retired> left;
+  for (const Retired& r : g_retired) {
+    if (r.dev != dev) {
+      left.push_back(r);
+      continue;
+    }
+    if (cudaFree(r.p) != cudaSuccess) st = GDN_ERR_CUDA;
+  }
+  g_retired.swap(left);
+  if (st != GDN_OK) cudaGetLastError();
+  return st;
+}
+
+}  // namespace gdn

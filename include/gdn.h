@@ -27,17 +27,20 @@
  *
  * Ownership.  The caller owns every buffer; all pointers are device (or
  * managed) pointers.  The library keeps no pointer to a caller's buffer after
- * a call returns.  It keeps, per (device, stream), one small context: the
- * scratch the bf16 path passes between its kernels and an error word.  The
- * first call on a stream allocates it (cudaMalloc), a larger problem grows
- * it, and gdn_workspace_release frees it.  Calls on one stream share their
- * context (they are ordered); calls on different streams share nothing.  A
- * call made while its stream is being captured into a CUDA graph cannot
- * allocate outside the graph: if the stream has no context yet, or too small
- * a scratch, the call allocates stream-ordered (cudaMallocAsync /
+ * a call returns.  It keeps, per (device, stream), one small context: an error
+ * word, the scratch the bf16 scan passes between its kernels, and that of the
+ * softmax blocks' operators.  The first call on a stream allocates it, a larger
+ * problem grows it, and gdn_workspace_release frees it.  A scan's scratch that
+ * was replaced by a larger one is kept until then, since a captured graph may
+ * name it; an operator's is freed behind the work on its stream.  Calls on one
+ * stream share their context (they are ordered); calls on different streams
+ * share nothing.  A call made while its stream is being captured into a CUDA
+ * graph cannot allocate outside the graph: if the stream has no context yet, or
+ * too small a scratch, the call allocates stream-ordered (cudaMallocAsync /
  * cudaFreeAsync, captured as graph memory nodes) and reports through the
  * device-wide error word.  Make one call on a stream before capturing on it
- * to keep memory nodes out of the graph.  Contexts are found by the stream's
+ * to keep the scan's memory nodes out of the graph (the operators' scratch in a
+ * captured call always is the graph's own).  Contexts are found by the stream's
  * handle, and cudaStreamDestroy returns before the stream's work is done: let
  * a stream's calls finish before destroying it, since a stream created
  * afterwards may get the same handle, and with it the same scratch.

@@ -222,3 +222,28 @@ def test_two_threads_on_one_stream():
         for *_, want, nwant, got, ngot in jobs:
             assert all(torch.equal(a, b) for a, b in zip(got, (want["dq"], want["dk"], want["dv"])))
             assert torch.equal(ngot[0], nwant["dq"]) and torch.equal(ngot[1], nwant["dq_weight"])
+
+
+def test_lengths_that_creep_up():
+    """Gradients for one prompt length after another: the stream's scratch is replaced by
+    larger ones and freed under work in flight, and every result is that of the same call
+    in a scratch that stays."""
+    s = torch.cuda.Stream()
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    n = lambda *z: torch.randn(z, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    q, g = n(1, 3000, 4, 128), n(1, 3000, 4, 128)
+    kv = n(1, 3000, 2, 2, 128)
+    lengths = range(200, 3000, 56)
+
+    def run(S):
+        k, v = kv[:, :S, 0], kv[:, :S, 1]
+        out, lse = gdn.cross_attention(q, k, v, return_lse=True)
+        return gdn.cross_attention_backward(q, k, v, out, lse, g)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        first = [run(S) for S in lengths]                       # growing
+        again = [run(S) for S in reversed(lengths)][::-1]       # in the largest
+    torch.cuda.synchronize()
+    assert gdn.device_error(s) == _lib.GDN_OK
+    for a, b in zip(first, again):
+        assert all(torch.equal(a[x], b[x]) for x in a)
