@@ -359,10 +359,14 @@ gdn_status sink_window(const void* q, const void* k, const void* v, void* k_cach
   c.q = q; c.k = k; c.v = v; c.k_cache = k_cache; c.v_cache = v_cache; c.out = out;
   c.B = B; c.Tc = Tc; c.H = H; c.D = D; c.n_sink = n_sink; c.window = window; c.chunk = chunk;
   c.stream = static_cast<cudaStream_t>(stream);
-  const gdn_status st = stream_error_word(dev, c.stream, &c.err);
+  std::unique_lock<std::mutex> launching;
+  void* ws = nullptr;
+  const gdn_status st = scan_scratch(dev, c.stream, 0, &c.err, &ws, &launching);  // the error word
   if (st != GDN_OK) return st;
   c.limit = g_wait_limit.load();
-  return finish(c.stream, launch_sink_window(c), c.err);
+  const cudaError_t e = launch_sink_window(c);
+  launching.unlock();
+  return finish(c.stream, e, c.err);
 }
 
 }  // namespace
@@ -515,11 +519,7 @@ gdn_status gdn_workspace_release(void) {
     cudaGetLastError();
     return GDN_ERR_CUDA;
   }
-  if (cudaDeviceSynchronize() != cudaSuccess) {
-    cudaGetLastError();
-    return GDN_ERR_CUDA;
-  }
-  return gdn::release_contexts(dev);
+  return gdn::release_contexts(dev, [] { return cudaDeviceSynchronize(); });
 }
 
 int gdn_set_time_segments(int segments) {

@@ -255,18 +255,19 @@ cudaError_t launch_sink_window(const SwaCall& c);
 // `err` gets the stream's error word, or the device-wide one.
 //
 // The scan's scratch of at least `bytes`, or nullptr under a capture that it cannot
-// serve.  No other call that uses scratch launches while `launching` is held.
+// serve.  No other call on the stream that uses scratch launches while `launching` is
+// held; calls on other streams go on.
 gdn_status scan_scratch(int dev, cudaStream_t s, size_t bytes, unsigned int** err, void** ws,
                         std::unique_lock<std::mutex>* launching);
-gdn_status stream_error_word(int dev, cudaStream_t s, unsigned int** err);
 unsigned int* own_error_word(int dev, cudaStream_t s);  // nullptr if the stream has none
-// Frees all that streams of the device hold; its work has to be done.
-gdn_status release_contexts(int dev);
+// Frees all that the streams of the device hold, once no call is in between its
+// launches and finish_work (which waits for the device) has returned.
+gdn_status release_contexts(int dev, cudaError_t (*finish_work)());
 
 // Scratch of one call of an operator: the stream's, or, for a call that is being
 // captured, an allocation of the graph's own (memory nodes), so that two captured
-// graphs never share it whatever streams they are replayed on.  No other call that
-// uses scratch launches until op_scratch_done (or the end of `sc`).
+// graphs never share it whatever streams they are replayed on.  No other call on the
+// stream that uses scratch launches until op_scratch_done (or the end of `sc`).
 struct OpScratch {
   void* p = nullptr;
   cudaStream_t stream = nullptr;

@@ -42,14 +42,16 @@ struct StreamCtx {
   int dev;
   cudaStream_t stream;
   size_t thread;  // owning host thread for the per-thread default stream, else 0
+  // Guards what follows, and is held over the launches of a call that passes scratch
+  // between them: two threads that call on one stream share its scratch, so their
+  // launches must not interleave.  Calls on other streams have their own.
+  std::mutex mu;
   unsigned int* err = nullptr;  // error word of this stream's calls
   Buffer scan, op;
 };
 
-// Held over the launches of a call that passes scratch between them: two threads
-// that call on one stream share its scratch, so their launches must not interleave.
-std::mutex g_launch_mu;
-
+// Entries stay for the life of the process (a thread may be waiting for one's lock);
+// gdn_workspace_release empties them.  Lock order: an entry's, then this one.
 std::mutex g_ctx_mu;
 std::vector<StreamCtx*> g_ctx;
 struct Retired {
@@ -73,11 +75,16 @@ bool capturing(cudaStream_t s) {
   return cs != cudaStreamCaptureStatusNone;
 }
 
-StreamCtx* find(int dev, cudaStream_t s) {
+// The entry of (dev, s), made if there is none (unless only looked for); nullptr if there
+// is none or the host has no memory.
+StreamCtx* entry(int dev, cudaStream_t s, bool make = true) {
   const size_t tk = thread_key(s);
+  std::lock_guard<std::mutex> lock(g_ctx_mu);
   for (StreamCtx* x : g_ctx)
     if (x->dev == dev && x->stream == s && x->thread == tk) return x;
-  return nullptr;
+  StreamCtx* c = make ? new (std::nothrow) StreamCtx{dev, s, tk} : nullptr;
+  if (c) g_ctx.push_back(c);
+  return c;
 }
 
 gdn_status failed() {
@@ -91,7 +98,10 @@ gdn_status grow_scan(StreamCtx* c, size_t bytes) {
   const size_t n = (bytes + grain - 1) / grain * grain;
   void* p = nullptr;
   if (cudaMalloc(&p, n) != cudaSuccess) return failed();
-  if (c->scan.p) g_retired.push_back({c->dev, c->scan.p});
+  if (c->scan.p) {
+    std::lock_guard<std::mutex> lock(g_ctx_mu);
+    g_retired.push_back({c->dev, c->scan.p});
+  }
   c->scan = {p, n};
   return GDN_OK;
 }
@@ -108,31 +118,22 @@ gdn_status grow_op(StreamCtx* c, size_t bytes) {
   return GDN_OK;
 }
 
-// The error word and one scratch of (dev, s), the context created or the scratch grown
-// to at least `bytes` as needed.  Both are copied out under the lock.  Sets them to
-// nullptr (and returns GDN_OK) when the stream is being captured and its context
-// cannot serve the call as it is.
-gdn_status stream_context(int dev, cudaStream_t s, size_t bytes, Buffer StreamCtx::*which,
-                          unsigned int** err, void** ws) {
+// The error word and one scratch of an entry whose lock is held, allocated or grown to
+// at least `bytes` as needed.  Sets them to nullptr (and returns GDN_OK) when the
+// stream is being captured and the entry cannot serve the call as it is.
+gdn_status provide(StreamCtx* c, size_t bytes, Buffer StreamCtx::*which, unsigned int** err, void** ws) {
   *err = nullptr;
   *ws = nullptr;
-  std::lock_guard<std::mutex> lock(g_ctx_mu);
-  StreamCtx* c = find(dev, s);
-  if (!(c && (c->*which).bytes >= bytes)) {
-    if (capturing(s)) return GDN_OK;
-    if (!c) {
+  if (!(c->err && (c->*which).bytes >= bytes)) {
+    if (capturing(c->stream)) return GDN_OK;
+    if (!c->err) {
       void* p = nullptr;
       if (cudaMalloc(&p, 256) != cudaSuccess) return failed();
-      if (cudaMemsetAsync(p, 0, 256, s) != cudaSuccess) {
+      if (cudaMemsetAsync(p, 0, 256, c->stream) != cudaSuccess) {
         cudaFree(p);
         return failed();
       }
-      c = new (std::nothrow) StreamCtx{dev, s, thread_key(s), static_cast<unsigned int*>(p)};
-      if (!c) {
-        cudaFree(p);
-        return GDN_ERR_CUDA;
-      }
-      g_ctx.push_back(c);
+      c->err = static_cast<unsigned int*>(p);
     }
     if (bytes > (c->*which).bytes) {
       const gdn_status st = which == &StreamCtx::op ? grow_op(c, bytes) : grow_scan(c, bytes);
@@ -153,22 +154,20 @@ gdn_status some_error_word(unsigned int** err) {
 
 gdn_status scan_scratch(int dev, cudaStream_t s, size_t bytes, unsigned int** err, void** ws,
                         std::unique_lock<std::mutex>* launching) {
-  *launching = std::unique_lock<std::mutex>(g_launch_mu);
-  const gdn_status st = stream_context(dev, s, bytes, &StreamCtx::scan, err, ws);
-  return st != GDN_OK ? st : some_error_word(err);
-}
-
-gdn_status stream_error_word(int dev, cudaStream_t s, unsigned int** err) {
-  void* ws = nullptr;
-  const gdn_status st = stream_context(dev, s, 0, &StreamCtx::scan, err, &ws);
+  StreamCtx* c = entry(dev, s);
+  if (!c) return GDN_ERR_CUDA;
+  *launching = std::unique_lock<std::mutex>(c->mu);
+  const gdn_status st = provide(c, bytes, &StreamCtx::scan, err, ws);
   return st != GDN_OK ? st : some_error_word(err);
 }
 
 gdn_status op_scratch(int dev, cudaStream_t s, size_t bytes, unsigned int** err, OpScratch* sc) {
+  StreamCtx* c = entry(dev, s);
+  if (!c) return GDN_ERR_CUDA;
   sc->stream = s;
-  sc->launching = std::unique_lock<std::mutex>(g_launch_mu);
+  sc->launching = std::unique_lock<std::mutex>(c->mu);
   sc->captured = bytes > 0 && capturing(s);
-  gdn_status st = stream_context(dev, s, sc->captured ? 0 : bytes, &StreamCtx::op, err, &sc->p);
+  gdn_status st = provide(c, sc->captured ? 0 : bytes, &StreamCtx::op, err, &sc->p);
   if (st == GDN_OK) st = some_error_word(err);
   if (st != GDN_OK || !sc->captured) return st;
   return cudaMallocAsync(&sc->p, bytes, s) == cudaSuccess ? GDN_OK : failed();
@@ -181,34 +180,47 @@ cudaError_t op_scratch_done(OpScratch* sc) {
 }
 
 unsigned int* own_error_word(int dev, cudaStream_t s) {
-  std::lock_guard<std::mutex> lock(g_ctx_mu);
-  const StreamCtx* c = find(dev, s);
-  return c ? c->err : nullptr;
+  StreamCtx* c = entry(dev, s, false);
+  if (!c) return nullptr;
+  std::lock_guard<std::mutex> lock(c->mu);
+  return c->err;
 }
 
-gdn_status release_contexts(int dev) {
-  std::lock_guard<std::mutex> lock(g_ctx_mu);
-  gdn_status st = GDN_OK;
-  std::vector<StreamCtx*> keep;
-  for (StreamCtx* c : g_ctx) {
-    if (c->dev != dev) {
-      keep.push_back(c);
-      continue;
-    }
+gdn_status release_contexts(int dev, cudaError_t (*finish_work)()) {
+  // every entry's lock, so that no call is between taking its scratch and its last
+  // launch; entries made meanwhile are not this release's
+  std::vector<StreamCtx*> mine;
+  {
+    std::lock_guard<std::mutex> lock(g_ctx_mu);
+    for (StreamCtx* c : g_ctx)
+      if (c->dev == dev) mine.push_back(c);
+  }
+  std::vector<std::unique_lock<std::mutex>> held;
+  for (StreamCtx* c : mine) held.emplace_back(c->mu);
+  std::vector<Retired> old;  // what is here now was named by launches that finish_work waits for
+  {
+    std::lock_guard<std::mutex> lock(g_ctx_mu);
+    old.swap(g_retired);
+  }
+  gdn_status st = finish_work() == cudaSuccess ? GDN_OK : failed();
+  std::vector<Retired> left;
+  for (const Retired& r : old) {
+    if (st != GDN_OK || r.dev != dev)
+      left.push_back(r);
+    else if (cudaFree(r.p) != cudaSuccess)
+      st = failed();
+  }
+  {
+    std::lock_guard<std::mutex> lock(g_ctx_mu);
+    g_retired.insert(g_retired.end(), left.begin(), left.end());
+  }
+  if (st != GDN_OK) return st;
+  for (StreamCtx* c : mine) {
     for (void* p : {c->scan.p, c->op.p, static_cast<void*>(c->err)})
       if (p && cudaFree(p) != cudaSuccess) st = GDN_ERR_CUDA;
-    delete c;
+    c->scan = c->op = {};
+    c->err = nullptr;
   }
-  g_ctx.swap(keep);
-  std::vector<Retired> left;
-  for (const Retired& r : g_retired) {
-    if (r.dev != dev) {
-      left.push_back(r);
-      continue;
-    }
-    if (cudaFree(r.p) != cudaSuccess) st = GDN_ERR_CUDA;
-  }
-  g_retired.swap(left);
   if (st != GDN_OK) cudaGetLastError();
   return st;
 }

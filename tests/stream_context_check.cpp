@@ -87,6 +87,8 @@ using namespace gdn;
 namespace {
 constexpr size_t MB = size_t(1) << 20;
 
+cudaError_t done() { return cudaSuccess; }
+
 void* op(int dev, cudaStream_t s, size_t bytes, gdn_status want = GDN_OK) {
   OpScratch sc;
   unsigned* err = nullptr;
@@ -146,11 +148,11 @@ void graphs() {
 void release() {
   CHECK(scan(0, stream(1), 8 * MB) && scan(0, stream(1), 20 * MB) && op(0, stream(1), 3 * MB) && op(0, stream(2), MB));
   void* other = op(1, stream(1), MB);
-  CHECK(release_contexts(0) == GDN_OK);
+  CHECK(release_contexts(0, done) == GDN_OK);
   CHECK(live.count(other) && live.size() == 2);  // and its error word
   CHECK(!own_error_word(0, stream(1)) && own_error_word(1, stream(1)));
   CHECK(op(0, stream(1), MB) && scan(0, stream(1), MB));
-  CHECK(release_contexts(0) == GDN_OK && release_contexts(1) == GDN_OK && live.empty());
+  CHECK(release_contexts(0, done) == GDN_OK && release_contexts(1, done) == GDN_OK && live.empty());
 }
 
 // An allocation that fails is reported, and the next call is served.
@@ -160,20 +162,54 @@ void failures() {
     op(0, stream(1), 4 * MB, GDN_ERR_CUDA);
     fail_after = -1;
     CHECK(op(0, stream(1), 4 * MB));
-    release_contexts(0);
+    release_contexts(0, done);
   }
   CHECK(op(0, stream(1), 4 * MB));
   fail_after = 0;
   op(0, stream(1), 400 * MB, GDN_ERR_CUDA);
   fail_after = -1;
-  CHECK(op(0, stream(1), 4 * MB) && release_contexts(0) == GDN_OK && live.empty());
+  CHECK(op(0, stream(1), 4 * MB) && release_contexts(0, done) == GDN_OK && live.empty());
+}
+
+// Whether a thread that does `call` has come through, given a little time.
+template <typename F>
+bool comes_through(F call, std::thread* t, std::atomic<bool>* through) {
+  *through = false;
+  *t = std::thread([=] {
+    call();
+    *through = true;
+  });
+  for (int i = 0; i < 200 && !*through; ++i) std::this_thread::sleep_for(std::chrono::milliseconds(10));
+  return *through;
+}
+
+// A call that holds its stream's scratch keeps others off that stream, and off no other
+// stream or device; a release waits for it.
+void threads() {
+  op(0, stream(1), MB);
+  OpScratch held;
+  unsigned* err = nullptr;
+  CHECK(op_scratch(0, stream(1), MB, &err, &held) == GDN_OK);
+  std::thread t[6];
+  std::atomic<bool> through[6];
+  CHECK(comes_through([] { op(0, stream(2), MB); }, &t[0], &through[0]));
+  CHECK(comes_through([] { scan(0, stream(3), MB); }, &t[1], &through[1]));
+  CHECK(comes_through([] { op(1, stream(1), MB); }, &t[2], &through[2]));
+  CHECK(!comes_through([] { op(0, stream(1), MB); }, &t[3], &through[3]));
+  CHECK(!comes_through([] { scan(0, stream(1), MB); }, &t[4], &through[4]));
+  CHECK(!comes_through([] { release_contexts(0, done); }, &t[5], &through[5]));
+  CHECK(live.count(held.p));
+  CHECK(op_scratch_done(&held) == cudaSuccess);
+  for (auto& x : t) x.join();
+  CHECK(release_contexts(0, done) == GDN_OK && release_contexts(1, done) == GDN_OK && live.empty());
 }
 
 }  // namespace
 
 int main(int argc, char** argv) {
   const std::map<std::string, void (*)()> checks = {
-      {"creeping", creeping}, {"graphs", graphs}, {"release", release}, {"failures", failures}};
+      {"creeping", creeping}, {"graphs", graphs}, {"release", release}, {"failures", failures},
+      {"threads", threads}};
   CHECK(argc == 2 && checks.count(argv[1]));
   checks.at(argv[1])();
   return 0;

@@ -247,3 +247,40 @@ def test_lengths_that_creep_up():
     assert gdn.device_error(s) == _lib.GDN_OK
     for a, b in zip(first, again):
         assert all(torch.equal(a[x], b[x]) for x in a)
+
+
+def test_threads_on_streams_of_their_own():
+    """Three host threads on three streams at once, while a fourth frees what the streams
+    hold between calls: every result is that of the call alone."""
+    import threading
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    n = lambda *z: torch.randn(z, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    jobs = []
+    for Tq, S in ((1500, 140), (2100, 260), (40, 3000)):
+        q, k, v, g = n(1, Tq, 4, 64), n(1, S, 2, 64), n(1, S, 2, 64), n(1, Tq, 4, 64)
+        out, lse = gdn.cross_attention(q, k, v, return_lse=True)
+        jobs.append((q, k, v, g, out, lse, gdn.cross_attention_backward(q, k, v, out, lse, g)))
+    torch.cuda.synchronize()
+    wrong, done = [], threading.Event()
+
+    def work(q, k, v, g, out, lse, want):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(100):
+                got = gdn.cross_attention_backward(q, k, v, out, lse, g)
+                o, _ = gdn.cross_attention(q, k, v, return_lse=True)
+                if not torch.equal(o, out) or not all(torch.equal(got[x], want[x]) for x in want):
+                    wrong.append(q.shape)
+
+    def release():
+        while not done.wait(0.005):
+            gdn.workspace_release()
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    other = threading.Thread(target=release)
+    for t in (*threads, other):
+        t.start()
+    for t in threads:
+        t.join()
+    done.set()
+    other.join()
+    torch.cuda.synchronize()
+    assert not wrong and gdn.device_error() == _lib.GDN_OK

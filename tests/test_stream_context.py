@@ -22,7 +22,7 @@ def program(tmp_path_factory):
     return path
 
 
-@pytest.mark.parametrize("check", ["creeping", "graphs", "release", "failures"])
+@pytest.mark.parametrize("check", ["creeping", "graphs", "release", "failures", "threads"])
 def test_stream_context(program, check):
     r = subprocess.run([program, check], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0, r.stderr
