@@ -13,16 +13,15 @@ namespace {
 
 constexpr long long kMaxStride = 1ll << 36;  // elements: TMA strides stay below 2^40 bytes
 
-// A [B, T, H, D] bf16 view the TMA maps can take: data aligned to 16 bytes,
-// strides in range and multiples of 16 bytes.
-bool good_view(const gdn_rows* v, int B, int T) {
+// Whether a view is one that the TMA maps can take: data aligned to 16 bytes, strides
+// in range and multiples of 16 bytes.  A stride that is never stepped by is not
+// looked at, and comes back as 0.
+bool good_view(const gdn_rows* v, int B, int T, gdn_rows* to) {
   if (!v || !v->data || !aligned16(v->data)) return false;
-  if (v->batch_stride < 0 || v->batch_stride > kMaxStride || v->token_stride < 0 ||
-      v->token_stride > kMaxStride)
+  *to = {v->data, B > 1 ? v->batch_stride : 0, T > 1 ? v->token_stride : 0};
+  if (to->batch_stride < 0 || to->batch_stride > kMaxStride || to->token_stride < 0 || to->token_stride > kMaxStride)
     return false;
-  if ((B > 1 && v->batch_stride % 8) || (T > 1 && (v->token_stride % 8 || v->token_stride == 0)))
-    return false;
-  return true;
+  return to->batch_stride % 8 == 0 && to->token_stride % 8 == 0 && (T <= 1 || to->token_stride != 0);
 }
 
 Range range_of_view(const gdn_rows& v, int B, int T, long long row) {
@@ -48,6 +47,7 @@ gdn_status check_inputs(const gdn_rows* q, const gdn_rows* k, const gdn_rows* v,
   if (B < 0 || Tq < 0 || S < 0 || Hq < 0 || Hk < 0 || D < 0) return GDN_ERR_INVALID_ARG;
   // 0 times the -infinity of a masked score is no number
   if (!(scale > 0.f) || !std::isnormal(scale) || !std::isnormal(scale * 1.5f)) return GDN_ERR_INVALID_ARG;
+  if (B <= 1) mask_bs = 0;  // not stepped by
   if (mask_bs < 0 || mask_bs > kMaxStride) return GDN_ERR_INVALID_ARG;
   if (dtype != GDN_BF16 || !supported_dim(D)) return GDN_ERR_UNSUPPORTED;
   if (Hq > 0 && (Hk == 0 || Hq % Hk)) return GDN_ERR_INVALID_ARG;
@@ -65,16 +65,13 @@ gdn_status check_inputs(const gdn_rows* q, const gdn_rows* k, const gdn_rows* v,
   o->nothing = B == 0 || Hq == 0;
   if (o->nothing) return GDN_OK;
   if (Tq > 0) {
-    if (!good_view(q, B, Tq)) return GDN_ERR_INVALID_ARG;
-    c.q = *q;
+    if (!good_view(q, B, Tq, &c.q)) return GDN_ERR_INVALID_ARG;
     if (B == 1) c.q.batch_stride = 1;  // not used; nonzero, so that it is no broadcast
     o->reads[o->nreads++] = range_of_view(c.q, B, Tq, (long long)Hq * D);
     o->ptrs[o->nptrs++] = q->data;
   }
   if (S > 0) {
-    if (!good_view(k, B, S) || !good_view(v, B, S)) return GDN_ERR_INVALID_ARG;
-    c.k = *k;
-    c.v = *v;
+    if (!good_view(k, B, S, &c.k) || !good_view(v, B, S, &c.v)) return GDN_ERR_INVALID_ARG;
     if (B == 1) c.k.batch_stride = c.v.batch_stride = 1;
     o->reads[o->nreads++] = range_of_view(c.k, B, S, (long long)Hk * D);
     o->reads[o->nreads++] = range_of_view(c.v, B, S, (long long)Hk * D);

@@ -574,7 +574,8 @@ cudaError_t launch_t(NormRopeParams& P, bool backward, cudaStream_t stream, unsi
   }
 }
 
-// A [B, T, H, D] view with its strides in bytes, for the overlap checks.
+// A [B, T, H, D] view with its strides in bytes (0 where the extent is at most 1), for
+// the overlap checks.
 struct View {
   const uint8_t* p;
   long long bs, ts, row;  // bytes; row = H * D elements
@@ -583,6 +584,9 @@ struct View {
     return {(uintptr_t)p, (uintptr_t)p + (B - 1) * bs + (T - 1) * ts + row};
   }
 };
+
+// A stride that is never stepped by is not looked at.
+long long used(long long stride, int extent) { return extent > 1 ? stride : 0; }
 
 // Whether no two rows of the view share memory: tokens inside batch rows, or
 // batch rows inside tokens (a sequence-first buffer).
@@ -607,7 +611,7 @@ bool views_clash(const View& a, const View& b) {
 }
 
 bool same_view(const View& a, const View& b) {
-  return a.p == b.p && (a.bs == b.bs || a.B == 1) && (a.ts == b.ts || a.T == 1);
+  return a.p == b.p && a.bs == b.bs && a.ts == b.ts;
 }
 
 struct Call {
@@ -633,6 +637,7 @@ gdn_status run(const Call& c) {
   if ((long long)c.B * c.T > 0x3FFFFFFFll || (long long)c.H[0] + c.H[1] > (1 << 20))
     return GDN_ERR_UNSUPPORTED;
   const gdn_rotation* r = c.rot;
+  long long pos_bs = 0;
   if (r) {
     if (r->rot_dim < 0 || r->rot_dim > c.D || r->axes < 1 || r->axes > 3) return GDN_ERR_INVALID_ARG;
     if (r->layout != GDN_ROPE_HALF && r->layout != GDN_ROPE_INTERLEAVED) return GDN_ERR_INVALID_ARG;
@@ -644,7 +649,8 @@ gdn_status run(const Call& c) {
     }
     if (pairs != r->rot_dim / 2) return GDN_ERR_INVALID_ARG;
     if (r->position_bytes != 4 && r->position_bytes != 8) return GDN_ERR_INVALID_ARG;
-    if (r->position_batch_stride < 0 || r->position_batch_stride > kMaxStride) return GDN_ERR_INVALID_ARG;
+    pos_bs = used(r->position_batch_stride, c.B);
+    if (pos_bs < 0 || pos_bs > kMaxStride) return GDN_ERR_INVALID_ARG;
   }
   const int R = r ? r->rot_dim : 0;
   const bool empty = c.B == 0 || c.T == 0 || c.H[0] + c.H[1] == 0;
@@ -658,12 +664,10 @@ gdn_status run(const Call& c) {
   int nptr = 0;
   auto view = [&](const gdn_rows* v, int s, View* to) {
     if (!v || !v->data || !aligned16(v->data)) return false;
-    if (v->batch_stride < 0 || v->batch_stride > kMaxStride || v->token_stride < 0 ||
-        v->token_stride > kMaxStride)
-      return false;
-    if ((v->batch_stride * es) % 16 || (v->token_stride * es) % 16) return false;
-    *to = {static_cast<const uint8_t*>(v->data), v->batch_stride * es, v->token_stride * es,
-           (long long)c.H[s] * c.D * es, c.B, c.T};
+    const long long bs = used(v->batch_stride, c.B), ts = used(v->token_stride, c.T);
+    if (bs < 0 || bs > kMaxStride || ts < 0 || ts > kMaxStride) return false;
+    if ((bs * es) % 16 || (ts * es) % 16) return false;
+    *to = {static_cast<const uint8_t*>(v->data), bs * es, ts * es, (long long)c.H[s] * c.D * es, c.B, c.T};
     ptrs[nptr++] = v->data;
     return true;
   };
@@ -685,7 +689,7 @@ gdn_status run(const Call& c) {
     if (!r->positions || !r->inv_freq || (uintptr_t)r->positions % r->position_bytes ||
         (uintptr_t)r->inv_freq % 8)
       return GDN_ERR_INVALID_ARG;
-    read(r->positions, (size_t)((c.B - 1) * r->position_batch_stride + (long long)c.T * r->axes) *
+    read(r->positions, (size_t)((c.B - 1) * pos_bs + (long long)c.T * r->axes) *
                            r->position_bytes);
     read(r->inv_freq, (size_t)R / 2 * 8);
   }
@@ -742,16 +746,16 @@ gdn_status run(const Call& c) {
     S.H = c.H[s];
     S.w = c.w[s];
     if (!S.H) continue;
-    S.x = c.in[s]->data;
-    S.x_bs = c.in[s]->batch_stride;
-    S.x_ts = c.in[s]->token_stride;
-    S.out = c.out[s]->data;
-    S.o_bs = c.out[s]->batch_stride;
-    S.o_ts = c.out[s]->token_stride;
+    S.x = in[s].p;
+    S.x_bs = in[s].bs / es;
+    S.x_ts = in[s].ts / es;
+    S.out = const_cast<uint8_t*>(out[s].p);
+    S.o_bs = out[s].bs / es;
+    S.o_ts = out[s].ts / es;
     if (c.backward) {
-      S.dy = c.dy[s]->data;
-      S.dy_bs = c.dy[s]->batch_stride;
-      S.dy_ts = c.dy[s]->token_stride;
+      S.dy = dy[s].p;
+      S.dy_bs = dy[s].bs / es;
+      S.dy_ts = dy[s].ts / es;
     }
   }
   P.T = c.T;
@@ -764,7 +768,7 @@ gdn_status run(const Call& c) {
   if (r) {
     P.pos = r->positions;
     P.freq = r->inv_freq;
-    P.pos_bs = r->position_batch_stride;
+    P.pos_bs = pos_bs;
     P.pos_wide = r->position_bytes == 8;
     P.axes = r->axes;
     P.sec1 = r->section[0];

@@ -83,6 +83,19 @@ def test_pointers_and_strides():
     assert call(k=None, v=None, S=0) in REACHES_DEVICE
 
 
+@pytest.mark.parametrize("stride", (3, 132, -128, -(1 << 62), 1 << 60))
+@pytest.mark.parametrize("f", [call, back])
+def test_unused_strides_are_not_looked_at(f, stride):
+    """Strides whose extent is 1 are not used: such a call goes as far as one with plain ones."""
+    one = dict(B=1)
+    for name, t, n in (("q", 8, 0), ("k", 16, 1), ("v", 16, 2)):
+        h = 4 if name == "q" else 2
+        assert f(B=1, **{name: rows(n, T=t, H=h, bs=stride)}) == f(**one), name
+    assert f(Tq=1, q=rows(0, bs=256, ts=stride)) == f(**one)
+    assert f(S=1, k=rows(1, bs=128, ts=stride), v=rows(2, bs=128, ts=stride)) == f(**one)
+    assert f(B=1, mbs=stride) == f(**one)
+
+
 def test_overlaps():
     for i in (0, 1, 2, 3):
         assert call(out=fake(i) + 16) == _lib.GDN_ERR_ALIAS, i

@@ -164,6 +164,35 @@ def test_overlaps():
     assert back(dwq=fake(8) + 4) == _lib.GDN_ERR_INVALID_ARG
 
 
+# Strides whose extent is 1 are not used: odd ones, negative ones, too large ones, and
+# different ones of views that lie side by side.
+UNUSED = (0, 3, 132, -128, -(1 << 62), 1 << 60)
+
+
+@pytest.mark.parametrize("stride", UNUSED)
+def test_unused_strides_are_not_looked_at(stride):
+    def reaches(status):
+        # the same call with strides that nothing can object to goes as far
+        assert status == call(B=1, T=8), status
+
+    for name in ("q", "k", "qo", "ko"):
+        i = {"q": 0, "k": 1, "qo": 4, "ko": 5}[name]
+        reaches(call(B=1, **{name: rows(i, bs=stride)}))
+        reaches(call(T=1, **{name: rows(i, bs=128, ts=stride)}))
+        reaches(call(B=1, T=1, **{name: rows(i, bs=stride, ts=stride)}))
+    for name in ("gq", "gk", "dq", "dk"):
+        i = {"gq": 4, "gk": 5, "dq": 6, "dk": 7}[name]
+        reaches(back(B=1, **{name: rows(i, bs=stride)}))
+        reaches(back(T=1, **{name: rows(i, bs=128, ts=stride)}))
+    reaches(call(B=1, r=rot(bs=stride)))
+    # side by side in one projection, in place, with different unused strides
+    p = dict(ts=384)
+    q, k = rows(0, bs=stride, **p), rows(0, off=256, bs=7, **p)
+    reaches(call(B=1, q=q, k=k, qo=rows(0, bs=8 * 384, **p), ko=rows(0, off=256, bs=0, **p)))
+    k = rows(0, off=128, bs=7, **p)
+    assert call(B=1, q=q, k=k, qo=q, ko=k) == _lib.GDN_ERR_ALIAS
+
+
 def test_kernel_names():
     lib = _lib.load()
     assert ctypes.string_at(lib.gdn_kernel_name(11)) == b"gdn_norm_rope_kernel"
