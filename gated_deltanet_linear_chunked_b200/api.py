@@ -308,7 +308,8 @@ def cross_attention(q, k, v, key_mask=None, *, scale=None, out=None, return_lse=
     """Softmax attention of q [B,Tq,Hq,D] over an encoder's k, v [B,S,Hk,D] (bf16;
     Hq a multiple of Hk, query head h reading key head h // (Hq // Hk)).
     ``key_mask`` [B,S] (bool or uint8) keeps the keys it is nonzero for; a batch row
-    that keeps none gives zeros.  ``scale`` defaults to 1/sqrt(D).  k and v may be
+    that keeps none gives zeros and an lse of -inf, as does a query row whose scores all
+    are -inf.  ``scale`` defaults to 1/sqrt(D).  k and v may be
     views of one projection, or expanded over the batch.  Returns ``out``
     [B,Tq,Hq,D], or ``(out, lse)`` with lse [B,Hq,Tq] fp32, which
     ``cross_attention_backward`` takes."""

@@ -46,10 +46,11 @@
 // rows of V are cleared in shared memory, since 0 * NaN would reach the sum.
 // Few query tiles and many keys: the key tiles are split over CTAs, each leaves
 // its normalised fp32 part and its lse, and gdn_cross_join_kernel joins them.
-// 2640 queries over 7920 keys, 20 heads of 112: 180 us, 1040 TFLOP/s, tensor core 53%
-// and special-function unit 46% busy; what is left is the hand-offs between them, and
-// when repeated the power limit.  Over 300 keys 19.7 us, the chain of a CTA's three
-// tiles, twice.
+// 2640 queries over 7920 keys, 20 heads of 112: 203-210 us on fresh inputs (891-920
+// TFLOP/s); replayed a few times from a cool start 180 (1040), tensor core 53% and
+// special-function unit 46% busy: what is left is the hand-offs between them, and the
+// power limit.  Over 300 keys 21.2 us, over 225 of them 17.6-19.4, the chain of a
+// CTA's three or two tiles, twice.
 // Every wait is bounded; one that gives up sets the error word and the CTA drains
 // its copies and MMAs before it frees TMEM.
 #include <cuda.h>
@@ -614,9 +615,13 @@ int cross_shape(const CrossCall& c, CrossParams* P) {
   P->ntiles = (c.S + kRows - 1) / kRows;
   // Up to 16 key tiles two CTAs of one query tile each share an SM, their starts
   // and ends under each other's work; beyond, one CTA of two tiles halves the keys
-  // and values that are loaded.  2640 queries, 20 heads of 112 (pair / single, us):
-  // 128 keys 15.1 / 12.3, 300 22.0 / 19.7, 1024 45.6 / 44.9, 2640 78.2 / 77.2,
-  // 7920 181 / 188.
+  // and values that are loaded.  Fresh inputs (pair / single, us): 2640 queries, 20 heads
+  // of 112, 128 keys 15.9 / 14.4, 300 23.7 / 21.2, 1024 44.3 / 43.4, 2048 65.2 / 64.9,
+  // 2640 78.9 / 79.2, 7920 181 / 190 (heads of 64: 180 / 172); 1024 queries, 16 heads of
+  // 128, 4096 keys 48.9 / 51.3.  The rule does not look at the queries: with one query
+  // tile (17 to 128 rows) over more than 16 key tiles a pair's second half is idle,
+  // 20 heads of 112 over 2640 keys 22.4 / 18.9, over 7920 31.9 / 30.8, 8 requests of
+  // them 123 / 126.
   const int nq = P->ntiles <= kSingleTiles ? 1 : 2;
   P->groups = (P->qtiles + nq - 1) / nq;
   const long long units = (long long)c.B * c.Hk * P->groups;

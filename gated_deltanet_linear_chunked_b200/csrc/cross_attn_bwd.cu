@@ -27,11 +27,11 @@
 // bounds calls that small: 333 queries of 77 keys 19.1 -> 21 us).
 // No maximum is searched and no row's threads meet: lse is known.  16 warps take
 // a 128 x 128 tile, 32 columns a thread; one warp copies, one issues products.
-// 2 x 4095 queries of 16 heads over 2641 keys of 4, 128 wide, a fifth masked: 400 us,
-// 1260 TFLOP/s of the seven products, tensor core 67% busy; TMEM is full, so a tile's
-// exponentials and its products take turns in part.  2640 queries over 300 keys, 20
-// heads of 112: 48 us, of which the row statistics and the join of the shares 13:
-// short tiles, one CTA an SM, their starts and ends bare.
+// 2 x 4095 queries of 16 heads over 2641 keys of 4, 128 wide, a fifth masked: 442 us on
+// fresh inputs, 1140 TFLOP/s of the seven products, tensor core 64% busy; TMEM is full, so
+// a tile's exponentials and its products take turns in part.  2640 queries over 225 of
+// 300 keys, 20 heads of 112: 48 us, of which the row statistics and the join of the shares
+// 13: short tiles, one CTA an SM, their starts and ends bare.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -12,9 +12,10 @@
 // arrive as zeros (so that 0 * NaN never arises), their scores become -inf, and
 // groups without any seen key are skipped.  The warps of a CTA join in shared
 // memory, up to eight CTAs of one (b, key head) in each other's as a cluster, more
-// through gdn_cross_join_kernel.  Bound by memory and, at such sizes, by its start
-// and end: 8 requests of one token, 16 query heads on 4 key heads of 128, over 4096
-// keys, a seventh of them masked, 13.8 us (4.2 TB/s).
+// through gdn_cross_join_kernel.  Bound by its start (the mask's bytes, then the first
+// keys) and end: 8 requests of one token, 16 query heads on 4 key heads of 128, over 4096
+// keys, a seventh of them masked, 18.5 us from memory (3.1 TB/s), DRAM at 33% while it
+// runs; repeated on the same tensors, out of L2, 14.0 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -331,8 +332,10 @@ cudaError_t launch_nk(const FewParams& F, unsigned grid, cudaStream_t stream) {
 
 }  // namespace
 
-// Two CTAs an SM, each warp at least two groups of keys; where that is up to ten
-// CTAs, eight, which are a cluster and join without a second kernel.
+// Two CTAs an SM, each warp at least two groups of keys; where that is nine or ten
+// CTAs, eight, which are a cluster and join without a second kernel (one token over
+// 4096 keys, heads of 112 and 128, eight / all, us: ten CTAs, 28 key heads, 15.5-16.8 /
+// 15.6-15.9; nine, 30 and 32 key heads, 16.1 / 17.1 and 15.4-16.6 / 16.5-17.7).
 int few_splits(int B, int Hk, int S) {
   const long long units = (long long)B * Hk;
   const long long most = ((S + kKeys - 1) / kKeys) / (2 * kWarps);

@@ -21,11 +21,13 @@
 // and keeps them for its heads, two of which are always on their way from memory.
 // Angles are formed in 64 bits and reduced to a fraction of a turn there: a
 // position of 10^6 has an angle whose 32-bit rounding is already 0.06.
-// Bound by memory: 65536 tokens, 16 + 4 heads of 128 in fp32 219 us (6.1 TB/s), 2640
-// tokens, 20 + 20 heads of 112 in bf16 10.0 us (4.7 TB/s, two waves of blocks).  The
-// gradients, which read twice as much and hold the weights' sums in registers, are
-// bound by latency at 16 warps an SM: the same 18.5 us (3.8 TB/s), 4 x 4096 tokens,
-// 16 + 4 heads of 128 in bf16 61 us (4.1 TB/s).
+// Inputs from memory: 65536 tokens, 16 + 4 heads of 128 in fp32 220 us (6.1 TB/s, bound
+// by memory), 2640 tokens, 20 + 20 heads of 112 in bf16 12.2 us (3.9 TB/s: 880 blocks for
+// 444 places, each forming its angles before it stores).  The gradients, which read
+// twice as much and hold the weights' sums in registers, are bound by latency at 16
+// warps an SM: the same 22.9 us (3.1 TB/s), 4 x 4096 tokens, 16 + 4 heads of 128 in bf16
+// 60 us (4.2 TB/s).  Repeated on the same tensors, so largely out of L2: 10.1, 18.8
+// and 60 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
