@@ -42,6 +42,14 @@ void connect(const py::dict& at) {
   get("gdn_cross_attention_backward", f_cross_bwd);
 }
 
+// Calls an entry point without the interpreter's lock: it may wait, for another thread's
+// launches on the stream or for room in its queue, and what it waits for may need Python.
+template <typename... P, typename... A>
+int enqueue(gdn_status (*entry)(P...), A... args) {
+  py::gil_scoped_release release;
+  return entry(args...);
+}
+
 using Shape = std::array<int64_t, 4>;
 
 // Refusals, as Python's ValueError and TypeError.  Messages are put together as
@@ -196,7 +204,7 @@ std::tuple<int, Tensor, OptTensor> rope(const Tensor& q, const OptTensor& k, con
     ok = or_new(k_out, q, h.k);
     wk = rows(*ok, "k_out", h.type, h.k);
   }
-  const int st = f_rope(&vq, k ? &vk : nullptr, r.get(), inverse, &wq, k ? &wk : nullptr, h.B, h.T, h.Hq, h.Hk, h.D,
+  const int st = enqueue(f_rope, &vq, k ? &vk : nullptr, r.get(), inverse, &wq, k ? &wk : nullptr, h.B, h.T, h.Hq, h.Hk, h.D,
                         h.dtype, stream_of(q));
   return {st, oq, ok};
 }
@@ -219,7 +227,7 @@ std::tuple<int, Tensor, OptTensor> qk_norm_rope(const Tensor& q, const OptTensor
     ok = or_new(k_out, q, h.k);
     wk = rows(*ok, "k_out", h.type, h.k);
   }
-  const int st = f_norm_rope(&vq, k ? &vk : nullptr, gq, gk, r.get(), &wq, k ? &wk : nullptr, h.B, h.T, h.Hq, h.Hk,
+  const int st = enqueue(f_norm_rope, &vq, k ? &vk : nullptr, gq, gk, r.get(), &wq, k ? &wk : nullptr, h.B, h.T, h.Hq, h.Hk,
                              h.D, (float)eps, h.dtype, stream_of(q));
   return {st, oq, ok};
 }
@@ -246,7 +254,7 @@ std::tuple<int, Tensor, OptTensor, Tensor, OptTensor> qk_norm_rope_backward(
     wk = rows(*ok, "dk", h.type, h.k);
     dwk = fresh(q, at::kFloat, {h.D});
   }
-  const int st = f_norm_rope_bwd(&vq, k ? &vk : nullptr, gq, gk, r.get(), &yq, k ? &yk : nullptr, &wq,
+  const int st = enqueue(f_norm_rope_bwd, &vq, k ? &vk : nullptr, gq, gk, r.get(), &yq, k ? &yk : nullptr, &wq,
                                  k ? &wk : nullptr, dwq.data_ptr<float>(), k ? dwk->data_ptr<float>() : nullptr, h.B,
                                  h.T, h.Hq, h.Hk, h.D, (float)eps, h.dtype, stream_of(q));
   return {st, oq, ok, dwq, dwk};
@@ -294,7 +302,7 @@ std::tuple<int, Tensor, OptTensor> cross_attention(const Tensor& q, const Tensor
   if (out) check_contiguous(o, "out", at::kBFloat16, c.q);
   OptTensor lse;
   if (want_lse) lse = fresh(q, at::kFloat, {c.q[0], c.q[2], c.q[1]});
-  const int st = f_cross(&c.vq, &c.vk, &c.vv, c.mask, c.mask_bs, o.data_ptr(), lse ? lse->data_ptr<float>() : nullptr,
+  const int st = enqueue(f_cross, &c.vq, &c.vk, &c.vv, c.mask, c.mask_bs, o.data_ptr(), lse ? lse->data_ptr<float>() : nullptr,
                          (int)c.q[0], (int)c.q[1], (int)c.k[1], (int)c.q[2], (int)c.k[2], (int)c.q[3], c.scale,
                          GDN_BF16, stream_of(q));
   return {st, o, lse};
@@ -309,7 +317,7 @@ std::tuple<int, Tensor, Tensor, Tensor> cross_attention_backward(const Tensor& q
   check_contiguous(lse, "lse", at::kFloat, {c.q[0], c.q[2], c.q[1]});
   check_contiguous(d_out, "d_out", at::kBFloat16, c.q);
   const Tensor dq = fresh(q, at::kBFloat16, c.q), dk = fresh(q, at::kBFloat16, c.k), dv = fresh(q, at::kBFloat16, c.k);
-  const int st = f_cross_bwd(&c.vq, &c.vk, &c.vv, c.mask, c.mask_bs, out.data_ptr(), lse.data_ptr<float>(),
+  const int st = enqueue(f_cross_bwd, &c.vq, &c.vk, &c.vv, c.mask, c.mask_bs, out.data_ptr(), lse.data_ptr<float>(),
                              d_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), (int)c.q[0], (int)c.q[1],
                              (int)c.k[1], (int)c.q[2], (int)c.k[2], (int)c.q[3], c.scale, GDN_BF16, stream_of(q));
   return {st, dq, dk, dv};

@@ -284,3 +284,46 @@ def test_threads_on_streams_of_their_own():
     other.join()
     torch.cuda.synchronize()
     assert not wrong and gdn.device_error() == _lib.GDN_OK
+
+
+SLOW_ENTRIES = r"""
+#include <unistd.h>
+#define SLOW(name) int name() { usleep(300000); return 0; }
+SLOW(gdn_rope) SLOW(gdn_qk_norm_rope) SLOW(gdn_qk_norm_rope_backward) SLOW(gdn_cross_attention)
+SLOW(gdn_cross_attention_backward)
+"""
+
+
+def test_other_threads_run_while_a_call_waits(tmp_path):
+    """The binding connected to entries that take 0.3 s, as one does that waits for its
+    stream: another thread's Python goes on meanwhile."""
+    import ctypes
+    import subprocess
+    import threading
+    import time
+    (tmp_path / "slow.c").write_text(SLOW_ENTRIES)
+    so = str(tmp_path / "slow.so")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", so, str(tmp_path / "slow.c")], check=True)
+    slow, lib, bind = ctypes.CDLL(so), _lib.load(), _lib.bind()
+    at = lambda x: {n: ctypes.cast(getattr(x, n), ctypes.c_void_p).value for n in _lib._BOUND}  # noqa: E731
+    q = torch.zeros(1, 4, 2, 32, dtype=torch.bfloat16, device="cuda")
+    pos, (freq, _) = torch.arange(4, device="cuda"), gdn.rope_frequencies(32)
+    lse = torch.zeros(1, 2, 4, device="cuda")
+    calls = [lambda: gdn.rope(q, q, pos, freq), lambda: gdn.qk_norm_rope(q, q),
+             lambda: gdn.qk_norm_rope_backward(q, q, None, None, q, q), lambda: gdn.cross_attention(q, q, q),
+             lambda: gdn.cross_attention_backward(q, q, q, q, lse, q)]
+    bind.connect(at(slow))
+    try:
+        for call in calls:
+            t = threading.Thread(target=call)
+            start = time.monotonic()
+            t.start()
+            turns = 0
+            while time.monotonic() - start < 0.15:
+                time.sleep(0.005)
+                turns += 1
+            assert t.is_alive() and turns >= 3
+            t.join()
+    finally:
+        bind.connect(at(lib))
+    torch.cuda.synchronize()
